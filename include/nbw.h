@@ -355,6 +355,162 @@ nbw_status nbw_file_header(int64_t n, int64_t k, void *header_out);
  * group size), NBW_ERANGE (the prefix ends before the planes start). */
 nbw_status nbw_file_parse(const void *header, int64_t file_bytes, nbw_file_info *info);
 
+/* ---------------------------------------------------------------------------
+ * The key-value cache of a decode step: what runs between a layer's qkv
+ * product and its o product.
+ *
+ * A cache is two pools of pages, K and V, [pages][heads][page][dim], and a
+ * table of page numbers, [rows][width]: slot j of sequence (row) r lies in
+ * page table[r][j / page] at place j % page, for every head.  A row holds at
+ * most width * page slots (its capacity).  One layer has one cache; the layers
+ * of a model may share a table.
+ *  - Keys are stored rotated, so a slot's number says nothing about its
+ *    token's position and attention does not depend on the order of the slots.
+ *  - Element types: bf16, or 8 bits (1 sign, 4 exponent and 3 mantissa bits, no
+ *    infinities, largest finite value 448) with one fp32 factor for each head:
+ *    key = stored value * k_scale[head], and likewise v_scale.
+ *  - A table entry outside [0, pages) is a page that is not there: its slots
+ *    are not written, and attention leaves them out.  Entries past a row's
+ *    length are not looked at.
+ *  - A row's length (device int32) below 0 counts as 0, above the capacity, or
+ *    above max_len where a call takes one, as that bound.
+ *  - Rows may share pages that are only read; nbw_kv_append and nbw_kv_evict
+ *    write pages, which must then belong to one row.
+ * Running totals of the attention weights (fp32) and token positions (int32)
+ * are kept apart from the pools, dense: [rows][heads][width * page].
+ *
+ * Alignment: pools and all bf16 tensors 16 bytes; everything else 4 bytes. */
+typedef enum nbw_kvdtype {
+    NBW_KV_BF16 = 0,
+    NBW_KV_FP8 = 1
+} nbw_kvdtype;
+
+typedef struct nbw_kvcache {
+    void *k, *v;           /* pools [pages][heads][page][dim] */
+    int64_t pages;         /* >= 1 */
+    int32_t heads;         /* key-value heads, 1..1024 */
+    int32_t page;          /* slots of a page: a power of two, 1..4096 */
+    int32_t dim;           /* 64, 128 or 256 */
+    int32_t dtype;         /* nbw_kvdtype */
+    const float *k_scale;  /* NBW_KV_FP8: [heads], positive; else NULL */
+    const float *v_scale;
+    const int32_t *table;  /* [rows][table_ld] */
+    int64_t rows;          /* sequences, >= 0 */
+    int64_t width;         /* pages of a row, >= 1; width * page <= 2^30 */
+    int64_t table_ld;      /* elements from one table row to the next: 0 (= width) or >= width */
+} nbw_kvcache;
+
+/* Arguments of nbw_kv_append. */
+typedef struct nbw_kv_append_args {
+    const void *k, *v;        /* new keys and values, bf16 [tokens][heads][dim] */
+    const void *q;            /* NULL, or queries bf16 [tokens][q_heads][dim] */
+    void *q_out;              /* with q: bf16 [tokens][q_heads][dim], may be q */
+    int64_t k_ld, v_ld, q_ld, q_out_ld; /* elements from one token to the next: 0 (dense), or
+                                 at least heads * dim (q_heads * dim) and a multiple of 8 */
+    int64_t tokens;           /* >= 0; below 2^31 */
+    int32_t q_heads;
+    float eps;                /* of the norms, >= 0 */
+    const int32_t *cu;        /* NULL: one token for each row (tokens = rows).  Else [rows + 1],
+                                 ascending from 0 to tokens: row r has tokens cu[r]..cu[r+1]-1 */
+    const int32_t *lens;      /* [rows] slots in use before the call */
+    const int32_t *positions; /* [tokens] */
+    const float *rope;        /* NULL: no rotation.  Else [rope_rows][dim]: the cosines of a
+                                 position's dim/2 angles, then the sines (16-byte aligned) */
+    int64_t rope_rows;
+    const void *q_norm, *k_norm; /* NULL, or bf16 [dim]: weights of the heads' norms */
+    int32_t *pos;             /* NULL, or [rows][heads][width * page] */
+    float *acc;               /* NULL, or the same shape */
+    int32_t *lens_out;        /* NULL, or [rows], not lens */
+} nbw_kv_append_args;
+
+/* New tokens go into the cache: token i of row r (i = 0 for its first) takes
+ * slot lens[r] + i.  A key's head x is, in fp32, divided by its root mean
+ * square where k_norm is given, x * k_norm / sqrt(mean(x^2) + eps); then
+ * rotated where rope is given, its halves (a, b) turning into
+ * (a cos - b sin, b cos + a sin) at the token's position; then rounded once to
+ * the cache's type (8 bits: of x / k_scale, limited to +-448, NaN kept).  A
+ * value is stored as it is (or rounded to 8 bits likewise).  Queries take the
+ * same two steps with q_norm and go to q_out.  pos of the new slots becomes
+ * the token's position and acc 0; lens_out = lens + the row's new tokens.
+ * Slots past the capacity, or on pages that are not there, are dropped.  A
+ * position outside [0, rope_rows) turns keys and queries into NaN.  In place
+ * (q_out = q) is fine; other overlaps of inputs and outputs are not.
+ * Errors: NBW_EINVAL, NBW_EALIGN, NBW_EUNSUPPORTED (dim, page or type), NBW_EHIP. */
+nbw_status nbw_kv_append(const nbw_kvcache *cache, const nbw_kv_append_args *args, void *stream);
+
+/* Arguments of nbw_kv_attend. */
+typedef struct nbw_kv_attend_args {
+    const void *q;          /* bf16 [rows][q_heads][dim], rotated: the rows' new tokens */
+    void *out;              /* bf16 [rows][q_heads][dim] */
+    int64_t q_ld, out_ld;   /* elements from one row to the next: 0 (dense), or at least
+                               q_heads * dim and a multiple of 8 */
+    int32_t q_heads;        /* a multiple of the cache's heads */
+    float scale;            /* of the scores; 0: 1 / sqrt(dim) */
+    const int32_t *lens;    /* [rows] slots in use, the new token's among them */
+    int64_t max_len;        /* 0 (the capacity), or a bound of the lengths, which sizes launch
+                               and workspace; longer rows are cut to it */
+    const float *acc;       /* NULL, or [rows][heads][width * page] totals */
+    float *acc_out;         /* with acc: the same shape, may be acc */
+    float decay;            /* of the totals, finite */
+    void *workspace;        /* caller-owned device scratch, 256-byte aligned, of at least
+                               nbw_kv_attend_workspace_bytes bytes; no initial contents
+                               needed; calls that overlap in time must not share one */
+    int64_t workspace_bytes;
+} nbw_kv_attend_args;
+
+/* Attention of one new token for each row over its cached ones.  Query heads
+ * g of key-value head h are h * G .. h * G + G - 1, G = q_heads / heads:
+ *     s_j = scale * q_g . k_j,  p = softmax over j < len,  out_g = sum_j p_j v_j
+ * and, with acc, for j < len (other entries are left as they are):
+ *     acc_out_j = decay * acc_j + sum over g of p_j.
+ * Products, softmax and sums are in fp32; out is rounded once.  A row of
+ * length 0 gives zeros, as does a head whose scores are all -infinity; a NaN
+ * among a row's scores or values gives NaN; what lies in slots past the length
+ * has no part.  Deterministic: the same inputs give the same bits.
+ * Errors: NBW_EINVAL, NBW_EALIGN, NBW_EUNSUPPORTED, NBW_ESCRATCH (workspace
+ * missing or too small), NBW_EHIP. */
+nbw_status nbw_kv_attend(const nbw_kvcache *cache, const nbw_kv_attend_args *args, void *stream);
+
+/* Bytes of workspace nbw_kv_attend needs (weights: whether acc is given), or
+ * -1 on bad arguments.  Host only; queries the device's compute-unit count. */
+int64_t nbw_kv_attend_workspace_bytes(const nbw_kvcache *cache, int32_t q_heads, int64_t max_len,
+                                      int32_t weights);
+
+/* Arguments of nbw_kv_evict. */
+typedef struct nbw_kv_evict_args {
+    const float *acc;       /* [rows][heads][width * page] totals */
+    const int32_t *pos;     /* [rows][heads][width * page] positions */
+    const int32_t *lens;    /* [rows] slots in use */
+    int64_t budget;         /* slots a row keeps, 1..width * page */
+    int64_t sink, recent;   /* >= 0, sink + recent <= budget */
+    float *acc_out;         /* acc's shape, not acc */
+    int32_t *pos_out;       /* pos's shape, not pos */
+    int32_t *lens_out;      /* [rows], not lens */
+    int64_t max_len;        /* 0 (the capacity), or a bound of the lengths */
+    void *workspace;        /* as for nbw_kv_attend; nbw_kv_evict_workspace_bytes bytes */
+    int64_t workspace_bytes;
+} nbw_kv_evict_args;
+
+/* Rows longer than `budget` keep, for each head, the budget slots of the
+ * largest key, the lowest slot first among equals, where a slot's key is
+ *     +infinity  if its position is below sink, or among the `recent` last
+ *                (above the head's largest position - recent);
+ *     -infinity  if its total is NaN;
+ *     its total  otherwise.
+ * The i-th slot at or past the budget that stays (ascending) takes the place
+ * of the i-th slot below it that goes: key, value, total and position.  Every
+ * other slot below the budget stays where it is, so no more rows move than
+ * have to.  acc_out and pos_out get the first min(len, budget) entries of the
+ * row (the others are left as they are), lens_out min(len, budget); pages
+ * past that length may be given to other rows when the call has completed.
+ * Exact: no arithmetic but comparisons.  Slots on pages that are not there
+ * take part in the ranking, and what would move to or from them is not moved.
+ * Errors: as nbw_kv_attend. */
+nbw_status nbw_kv_evict(const nbw_kvcache *cache, const nbw_kv_evict_args *args, void *stream);
+
+/* Bytes of workspace nbw_kv_evict needs, or -1 on bad arguments.  Host only. */
+int64_t nbw_kv_evict_workspace_bytes(const nbw_kvcache *cache, int64_t budget, int64_t max_len);
+
 /* Name of the kernel template instance nbw_qgemm_kernel would launch for
  * this problem on the current device (for example "nbw::gemv_kernel<4, 1, 2>",
  * as profilers print it without the parameter list), or "" on bad input.  The

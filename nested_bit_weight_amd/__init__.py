@@ -76,6 +76,8 @@ EXPORTS = ("nbw_plane_bytes", "nbw_packed_bytes", "nbw_pack_bitplanes", "nbw_mak
            "nbw_choose_codes", "nbw_unpack_codes", "nbw_stream_sink_words", "nbw_stream_read",
            "nbw_mfma_rate_sink_floats", "nbw_mfma_rate",
            "nbw_file_prefix_bytes", "nbw_file_header", "nbw_file_parse",
+           "nbw_kv_append", "nbw_kv_attend", "nbw_kv_attend_workspace_bytes", "nbw_kv_evict",
+           "nbw_kv_evict_workspace_bytes",
            "nbw_kernel_name", "nbw_status_str", "nbw_last_hip_error", "nbw_version")
 
 
@@ -136,6 +138,7 @@ def _lib():
         lib.nbw_file_header.restype = ctypes.c_int
         lib.nbw_file_parse.argtypes = [vp, i64, ctypes.POINTER(FileInfo)]
         lib.nbw_file_parse.restype = ctypes.c_int
+        kv.declare(lib)
         _LIB = lib
     return _LIB
 
@@ -579,7 +582,10 @@ def version() -> str:
     return _lib().nbw_version().decode()
 
 
-__all__ = ["pack_bitplanes", "slice_view", "save_parent", "load_child", "file_info",
+from . import kv  # noqa: E402  (uses the helpers above)
+from .kv import KVCache, kv_append, kv_attend, kv_evict  # noqa: E402
+
+__all__ = ["KVCache", "kv_append", "kv_attend", "kv_evict", "pack_bitplanes", "slice_view", "save_parent", "load_child", "file_info",
            "file_prefix_bytes", "qgemm", "QgemmCall", "qgemm_grouped", "workspace_bytes", "choose_codes", "unpack_codes", "stream_read", "stream_sink", "mfma_rate", "mfma_rate_sink", "mfma_rate_flops", "plane_bytes",
            "packed_bytes", "PackedWeight", "NBWError", "KERNELS", "library", "kernel_name",
            "version"]

@@ -7,6 +7,7 @@
 #include <mutex>
 #include <vector>
 
+#include "kv.h"
 #include "launch.h"
 #include "nbw.h"
 
@@ -107,6 +108,56 @@ nbw_status auto_kernel(int64_t batch, int64_t n, int64_t k, int32_t r, int *kern
     const int64_t passes = (batch + rows - 1) / rows;
     *kernel = passes == 1 || (passes == 2 && k <= 8192) ? NBW_KERNEL_SMALLB : NBW_KERNEL_GEMM;
     return NBW_OK;
+}
+
+// A row stride of `cols` bf16 elements: 0 stands for dense; rows stay 16-byte aligned.
+nbw_status check_ld(int64_t ld, int64_t cols, int64_t *out) {
+    *out = ld ? ld : cols;
+    if (*out < cols) return NBW_EINVAL;
+    return *out % 8 == 0 ? NBW_OK : NBW_EALIGN;
+}
+
+// A cache's own fields, and the form its kernels take.  Rows of 0 are fine.
+nbw_status check_cache(const nbw_kvcache *c, nbw::KvCache *out) {
+    if (!c || !c->k || !c->v || !c->table) return NBW_EINVAL;
+    if (c->dim != 64 && c->dim != 128 && c->dim != 256) return NBW_EUNSUPPORTED;
+    if (c->dtype != NBW_KV_BF16 && c->dtype != NBW_KV_FP8) return NBW_EUNSUPPORTED;
+    if (c->page < 1 || c->page > 4096 || (c->page & (c->page - 1))) return NBW_EUNSUPPORTED;
+    if (c->heads < 1 || c->heads > 1024 || c->pages < 1 || c->pages > INT_MAX) return NBW_EINVAL;
+    if (c->rows < 0 || c->rows > (1 << 20)) return NBW_EINVAL;
+    if (c->width < 1 || c->width > (1 << 30) || c->width * c->page > (1 << 30)) return NBW_EINVAL;
+    if (c->table_ld && c->table_ld < c->width) return NBW_EINVAL;
+    const bool fp8 = c->dtype == NBW_KV_FP8;
+    if (fp8 != (c->k_scale != nullptr) || fp8 != (c->v_scale != nullptr)) return NBW_EINVAL;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->table, 4)) return NBW_EALIGN;
+    if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return NBW_EALIGN;
+    out->k = (uint8_t *)c->k;
+    out->v = (uint8_t *)c->v;
+    out->pages = c->pages;
+    out->heads = c->heads;
+    out->dim = c->dim;
+    out->fp8 = fp8 ? 1 : 0;
+    out->page_log2 = __builtin_ctz(c->page);
+    out->k_scale = c->k_scale;
+    out->v_scale = c->v_scale;
+    out->table = c->table;
+    out->rows = (int)c->rows;
+    out->width = (int)c->width;
+    out->table_ld = c->table_ld ? c->table_ld : c->width;
+    out->cap = (int)(c->width * c->page);
+    return NBW_OK;
+}
+
+// max_len of a call: 0 stands for the capacity, which it does not exceed.
+nbw_status check_max_len(int64_t max_len, const nbw::KvCache &c, int *out) {
+    if (max_len < 0) return NBW_EINVAL;
+    *out = max_len == 0 || max_len > c.cap ? c.cap : (int)max_len;
+    return NBW_OK;
+}
+
+nbw_status check_q_heads(int32_t q_heads, const nbw::KvCache &c) {
+    if (q_heads < 1 || q_heads % c.heads || q_heads / c.heads > 256) return NBW_EINVAL;
+    return (int64_t)q_heads * (c.rows ? c.rows : 1) <= INT_MAX ? NBW_OK : NBW_EINVAL;
 }
 
 }  // namespace
@@ -364,6 +415,150 @@ int64_t nbw_qgemm_workspace_bytes(int64_t batch, int64_t n, int64_t k, int32_t r
     a.n = (int)n;
     a.k = (int)k;
     return nbw::gemm_workspace_bytes(a, cus);
+}
+
+nbw_status nbw_kv_append(const nbw_kvcache *cache, const nbw_kv_append_args *args, void *stream) {
+    nbw::KvCache c;
+    nbw_status st = check_cache(cache, &c);
+    if (st != NBW_OK) return st;
+    if (!args) return NBW_EINVAL;
+    const nbw_kv_append_args &g = *args;
+    if (g.tokens < 0 || g.tokens > INT_MAX - (1 << 20)) return NBW_EINVAL;
+    if (!g.cu && g.tokens != c.rows) return NBW_EINVAL;
+    if (c.rows == 0) return g.tokens == 0 ? NBW_OK : NBW_EINVAL;
+    if (!g.lens || g.lens_out == g.lens) return NBW_EINVAL;
+    nbw::KvAppend a = {};
+    if (g.tokens > 0) {
+        if (!g.k || !g.v || !g.positions || (g.q && !g.q_out)) return NBW_EINVAL;
+        if (g.q && (st = check_q_heads(g.q_heads, c)) != NBW_OK) return st;
+        if (g.rope && g.rope_rows < 1) return NBW_EINVAL;
+        if (!(g.eps >= 0.f && g.eps <= 3.4e38f)) return NBW_EINVAL;  // NaN too
+        const int64_t kv = (int64_t)c.heads * c.dim;
+        if ((st = check_ld(g.k_ld, kv, &a.k_ld)) != NBW_OK) return st;
+        if ((st = check_ld(g.v_ld, kv, &a.v_ld)) != NBW_OK) return st;
+        if (g.q) {
+            const int64_t cols = (int64_t)g.q_heads * c.dim;
+            if ((st = check_ld(g.q_ld, cols, &a.q_ld)) != NBW_OK) return st;
+            if ((st = check_ld(g.q_out_ld, cols, &a.q_out_ld)) != NBW_OK) return st;
+        }
+        if (!aligned(g.k, 16) || !aligned(g.v, 16) || (g.q && (!aligned(g.q, 16) || !aligned(g.q_out, 16))))
+            return NBW_EALIGN;
+        if (!aligned(g.positions, 4) || !aligned(g.rope, 16) || !aligned(g.q_norm, 16) || !aligned(g.k_norm, 16))
+            return NBW_EALIGN;
+    }
+    if (!aligned(g.cu, 4) || !aligned(g.lens, 4) || !aligned(g.pos, 4) || !aligned(g.acc, 4) ||
+        !aligned(g.lens_out, 4))
+        return NBW_EALIGN;
+    a.k = (const uint16_t *)g.k;
+    a.v = (const uint16_t *)g.v;
+    a.q = (const uint16_t *)g.q;
+    a.q_out = (uint16_t *)g.q_out;
+    a.tokens = (int)g.tokens;
+    a.q_heads = g.q ? g.q_heads : 0;
+    a.eps = g.eps;
+    a.cu = g.cu;
+    a.lens = g.lens;
+    a.positions = g.positions;
+    a.rope = g.rope;
+    a.rope_rows = g.rope_rows;
+    a.q_norm = (const uint16_t *)g.q_norm;
+    a.k_norm = (const uint16_t *)g.k_norm;
+    a.pos = g.pos;
+    a.acc = g.acc;
+    a.lens_out = g.lens_out;
+    const hipError_t e = nbw::launch_kv_append(c, a, (hipStream_t)stream);
+    return e == hipSuccess ? NBW_OK : hip_failed(e);
+}
+
+int64_t nbw_kv_attend_workspace_bytes(const nbw_kvcache *cache, int32_t q_heads, int64_t max_len,
+                                      int32_t weights) {
+    nbw::KvCache c;
+    int most = 0, cus = 0;
+    if (check_cache(cache, &c) != NBW_OK || check_q_heads(q_heads, c) != NBW_OK ||
+        check_max_len(max_len, c, &most) != NBW_OK)
+        return -1;
+    if (c.rows == 0) return 0;
+    if (cu_count(&cus) != NBW_OK) return -1;
+    return nbw::kv_attend_workspace_bytes(c, q_heads, most, weights != 0, cus);
+}
+
+nbw_status nbw_kv_attend(const nbw_kvcache *cache, const nbw_kv_attend_args *args, void *stream) {
+    nbw::KvCache c;
+    nbw_status st = check_cache(cache, &c);
+    if (st != NBW_OK) return st;
+    if (!args) return NBW_EINVAL;
+    const nbw_kv_attend_args &g = *args;
+    nbw::KvAttend a = {};
+    if ((st = check_q_heads(g.q_heads, c)) != NBW_OK) return st;
+    if ((st = check_max_len(g.max_len, c, &a.max_len)) != NBW_OK) return st;
+    const int64_t cols = (int64_t)g.q_heads * c.dim;
+    if ((st = check_ld(g.q_ld, cols, &a.q_ld)) != NBW_OK) return st;
+    if ((st = check_ld(g.out_ld, cols, &a.out_ld)) != NBW_OK) return st;
+    if (!(g.scale >= -3.4e38f && g.scale <= 3.4e38f)) return NBW_EINVAL;  // NaN too
+    if ((g.acc != nullptr) != (g.acc_out != nullptr)) return NBW_EINVAL;
+    if (g.acc && !(g.decay >= -3.4e38f && g.decay <= 3.4e38f)) return NBW_EINVAL;
+    if (g.workspace_bytes < 0) return NBW_EINVAL;
+    if (c.rows == 0) return NBW_OK;
+    if (!g.q || !g.out || !g.lens) return NBW_EINVAL;
+    if (!aligned(g.q, 16) || !aligned(g.out, 16) || !aligned(g.lens, 4) || !aligned(g.acc, 4) ||
+        !aligned(g.acc_out, 4) || !aligned(g.workspace, 256))
+        return NBW_EALIGN;
+    int cus = 0;
+    if ((st = cu_count(&cus)) != NBW_OK) return st;
+    const int64_t need = nbw::kv_attend_workspace_bytes(c, g.q_heads, a.max_len, g.acc != nullptr, cus);
+    if (need > 0 && (!g.workspace || g.workspace_bytes < need)) return NBW_ESCRATCH;
+    a.q = (const uint16_t *)g.q;
+    a.out = (uint16_t *)g.out;
+    a.q_heads = g.q_heads;
+    a.scale = g.scale != 0.f ? g.scale : c.dim == 64 ? 0.125f : c.dim == 256 ? 0.0625f : 0.08838834764831845f;
+    a.lens = g.lens;
+    a.acc = g.acc;
+    a.acc_out = g.acc_out;
+    a.decay = g.decay;
+    a.ws = (uint8_t *)g.workspace;
+    const hipError_t e = nbw::launch_kv_attend(c, a, cus, (hipStream_t)stream);
+    return e == hipSuccess ? NBW_OK : hip_failed(e);
+}
+
+int64_t nbw_kv_evict_workspace_bytes(const nbw_kvcache *cache, int64_t budget, int64_t max_len) {
+    nbw::KvCache c;
+    int most = 0;
+    if (check_cache(cache, &c) != NBW_OK || check_max_len(max_len, c, &most) != NBW_OK) return -1;
+    if (budget < 1 || budget > c.cap) return -1;
+    return nbw::kv_evict_workspace_bytes(c, (int)budget, most);
+}
+
+nbw_status nbw_kv_evict(const nbw_kvcache *cache, const nbw_kv_evict_args *args, void *stream) {
+    nbw::KvCache c;
+    nbw_status st = check_cache(cache, &c);
+    if (st != NBW_OK) return st;
+    if (!args) return NBW_EINVAL;
+    const nbw_kv_evict_args &g = *args;
+    nbw::KvEvict a = {};
+    if ((st = check_max_len(g.max_len, c, &a.max_len)) != NBW_OK) return st;
+    if (g.budget < 1 || g.budget > c.cap) return NBW_EINVAL;
+    if (g.sink < 0 || g.recent < 0 || g.sink > g.budget || g.recent > g.budget - g.sink) return NBW_EINVAL;
+    if (g.workspace_bytes < 0) return NBW_EINVAL;
+    if (c.rows == 0) return NBW_OK;
+    if (!g.acc || !g.pos || !g.lens || !g.acc_out || !g.pos_out || !g.lens_out) return NBW_EINVAL;
+    if (g.acc == g.acc_out || g.pos == g.pos_out || g.lens == g.lens_out) return NBW_EINVAL;
+    if (!aligned(g.acc, 4) || !aligned(g.pos, 4) || !aligned(g.lens, 4) || !aligned(g.acc_out, 4) ||
+        !aligned(g.pos_out, 4) || !aligned(g.lens_out, 4) || !aligned(g.workspace, 256))
+        return NBW_EALIGN;
+    const int64_t need = nbw::kv_evict_workspace_bytes(c, (int)g.budget, a.max_len);
+    if (need > 0 && (!g.workspace || g.workspace_bytes < need)) return NBW_ESCRATCH;
+    a.acc = g.acc;
+    a.pos = g.pos;
+    a.lens = g.lens;
+    a.budget = (int)g.budget;
+    a.sink = (int)g.sink;
+    a.recent = (int)g.recent;
+    a.acc_out = g.acc_out;
+    a.pos_out = g.pos_out;
+    a.lens_out = g.lens_out;
+    a.ws = (uint8_t *)g.workspace;
+    const hipError_t e = nbw::launch_kv_evict(c, a, (hipStream_t)stream);
+    return e == hipSuccess ? NBW_OK : hip_failed(e);
 }
 
 int32_t nbw_stream_sink_words(void) { return nbw::stream_sink_words(); }

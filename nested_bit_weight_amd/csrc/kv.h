@@ -1,0 +1,112 @@
+// kv.h -- what the key-value cache's kernels share: the launchers' arguments,
+// the place of a slot in the pools, and the conversions of the element types.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace nbw {
+
+// A cache as the kernels take it (see nbw_kvcache in nbw.h).
+struct KvCache {
+    uint8_t *k, *v;         // pools [pages][heads][page][dim]
+    int64_t pages;
+    int heads, dim, fp8;
+    int page_log2;          // slots of a page: 1 << page_log2
+    const float *k_scale, *v_scale;  // fp8: [heads]
+    const int32_t *table;   // [rows][table_ld]
+    int rows, width;
+    int64_t table_ld;
+    int cap;                // width << page_log2
+};
+
+struct KvAppend {
+    const uint16_t *k, *v, *q;
+    uint16_t *q_out;
+    int64_t k_ld, v_ld, q_ld, q_out_ld;
+    int tokens, q_heads;
+    float eps;
+    const int32_t *cu, *lens, *positions;
+    const float *rope;
+    int64_t rope_rows;
+    const uint16_t *q_norm, *k_norm;
+    int32_t *pos;
+    float *acc;
+    int32_t *lens_out;
+};
+
+struct KvAttend {
+    const uint16_t *q;
+    uint16_t *out;
+    int64_t q_ld, out_ld;
+    int q_heads;
+    float scale;
+    const int32_t *lens;
+    int max_len;
+    const float *acc;
+    float *acc_out;
+    float decay;
+    uint8_t *ws;
+};
+
+struct KvEvict {
+    const float *acc;
+    const int32_t *pos, *lens;
+    int budget, sink, recent;
+    float *acc_out;
+    int32_t *pos_out, *lens_out;
+    int max_len;
+    uint8_t *ws;
+};
+
+hipError_t launch_kv_append(const KvCache &c, const KvAppend &a, hipStream_t stream);
+int64_t kv_attend_workspace_bytes(const KvCache &c, int q_heads, int max_len, bool weights, int cu_count);
+hipError_t launch_kv_attend(const KvCache &c, const KvAttend &a, int cu_count, hipStream_t stream);
+int64_t kv_evict_workspace_bytes(const KvCache &c, int budget, int max_len);
+hipError_t launch_kv_evict(const KvCache &c, const KvEvict &a, hipStream_t stream);
+
+typedef uint32_t u32x2_kv __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_kv __attribute__((ext_vector_type(4)));
+
+// A row's length within [0, bound].
+__device__ __forceinline__ int kv_len(const int32_t *lens, int row, int bound) {
+    const int n = lens[row];
+    return n < 0 ? 0 : n > bound ? bound : n;
+}
+
+// The number of (row, head, slot)'s row in a pool, counted in rows of dim
+// elements, or -1 where the table names no page of the pool.  64 bits: a long
+// cache has more than 2^31 elements.
+__device__ __forceinline__ int64_t kv_row(const KvCache &c, int row, int head, int slot) {
+    const int32_t page = c.table[(int64_t)row * c.table_ld + (slot >> c.page_log2)];
+    if (page < 0 || page >= c.pages) return -1;
+    return (((int64_t)page * c.heads + head) << c.page_log2) + (slot & ((1 << c.page_log2) - 1));
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// fp32 to bf16, to nearest even; a NaN stays one.
+__device__ __forceinline__ uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+
+// Four fp32 values, already divided by the head's factor, to the cache's 8 bits:
+// limited to the largest finite value and rounded to nearest even, NaN kept.
+__device__ __forceinline__ uint32_t to_fp8x4(float a, float b, float c, float d) {
+    auto limit = [](float x) { return x > 448.f ? 448.f : x < -448.f ? -448.f : x; };
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(limit(a), limit(b), 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(limit(c), limit(d), w, true);
+    return (uint32_t)w;
+}
+
+// Byte `i` (0..3) of a word of 8-bit values, as fp32 (exact).
+__device__ __forceinline__ float fp8_at(uint32_t w, int i) {
+    switch (i) {
+    case 0: return __builtin_amdgcn_cvt_f32_fp8(w, 0);
+    case 1: return __builtin_amdgcn_cvt_f32_fp8(w, 1);
+    case 2: return __builtin_amdgcn_cvt_f32_fp8(w, 2);
+    default: return __builtin_amdgcn_cvt_f32_fp8(w, 3);
+    }
+}
+
+}  // namespace nbw
