@@ -157,7 +157,7 @@ nbw_status check_max_len(int64_t max_len, const nbw::KvCache &c, int *out) {
 
 nbw_status check_q_heads(int32_t q_heads, const nbw::KvCache &c) {
     if (q_heads < 1 || q_heads % c.heads || q_heads / c.heads > 256) return NBW_EINVAL;
-    return (int64_t)q_heads * (c.rows ? c.rows : 1) <= INT_MAX ? NBW_OK : NBW_EINVAL;
+    return (int64_t)q_heads * (c.rows ? c.rows : 1) <= (1 << 30) ? NBW_OK : NBW_EINVAL;
 }
 
 }  // namespace
@@ -506,6 +506,7 @@ nbw_status nbw_kv_attend(const nbw_kvcache *cache, const nbw_kv_attend_args *arg
     int cus = 0;
     if ((st = cu_count(&cus)) != NBW_OK) return st;
     const int64_t need = nbw::kv_attend_workspace_bytes(c, g.q_heads, a.max_len, g.acc != nullptr, cus);
+    if (need < 0) return NBW_EINVAL;  // more units than an int counts
     if (need > 0 && (!g.workspace || g.workspace_bytes < need)) return NBW_ESCRATCH;
     a.q = (const uint16_t *)g.q;
     a.out = (uint16_t *)g.out;

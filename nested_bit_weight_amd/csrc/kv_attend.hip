@@ -1,116 +1,676 @@
 // kv_attend.hip -- attention of one new token for each row over its cached
 // ones, gfx950.
 //
-// The plain kernel: one workgroup takes one (row, query head), puts the head's
-// scores into the workspace, turns them into softmax weights there and adds up
-// the values; a second kernel adds a key-value head's weights to the totals.
+// For a query head g and the n slots of its row
+//     s_j = scale q.k_j,   o = sum_j 2^(s_j' - m) v_j / sum_j 2^(s_j' - m),
+// s' = s log2(e), with any m near the largest s'.  Every key and value is read
+// once and meets the G = q_heads / heads query heads of its head, 4 G flops for
+// 4 bytes (2 in the 8-bit cache): at the usual G = 4..8 the operator is bound
+// by the bandwidth of memory by a wide margin, and what follows is arranged
+// around keeping loads in flight.
+//
+// Work: units of CHUNK = 128 slots of one (row, head) in the order (row, head,
+// chunk).  The launch is as many workgroups as the device holds at once, and
+// workgroup w takes the w-th equal share of all units, whatever the rows'
+// lengths are: one long row is spread over the whole device, many short ones
+// are packed.  The lengths stay on the device; each workgroup finds its share
+// from their running sum.  A run of units within one (row, head) is a piece;
+// a (row, head) that lies in one share is finished there, others leave their
+// parts (m, sum, o) in the workspace, which a second launch joins in a fixed
+// order.
+//
+// A piece: wave w takes the 32-slot tile w of each unit, everything in its
+// registers, with the next tile's keys and values loading while this one's are
+// used.  S^T = K Q^T and O = P V on v_mfma_f32_16x16x32_bf16:
+//  - A of the first product is 16 keys by 32 dims, loaded as it is used: lane
+//    l holds 16 bytes of key l % 16.  Its result has head l % 16 in lane l and
+//    slots 4 (l / 16) + 0..3 in the lane's four registers, of each half tile;
+//  - these are the rows of P that the second product's A operand wants in that
+//    lane, if slot 4 (l / 16) + i of half h is given the product's inner index
+//    8 (l / 16) + 4 h + i: P never leaves the lane;
+//  - V is loaded row by row, lane l the dims 8 (l % 16) .. + 7 of the eight
+//    slots of its quarter, and one v_perm for each pair of slots makes the B
+//    operand of column t: dim 8 (l % 16) + t.
+// The weights enter the second product as two bf16 parts, p = hi + lo, so they
+// keep 15 bits or more; with up to 8 heads the parts share one product, hi in its rows
+// 0..7 and lo in rows 8..15, whose scores are computed twice instead of rows
+// standing empty.  Sums of p are taken in fp32 before that.
+//
+// The running maximum m of a head is only raised, and o and the sum rescaled,
+// when a score passes it by more than 8 (a factor of 2^8): the check is one
+// comparison and a branch that is almost never taken after the first tile.
+#include <algorithm>
+
 #include "kv.h"
 
 namespace nbw {
 
-constexpr int ATTEND_THREADS = 256;
+typedef float f32x4_kv __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8_kv __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2_kv __attribute__((ext_vector_type(2)));
 
-template <bool FP8>
-__device__ __forceinline__ float kv_at(const uint8_t *pool, int64_t i) {
-    if (FP8) return fp8_at(pool[i], 0);
-    return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(pool)[i] << 16);
+constexpr int ATTEND_WAVES = 4;
+constexpr int ATTEND_THREADS = 64 * ATTEND_WAVES;
+constexpr int TILE = 32;                     // slots of one wave's step
+constexpr int CHUNK = TILE * ATTEND_WAVES;   // slots of a unit
+constexpr float RAISE = 8.f;                 // how far a score may pass the running maximum
+constexpr float TINY = 1.17549435e-38f;      // the smallest normal number, fp32's and bf16's
+
+#define NEG_INF (-__builtin_inff())
+
+// The launch's division of work and its scratch, the same for both kernels.
+struct AttendPlan {
+    int wgs;             // workgroups that share the units
+    int group;           // query heads of a head
+    int blocks;          // blocks of up to 16 query heads that a head's are taken in
+    int block_heads;     // query heads of a block (the last may have fewer)
+    int32_t *before;     // [rows + 1] units of one (head, block) before each row
+    float *whole;        // [rows][heads * blocks][16][2]: m and sum where one workgroup had it all
+    float *part_ml;      // [2 * wgs][16][2]: m and sum of a piece
+    float *part_o;       // [2 * wgs][block_heads][dim]
+    float *scores;       // [unit][block_heads][CHUNK], with totals only
+};
+
+// The workgroup whose share a unit is in.  Workgroup w leaves the part of a
+// (row, head) that began in an earlier share at place 2 w, and of one that
+// begins in its own and goes on past it at 2 w + 1.
+__device__ __forceinline__ int owner_of(int64_t unit, int64_t units, int shares) {
+    return (int)(((unit + 1) * shares - 1) / units);
+}
+
+// One wave's tile: keys and values as loaded, and which slots count.
+template <int DIM, bool FP8>
+struct Tile {
+    static constexpr int KV4 = FP8 ? DIM / 64 : DIM / 32;  // 16-byte loads of a key
+    static constexpr int NC = DIM > 128 ? DIM / 128 : 1;   // blocks of dims of a value
+    static constexpr int DPL = DIM / NC / 16;              // dims of a block in one lane
+    static constexpr int VW = FP8 ? DPL / 4 : DPL / 2;     // words of them
+    u32x4_kv k[2][KV4];
+    uint32_t v[2][4][NC][VW];
+    uint32_t there;  // bit 4 h + i: slot 4 (lane / 16) + i of half h
+};
+
+template <int W>
+__device__ __forceinline__ void load_words(uint32_t *out, const uint8_t *p) {
+    if constexpr (W == 4) {
+        const u32x4_kv x = *reinterpret_cast<const u32x4_kv *>(p);
+        out[0] = x[0], out[1] = x[1], out[2] = x[2], out[3] = x[3];
+    } else if constexpr (W == 2) {
+        const u32x2_kv x = *reinterpret_cast<const u32x2_kv *>(p);
+        out[0] = x[0], out[1] = x[1];
+    } else {
+        out[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+}
+
+// Two 8-bit values of a word (half 0: its lower two) as a pair of bf16, exact.
+template <int HALF>
+__device__ __forceinline__ uint32_t fp8_pair(uint32_t w) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HALF));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const bf16x2_kv p = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, p);
+}
+
+template <int DIM, bool FP8, bool PACK, bool SMALL>
+__global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_kernel(KvCache c, KvAttend a, AttendPlan pl) {
+    using T = Tile<DIM, FP8>;
+    constexpr int HR = PACK ? 8 : 16;                 // heads a workgroup holds
+    constexpr int ROW_BYTES = FP8 ? DIM : DIM * 2;
+    constexpr int COLS = DIM / T::NC;                 // dims of a block
+    constexpr int QF = DIM / 32;                      // Q operands
+    __shared__ int scan[ATTEND_WAVES];
+    __shared__ int found[2];
+    __shared__ float wave_ml[ATTEND_WAVES][HR][2];
+    __shared__ __align__(16) float wave_o[ATTEND_WAVES][HR][COLS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int quad = lane >> 4, col = lane & 15;
+    const int vheads = c.heads * pl.blocks;
+
+    // Units of one (head, block) before each row, in strips of rows for each thread.
+    const int strip = (c.rows + ATTEND_THREADS - 1) / ATTEND_THREADS;
+    const int r0 = tid * strip, r1 = min(r0 + strip, c.rows);
+    int mine = 0;
+    for (int r = r0; r < r1; ++r) mine += (kv_len(a.lens, r, a.max_len) + CHUNK - 1) / CHUNK;
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int x = __shfl_up(upto, d);
+        if (lane >= d) upto += x;
+    }
+    if (lane == 63) scan[wave] = upto;
+    __syncthreads();
+    int chunks = 0;
+#pragma unroll
+    for (int w = 0; w < ATTEND_WAVES; ++w) {
+        if (w < wave) upto += scan[w];
+        chunks += scan[w];
+    }
+    const int before = upto - mine;
+    const int64_t units = (int64_t)chunks * vheads;
+    const int shares = (int)min((int64_t)pl.wgs, units);  // none is empty
+    const int u0 = (int)blockIdx.x < shares ? (int)(units * blockIdx.x / shares) : 0;
+    const int u1 = (int)blockIdx.x < shares ? (int)(units * (blockIdx.x + 1) / shares) : 0;
+    if (blockIdx.x == 0 && pl.before) {
+        int at = before;
+        for (int r = r0; r < r1; ++r) {
+            pl.before[r] = at;
+            at += (kv_len(a.lens, r, a.max_len) + CHUNK - 1) / CHUNK;
+        }
+        if (tid == 0) pl.before[c.rows] = chunks;
+    }
+    // Rows without a slot: zeros.
+    for (int r = blockIdx.x; r < c.rows; r += pl.wgs) {
+        if (kv_len(a.lens, r, a.max_len)) continue;
+        for (int i = tid; i < a.q_heads * DIM / 8; i += ATTEND_THREADS)
+            reinterpret_cast<u32x4_kv *>(a.out + (int64_t)r * a.out_ld)[i] = u32x4_kv{0, 0, 0, 0};
+    }
+    if (u0 >= u1) return;
+    {
+        const int64_t lo = (int64_t)before * vheads, hi = (int64_t)(before + mine) * vheads;
+        if (lo <= u0 && u0 < hi) {
+            int at = before, r = r0;
+            for (;; ++r) {
+                const int n = (kv_len(a.lens, r, a.max_len) + CHUNK - 1) / CHUNK;
+                if (u0 < (int64_t)(at + n) * vheads) break;
+                at += n;
+            }
+            found[0] = r;
+            found[1] = at;
+        }
+    }
+    __syncthreads();
+    int row = __builtin_amdgcn_readfirstlane(found[0]);
+    int row_at = __builtin_amdgcn_readfirstlane(found[1]);
+    int len = __builtin_amdgcn_readfirstlane(kv_len(a.lens, row, a.max_len));
+    int row_chunks = (len + CHUNK - 1) / CHUNK;
+    int vh = (u0 - row_at * vheads) / row_chunks;
+
+    for (int u = u0; u < u1;) {
+        // The piece: chunks [c0, c1) of (row, vh).
+        const int seg0 = row_at * vheads + vh * row_chunks, seg1 = seg0 + row_chunks;
+        const int c0 = u - seg0, c1 = min(u1, seg1) - seg0;
+        const int head = vh / pl.blocks, block = vh % pl.blocks;
+        const int g0 = block * pl.block_heads, heads = min(pl.block_heads, pl.group - g0);
+        const int32_t *table = c.table + (int64_t)row * c.table_ld;
+        const float by = a.scale * 1.44269504088896340736f * (FP8 ? c.k_scale[head] : 1.f);
+
+        // Q as the first product's B operand: column `col`'s head, the dims that
+        // the key operand of the same number holds in this lane.
+        u32x4_kv qf[QF];
+        const int qh = PACK ? col & 7 : col;
+        {
+            const uint16_t *q = a.q + (int64_t)row * a.q_ld + ((int64_t)head * pl.group + g0 + (qh < heads ? qh : 0)) * DIM;
+#pragma unroll
+            for (int f = 0; f < QF; ++f) {
+                const int d = FP8 ? (f >> 1) * 64 + quad * 16 + (f & 1) * 8 : f * 32 + quad * 8;
+                qf[f] = qh < heads ? *reinterpret_cast<const u32x4_kv *>(q + d) : u32x4_kv{0, 0, 0, 0};
+            }
+        }
+
+        // Page numbers of the tile at `slot`.  Pages of 16 slots and more: one for
+        // each half, the same in all lanes; smaller ones: lane l has slot l % 32's.
+        struct Pages { int32_t p[SMALL ? 1 : 2]; };
+        auto pages_of = [&](int chunk) {
+            Pages r;
+            const int slot = chunk * CHUNK + wave * TILE;
+            if constexpr (SMALL) {
+                const int s = slot + (lane & 31);
+                r.p[0] = s < len && chunk < c1 ? table[s >> c.page_log2] : -1;
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    r.p[h] = slot + 16 * h < len && chunk < c1 ? table[(slot + 16 * h) >> c.page_log2] : -1;
+            }
+            return r;
+        };
+        auto load = [&](T &t, const Pages &pg, int chunk) {
+            const int slot = chunk * CHUNK + wave * TILE, mask = (1 << c.page_log2) - 1;
+            t.there = 0;
+            if constexpr (SMALL) {
+                const int32_t own = pg.p[0];
+                const int mine_ok = own >= 0 && own < c.pages;
+                const int32_t safe = mine_ok ? own : -1;
+                auto place = [&](int s, bool &ok) -> int64_t {  // byte offset of slot s (0..31) of the tile
+                    const int32_t p = __shfl(safe, s);
+                    ok = p >= 0;
+                    return ((((int64_t)(ok ? p : 0) * c.heads + head) << c.page_log2) + ((slot + s) & mask)) * ROW_BYTES;
+                };
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    bool ok;
+                    const uint8_t *p = c.k + place(16 * h + col, ok) + quad * 16;
+#pragma unroll
+                    for (int f = 0; f < T::KV4; ++f) t.k[h][f] = *reinterpret_cast<const u32x4_kv *>(p + f * 64);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint8_t *q = c.v + place(16 * h + quad * 4 + i, ok) + col * T::VW * 4;
+                        t.there |= (uint32_t)ok << (4 * h + i);
+#pragma unroll
+                        for (int n = 0; n < T::NC; ++n) load_words<T::VW>(t.v[h][i][n], q + n * (ROW_BYTES / T::NC));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int s = slot + 16 * h;
+                    const bool ok = pg.p[h] >= 0 && pg.p[h] < c.pages;
+                    const int left = ok ? min(len - s, 16) - quad * 4 : 0;
+                    t.there |= (left >= 4 ? 15u : left <= 0 ? 0u : (1u << left) - 1) << (4 * h);
+                    const int64_t base = ((((int64_t)(ok ? pg.p[h] : 0) * c.heads + head) << c.page_log2) + (s & mask)) * ROW_BYTES;
+                    const uint8_t *kb = c.k + base, *vb = c.v + base;
+                    const uint32_t ko = col * ROW_BYTES + quad * 16, vo = quad * 4 * ROW_BYTES + col * T::VW * 4;
+#pragma unroll
+                    for (int f = 0; f < T::KV4; ++f) t.k[h][f] = *reinterpret_cast<const u32x4_kv *>(kb + ko + f * 64);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int n = 0; n < T::NC; ++n)
+                            load_words<T::VW>(t.v[h][i][n], vb + vo + i * ROW_BYTES + n * (ROW_BYTES / T::NC));
+                }
+            }
+        };
+
+        f32x4_kv o[T::NC][T::DPL];
+#pragma unroll
+        for (int n = 0; n < T::NC; ++n)
+#pragma unroll
+            for (int t = 0; t < T::DPL; ++t) o[n][t] = f32x4_kv{0.f, 0.f, 0.f, 0.f};
+        float m = NEG_INF, sum = 0.f;
+
+        auto use = [&](T &t, int chunk) {
+            f32x4_kv s[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+            for (int f = 0; f < QF; ++f)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    u32x4_kv kf;
+                    if constexpr (FP8) {
+                        const uint32_t w0 = t.k[h][f >> 1][(f & 1) * 2], w1 = t.k[h][f >> 1][(f & 1) * 2 + 1];
+                        kf = u32x4_kv{fp8_pair<0>(w0), fp8_pair<1>(w0), fp8_pair<0>(w1), fp8_pair<1>(w1)};
+                    } else {
+                        kf = t.k[h][f];
+                    }
+                    s[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_kv, kf),
+                                                                   __builtin_bit_cast(bf16x8_kv, qf[f]), s[h], 0, 0, 0);
+                }
+            const bool full = __all(t.there == 0xFFu);
+            float x[8], top = NEG_INF;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = s[i >> 2][i & 3] * by;
+            if (!full) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = t.there >> i & 1 ? x[i] : NEG_INF;
+            }
+            if (pl.scores && col < heads) {
+                float *dst = pl.scores + ((int64_t)(seg0 + chunk) * pl.block_heads + col) * CHUNK + wave * TILE + quad * 4;
+                *reinterpret_cast<f32x4_kv *>(dst) = f32x4_kv{x[0], x[1], x[2], x[3]};
+                *reinterpret_cast<f32x4_kv *>(dst + 16) = f32x4_kv{x[4], x[5], x[6], x[7]};
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
+            if (__any(top > m + RAISE)) {
+                top = fmaxf(m, top);
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                const float fade = top == m ? 1.f : exp2f(m - top);  // equal: -inf, or nothing to do
+                m = top;
+                sum *= fade;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float f = __shfl(fade, quad * 4 + i);
+#pragma unroll
+                    for (int n = 0; n < T::NC; ++n)
+#pragma unroll
+                        for (int e = 0; e < T::DPL; ++e) o[n][e][i] *= f;
+                }
+            }
+            const float ref = m == NEG_INF ? 0.f : m;
+            float p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                p[i] = __builtin_amdgcn_exp2f(x[i] - ref);
+                sum += p[i];
+            }
+            u32x4_kv hi, lo;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // hi is cut off, not rounded, so lo is not negative; neither is 0, so an
+                // infinite value stays one (0 * inf and inf - inf would be NaN).
+                const float a0 = fmaxf(p[2 * i], TINY), a1 = fmaxf(p[2 * i + 1], TINY);
+                hi[i] = __builtin_amdgcn_perm(__float_as_uint(a1), __float_as_uint(a0), 0x07060302u);
+                lo[i] = pack_bf16(fmaxf(a0 - bf16_lo(hi[i]), TINY), fmaxf(a1 - bf16_hi(hi[i]), TINY));
+                if (PACK) hi[i] = col < 8 ? hi[i] : lo[i];
+            }
+#pragma unroll
+            for (int n = 0; n < T::NC; ++n) {
+                uint32_t w[8][T::DPL / 2];  // the eight slots' dims as pairs of bf16
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t *src = t.v[i >> 2][i & 3][n];
+#pragma unroll
+                    for (int d = 0; d < T::DPL / 2; ++d) {
+                        if constexpr (FP8) w[i][d] = d & 1 ? fp8_pair<1>(src[d >> 1]) : fp8_pair<0>(src[d >> 1]);
+                        else w[i][d] = src[d];
+                    }
+                }
+                if (!full) {  // 0 * what lies there would be NaN for an infinity or a NaN
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int d = 0; d < T::DPL / 2; ++d) w[i][d] = t.there >> i & 1 ? w[i][d] : 0u;
+                }
+#pragma unroll
+                for (int e = 0; e < T::DPL; ++e) {
+                    u32x4_kv vf;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        vf[i] = __builtin_amdgcn_perm(w[2 * i + 1][e >> 1], w[2 * i][e >> 1], e & 1 ? 0x07060302u : 0x05040100u);
+                    o[n][e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_kv, hi),
+                                                                      __builtin_bit_cast(bf16x8_kv, vf), o[n][e], 0, 0, 0);
+                    if (!PACK)
+                        o[n][e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_kv, lo),
+                                                                          __builtin_bit_cast(bf16x8_kv, vf), o[n][e], 0, 0, 0);
+                }
+            }
+        };
+
+        // Two tiles in turn; page numbers one tile further ahead.
+        {
+            T ta, tb;
+            Pages pg = pages_of(c0);
+            load(ta, pg, c0);
+            pg = pages_of(c0 + 1);
+            for (int ch = c0; ch < c1; ch += 2) {
+                if (ch + 1 < c1) {
+                    load(tb, pg, ch + 1);
+                    pg = pages_of(ch + 2);
+                }
+                use(ta, ch);
+                if (ch + 1 < c1) {
+                    if (ch + 2 < c1) {
+                        load(ta, pg, ch + 2);
+                        pg = pages_of(ch + 3);
+                    }
+                    use(tb, ch + 1);
+                }
+            }
+        }
+
+        // The four waves' results together.
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        if (lane < HR) {
+            wave_ml[wave][lane][0] = m;
+            wave_ml[wave][lane][1] = sum;
+        }
+        __syncthreads();
+        const bool whole = c0 == 0 && c1 == row_chunks;
+        const int part = 2 * blockIdx.x + (c0 > 0 ? 0 : 1);
+        auto merged = [&](int h, float &top, float &total) {
+            top = NEG_INF;
+            total = 0.f;
+#pragma unroll
+            for (int w = 0; w < ATTEND_WAVES; ++w) top = fmaxf(top, wave_ml[w][h][0]);
+#pragma unroll
+            for (int w = 0; w < ATTEND_WAVES; ++w) {
+                const float mw = wave_ml[w][h][0];
+                total += wave_ml[w][h][1] * (mw == top ? 1.f : exp2f(mw - top));
+            }
+        };
+        float scale_o[4];  // of this lane's rows of o
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float top, total;
+            const int h = (quad * 4 + i) & (HR - 1);
+            merged(h, top, total);
+            const float mw = wave_ml[wave][h][0];
+            scale_o[i] = mw == top ? 1.f : exp2f(mw - top);
+        }
+        if (tid < heads) {
+            float top, total;
+            merged(tid, top, total);
+            if (!whole) {
+                pl.part_ml[(part * 16 + tid) * 2] = top;
+                pl.part_ml[(part * 16 + tid) * 2 + 1] = total;
+            } else if (pl.scores) {
+                float *w = pl.whole + (((int64_t)row * vheads + vh) * 16 + tid) * 2;
+                w[0] = top;
+                w[1] = total;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < T::NC; ++n) {
+            if (n) __syncthreads();
+#pragma unroll
+            for (int e = 0; e < T::DPL; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float x = o[n][e][i] * scale_o[i];
+                    if (PACK) x += __shfl_xor(x, 32);  // the weights' lower parts
+                    const int h = quad * 4 + i;
+                    if (h < HR) wave_o[wave][h][col * T::DPL + e] = x;
+                }
+            __syncthreads();
+            for (int i = tid; i < heads * (COLS / 4); i += ATTEND_THREADS) {
+                const int h = i / (COLS / 4), d = i % (COLS / 4) * 4;
+                f32x4_kv x = *reinterpret_cast<f32x4_kv *>(&wave_o[0][h][d]);
+#pragma unroll
+                for (int w = 1; w < ATTEND_WAVES; ++w) x += *reinterpret_cast<f32x4_kv *>(&wave_o[w][h][d]);
+                if (whole) {
+                    float top, total;
+                    merged(h, top, total);
+                    const float inv = total == 0.f ? 0.f : (FP8 ? c.v_scale[head] : 1.f) / total;
+                    uint16_t *dst = a.out + (int64_t)row * a.out_ld + ((int64_t)head * pl.group + g0 + h) * DIM + n * COLS + d;
+                    *reinterpret_cast<u32x2_kv *>(dst) = u32x2_kv{pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv)};
+                } else {
+                    float *dst = pl.part_o + ((int64_t)part * pl.block_heads + h) * DIM + n * COLS + d;
+                    *reinterpret_cast<f32x4_kv *>(dst) = x;
+                }
+            }
+        }
+        u = seg0 + c1;
+        if (u < u1) {  // the next (row, head): wave_ml and wave_o are free once all have read them
+            __syncthreads();
+            if (++vh == vheads) {
+                vh = 0;
+                row_at += row_chunks;
+                do {
+                    ++row;
+                    len = __builtin_amdgcn_readfirstlane(kv_len(a.lens, row, a.max_len));
+                } while (len == 0);
+                row_chunks = (len + CHUNK - 1) / CHUNK;
+            }
+        }
+    }
+}
+
+constexpr int JOIN_THREADS = 256;
+
+// The second launch.  Workgroups 0 .. rows * q_heads - 1 join one query head's
+// parts; those after them add the weights to the totals, each for an equal
+// share of the units of (row, head, chunk).
+template <int DIM>
+__global__ __launch_bounds__(JOIN_THREADS) void kv_join_kernel(KvCache c, KvAttend a, AttendPlan pl, int joins) {
+    constexpr int LANES = DIM / 4, SLICES = JOIN_THREADS / LANES;
+    __shared__ __align__(16) float slice_o[SLICES][DIM];
+    __shared__ float slice_l[SLICES];
+    __shared__ float head_m[256], head_inv[256];
+    const int tid = threadIdx.x, vheads = c.heads * pl.blocks;
+    const int64_t units = (int64_t)pl.before[c.rows] * vheads;
+    if (units == 0) return;
+    const int shares = (int)min((int64_t)pl.wgs, units);
+
+    if ((int)blockIdx.x < joins) {
+        const int row = blockIdx.x / a.q_heads, qh = blockIdx.x % a.q_heads;
+        const int head = qh / pl.group, block = qh % pl.group / pl.block_heads, h = qh % pl.group % pl.block_heads;
+        const int at = pl.before[row], chunks = pl.before[row + 1] - at;
+        if (chunks == 0) return;
+        const int64_t seg0 = (int64_t)at * vheads + (int64_t)(head * pl.blocks + block) * chunks;
+        const int w0 = owner_of(seg0, units, shares), w1 = owner_of(seg0 + chunks - 1, units, shares);
+        if (w0 == w1) return;  // written already
+        const int d = tid % LANES * 4, slice = tid / LANES;
+        float m = NEG_INF, l = 0.f;
+        f32x4_kv o = {0.f, 0.f, 0.f, 0.f};
+        for (int w = w0 + slice; w <= w1; w += SLICES) {
+            const int part = w == w0 ? 2 * w + 1 : 2 * w;
+            const float pm = pl.part_ml[(part * 16 + h) * 2], ps = pl.part_ml[(part * 16 + h) * 2 + 1];
+            const f32x4_kv x = *reinterpret_cast<const f32x4_kv *>(pl.part_o + ((int64_t)part * pl.block_heads + h) * DIM + d);
+            const float top = fmaxf(m, pm);
+            const float f0 = m == top ? 1.f : exp2f(m - top), f1 = pm == top ? 1.f : exp2f(pm - top);
+            l = l * f0 + ps * f1;
+            o = o * f0 + x * f1;
+            m = top;
+        }
+        if (tid % LANES == 0) {
+            head_m[slice] = m;
+        }
+        __syncthreads();
+        float top = NEG_INF;
+        for (int s = 0; s < SLICES; ++s) top = fmaxf(top, head_m[s]);
+        const float f = m == top ? 1.f : exp2f(m - top);
+        if (tid % LANES == 0) slice_l[slice] = l * f;
+        *reinterpret_cast<f32x4_kv *>(&slice_o[slice][d]) = o * f;
+        __syncthreads();
+        if (tid < LANES) {
+            float total = 0.f;
+            f32x4_kv x = {0.f, 0.f, 0.f, 0.f};
+            for (int s = 0; s < SLICES; ++s) {
+                total += slice_l[s];
+                x += *reinterpret_cast<f32x4_kv *>(&slice_o[s][d]);
+            }
+            const float inv = total == 0.f ? 0.f : (c.fp8 ? c.v_scale[head] : 1.f) / total;
+            uint16_t *dst = a.out + (int64_t)row * a.out_ld + (int64_t)qh * DIM + d;
+            *reinterpret_cast<u32x2_kv *>(dst) = u32x2_kv{pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv)};
+        }
+        return;
+    }
+
+    const int index = blockIdx.x - joins, sharers = gridDim.x - joins;
+    const int64_t all = (int64_t)pl.before[c.rows] * c.heads;
+    const int64_t t0 = all * index / sharers, t1 = all * (index + 1) / sharers;
+    if (t0 >= t1) return;
+    int row = 0;
+    for (int r0 = 0; r0 < c.rows; r0 += JOIN_THREADS) {
+        const int r = r0 + tid;
+        row += __syncthreads_count(r < c.rows && (int64_t)pl.before[r + 1] * c.heads <= t0);
+    }
+    for (int64_t t = t0; t < t1;) {
+        const int at = pl.before[row], chunks = pl.before[row + 1] - at;
+        if (chunks == 0) {
+            ++row;
+            continue;
+        }
+        const int64_t row0 = (int64_t)at * c.heads;
+        const int head = (int)((t - row0) / chunks), c0 = (int)((t - row0) % chunks);
+        const int c1 = (int)min((int64_t)chunks, c0 + (t1 - t));
+        const int n = kv_len(a.lens, row, a.max_len);
+        __syncthreads();
+        if (tid < pl.group) {  // each query head's m and 1 / sum over all of its parts
+            const int block = tid / pl.block_heads, h = tid % pl.block_heads;
+            const int64_t seg0 = (int64_t)at * vheads + (int64_t)(head * pl.blocks + block) * chunks;
+            const int w0 = owner_of(seg0, units, shares), w1 = owner_of(seg0 + chunks - 1, units, shares);
+            float m = NEG_INF, l = 0.f;
+            if (w0 == w1) {
+                const float *w = pl.whole + (((int64_t)row * vheads + head * pl.blocks + block) * 16 + h) * 2;
+                m = w[0];
+                l = w[1];
+            } else {
+                for (int w = w0; w <= w1; ++w) m = fmaxf(m, pl.part_ml[((w == w0 ? 2 * w + 1 : 2 * w) * 16 + h) * 2]);
+                for (int w = w0; w <= w1; ++w) {
+                    const float *p = pl.part_ml + ((w == w0 ? 2 * w + 1 : 2 * w) * 16 + h) * 2;
+                    l += p[1] * (p[0] == m ? 1.f : exp2f(p[0] - m));
+                }
+            }
+            head_m[tid] = m == NEG_INF ? 0.f : m;
+            head_inv[tid] = l == 0.f ? 0.f : 1.f / l;
+        }
+        __syncthreads();
+        for (int i = tid; i < (c1 - c0) * CHUNK; i += JOIN_THREADS) {
+            const int chunk = c0 + i / CHUNK, slot = chunk * CHUNK + i % CHUNK;
+            if (slot >= n) continue;
+            float w = 0.f;
+            for (int b = 0; b < pl.blocks; ++b) {
+                const int heads = min(pl.block_heads, pl.group - b * pl.block_heads);
+                const int64_t unit = (int64_t)at * vheads + (int64_t)(head * pl.blocks + b) * chunks + chunk;
+                const float *s = pl.scores + unit * pl.block_heads * CHUNK + i % CHUNK;
+                for (int h = 0; h < heads; ++h)
+                    w += __builtin_amdgcn_exp2f(s[h * CHUNK] - head_m[b * pl.block_heads + h]) * head_inv[b * pl.block_heads + h];
+            }
+            const int64_t j = ((int64_t)row * c.heads + head) * c.cap + slot;
+            a.acc_out[j] = a.decay * a.acc[j] + w;
+        }
+        t += c1 - c0;
+        if (head == c.heads - 1 && c1 == chunks) ++row;
+    }
+}
+
+// The plan, its scratch laid out from `base`; returns the bytes (-1: too many units).
+static int64_t attend_plan(const KvCache &c, int q_heads, int max_len, bool weights, int cu_count, uint8_t *base,
+                           AttendPlan *pl) {
+    pl->group = q_heads / c.heads;
+    pl->blocks = (pl->group + 15) / 16;
+    pl->block_heads = (pl->group + pl->blocks - 1) / pl->blocks;
+    const int64_t vheads = (int64_t)c.heads * pl->blocks, chunks = (max_len + CHUNK - 1) / CHUNK;
+    const int64_t most = c.rows * vheads * chunks;
+    if (most > INT32_MAX) return -1;
+    // As many workgroups as run at once: two on a CU, one at 256 dims (registers).
+    pl->wgs = (int)std::max<int64_t>(1, std::min<int64_t>(most, (int64_t)cu_count * (c.dim > 128 ? 1 : 2)));
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        uint8_t *p = base ? base + at : nullptr;
+        at += (bytes + 255) / 256 * 256;
+        return p;
+    };
+    pl->before = nullptr;
+    pl->whole = pl->part_ml = pl->part_o = pl->scores = nullptr;
+    if (chunks <= 1 && !weights) return 0;  // no (row, head) is divided
+    pl->before = (int32_t *)take((c.rows + 1) * 4);
+    pl->part_ml = (float *)take((int64_t)pl->wgs * 2 * 16 * 2 * 4);
+    pl->part_o = (float *)take((int64_t)pl->wgs * 2 * pl->block_heads * c.dim * 4);
+    if (weights) {
+        pl->whole = (float *)take(c.rows * vheads * 16 * 2 * 4);
+        pl->scores = (float *)take(most * pl->block_heads * CHUNK * 4);
+    }
+    return at;
+}
+
+int64_t kv_attend_workspace_bytes(const KvCache &c, int q_heads, int max_len, bool weights, int cu_count) {
+    AttendPlan pl;
+    return attend_plan(c, q_heads, max_len, weights, cu_count, nullptr, &pl);
 }
 
 template <int DIM, bool FP8>
-__global__ __launch_bounds__(ATTEND_THREADS) void kv_attend_kernel(KvCache c, KvAttend a) {
-    __shared__ float q[DIM];
-    __shared__ float part[ATTEND_THREADS];
-    const int tid = threadIdx.x;
-    const int row = blockIdx.x / a.q_heads, g = blockIdx.x % a.q_heads;
-    const int head = g / (a.q_heads / c.heads);
-    const int n = kv_len(a.lens, row, a.max_len);
-    float *p = reinterpret_cast<float *>(a.ws) + (int64_t)blockIdx.x * a.max_len;
-    for (int d = tid; d < DIM; d += ATTEND_THREADS)
-        q[d] = __uint_as_float((uint32_t)a.q[(int64_t)row * a.q_ld + (int64_t)g * DIM + d] << 16);
-    __syncthreads();
-    const float by = a.scale * (FP8 ? c.k_scale[head] : 1.f);
-    float top = -__builtin_inff();
-    for (int j = tid; j < n; j += ATTEND_THREADS) {
-        const int64_t at = kv_row(c, row, head, j);
-        float s = 0.f;
-        if (at < 0) s = -__builtin_inff();
-        else {
-            for (int d = 0; d < DIM; ++d) s += q[d] * kv_at<FP8>(c.k, at * DIM + d);
-            s *= by;
-        }
-        p[j] = s;
-        top = fmaxf(top, s);
-    }
-    part[tid] = top;
-    __syncthreads();
-    for (int d = ATTEND_THREADS / 2; d; d >>= 1) {
-        if (tid < d) part[tid] = fmaxf(part[tid], part[tid + d]);
-        __syncthreads();
-    }
-    top = part[0] == -__builtin_inff() ? 0.f : part[0];
-    __syncthreads();
-    float sum = 0.f;
-    for (int j = tid; j < n; j += ATTEND_THREADS) {
-        const float e = expf(p[j] - top);
-        p[j] = e;
-        sum += e;
-    }
-    part[tid] = sum;
-    __syncthreads();
-    for (int d = ATTEND_THREADS / 2; d; d >>= 1) {
-        if (tid < d) part[tid] += part[tid + d];
-        __syncthreads();
-    }
-    const float inv = part[0] == 0.f ? 0.f : 1.f / part[0];
-    __syncthreads();
-    for (int j = tid; j < n; j += ATTEND_THREADS) p[j] *= inv;
-    __syncthreads();
-    for (int d0 = 0; d0 < DIM; d0 += 64) {
-        const int d = d0 + (tid & 63);
-        float o = 0.f;
-        for (int j = tid >> 6; j < n; j += ATTEND_THREADS / 64) {
-            const int64_t at = kv_row(c, row, head, j);
-            if (at >= 0) o += p[j] * kv_at<FP8>(c.v, at * DIM + d);
-        }
-        part[tid] = o;
-        __syncthreads();
-        if (tid < 64) {
-            o = 0.f;
-            for (int w = 0; w < ATTEND_THREADS / 64; ++w) o += part[w * 64 + tid];
-            a.out[(int64_t)row * a.out_ld + (int64_t)g * DIM + d] = to_bf16(FP8 ? o * c.v_scale[head] : o);
-        }
-        __syncthreads();
+static void launch_attend(const KvCache &c, const KvAttend &a, const AttendPlan &pl, hipStream_t stream) {
+    const dim3 grid(pl.wgs), threads(ATTEND_THREADS);
+    const bool pack = pl.block_heads <= 8, small = c.page_log2 < 4;
+    if (pack && small) hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, true, true>), grid, threads, 0, stream, c, a, pl);
+    else if (pack) hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, true, false>), grid, threads, 0, stream, c, a, pl);
+    else if (small) hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, false, true>), grid, threads, 0, stream, c, a, pl);
+    else hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, false, false>), grid, threads, 0, stream, c, a, pl);
+    if (pl.before) {
+        const int joins = c.rows * a.q_heads;
+        const dim3 both((unsigned)joins + (pl.scores ? pl.wgs : 0));
+        hipLaunchKernelGGL((kv_join_kernel<DIM>), both, dim3(JOIN_THREADS), 0, stream, c, a, pl, joins);
     }
 }
 
-__global__ __launch_bounds__(ATTEND_THREADS) void kv_totals_kernel(KvCache c, KvAttend a) {
-    const int row = blockIdx.x / c.heads, head = blockIdx.x % c.heads, group = a.q_heads / c.heads;
-    const int n = kv_len(a.lens, row, a.max_len);
-    const float *p = reinterpret_cast<const float *>(a.ws) + ((int64_t)row * a.q_heads + head * group) * a.max_len;
-    for (int j = threadIdx.x; j < n; j += ATTEND_THREADS) {
-        float w = 0.f;
-        for (int g = 0; g < group; ++g) w += p[(int64_t)g * a.max_len + j];
-        const int64_t i = (int64_t)blockIdx.x * c.cap + j;
-        a.acc_out[i] = a.decay * a.acc[i] + w;
-    }
-}
-
-int64_t kv_attend_workspace_bytes(const KvCache &c, int q_heads, int max_len, bool, int) {
-    return (int64_t)c.rows * q_heads * max_len * 4;
-}
-
-hipError_t launch_kv_attend(const KvCache &c, const KvAttend &a, int, hipStream_t stream) {
-    const dim3 grid((unsigned)c.rows * a.q_heads);
-#define NBW_ATTEND(D, F)                                                                             \
-    hipLaunchKernelGGL((kv_attend_kernel<D, F>), grid, dim3(ATTEND_THREADS), 0, stream, c, a)
+hipError_t launch_kv_attend(const KvCache &c, const KvAttend &a, int cu_count, hipStream_t stream) {
+    AttendPlan pl;
+    attend_plan(c, a.q_heads, a.max_len, a.acc != nullptr, cu_count, a.ws, &pl);
     switch (c.dim) {
-    case 64: if (c.fp8) NBW_ATTEND(64, true); else NBW_ATTEND(64, false); break;
-    case 128: if (c.fp8) NBW_ATTEND(128, true); else NBW_ATTEND(128, false); break;
-    default: if (c.fp8) NBW_ATTEND(256, true); else NBW_ATTEND(256, false); break;
+    case 64:
+        if (c.fp8) launch_attend<64, true>(c, a, pl, stream); else launch_attend<64, false>(c, a, pl, stream);
+        break;
+    case 128:
+        if (c.fp8) launch_attend<128, true>(c, a, pl, stream); else launch_attend<128, false>(c, a, pl, stream);
+        break;
+    default:
+        if (c.fp8) launch_attend<256, true>(c, a, pl, stream); else launch_attend<256, false>(c, a, pl, stream);
+        break;
     }
-#undef NBW_ATTEND
-    if (a.acc)
-        hipLaunchKernelGGL(kv_totals_kernel, dim3((unsigned)c.rows * c.heads), dim3(ATTEND_THREADS), 0, stream, c, a);
     return hipGetLastError();
 }
 
