@@ -547,6 +547,7 @@ nbw_status nbw_kv_evict(const nbw_kvcache *cache, const nbw_kv_evict_args *args,
         !aligned(g.pos_out, 4) || !aligned(g.lens_out, 4) || !aligned(g.workspace, 256))
         return NBW_EALIGN;
     const int64_t need = nbw::kv_evict_workspace_bytes(c, (int)g.budget, a.max_len);
+    if (need < 0) return NBW_EINVAL;  // more workgroups than an int counts
     if (need > 0 && (!g.workspace || g.workspace_bytes < need)) return NBW_ESCRATCH;
     a.acc = g.acc;
     a.pos = g.pos;
