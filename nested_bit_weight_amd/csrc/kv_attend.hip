@@ -58,6 +58,12 @@ constexpr float TINY = 1.17549435e-38f;      // the smallest normal number, fp32
 
 #define NEG_INF (-__builtin_inff())
 
+// A word that no kernel of this launch writes, at an address all lanes share: a
+// scalar load, which does not wait in line behind the keys and values in flight.
+__device__ __forceinline__ int32_t uniform_word(const int32_t *p) {
+    return *reinterpret_cast<const __attribute__((address_space(4))) int32_t *>(reinterpret_cast<uintptr_t>(p));
+}
+
 // The launch's division of work and its scratch, the same for both kernels.
 struct AttendPlan {
     int wgs;             // workgroups that share the units
@@ -69,6 +75,8 @@ struct AttendPlan {
     float *part_ml;      // [2 * wgs][16][2]: m and sum of a piece
     float *part_o;       // [2 * wgs][block_heads][dim]
     float *scores;       // [unit][block_heads][CHUNK], with totals only
+    int sharers;         // workgroups that add to the totals
+    int vec;             // totals may be read and written 16 bytes at a time
 };
 
 // The workgroup whose share a unit is in.  Workgroup w leaves the part of a
@@ -129,63 +137,80 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
     const int quad = lane >> 4, col = lane & 15;
     const int vheads = c.heads * pl.blocks;
 
-    // Units of one (head, block) before each row, in strips of rows for each thread.
-    const int strip = (c.rows + ATTEND_THREADS - 1) / ATTEND_THREADS;
-    const int r0 = tid * strip, r1 = min(r0 + strip, c.rows);
-    int mine = 0;
-    for (int r = r0; r < r1; ++r) mine += (kv_len(a.lens, r, a.max_len) + CHUNK - 1) / CHUNK;
+    // Units of one (head, block) before this workgroup's rows.  Up to 64 rows: lane r
+    // of every wave has row r, and no wave waits for another.  More: strips of rows
+    // for each thread, summed over the workgroup.
+    auto chunks_of = [&](int n) { return (n + CHUNK - 1) / CHUNK; };
+    const bool few = c.rows <= 64;
+    const int strip = few ? 1 : (c.rows + ATTEND_THREADS - 1) / ATTEND_THREADS;
+    const int r0 = few ? lane : tid * strip, r1 = min(r0 + strip, c.rows);
+    int mine = 0, first_len = 0;
+    if (few) {
+        if (r0 < r1) first_len = kv_len(a.lens, r0, a.max_len);
+        mine = chunks_of(first_len);
+    } else {
+        for (int r = r0; r < r1; ++r) mine += chunks_of(kv_len(a.lens, r, a.max_len));
+    }
     int upto = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const int x = __shfl_up(upto, d);
         if (lane >= d) upto += x;
     }
-    if (lane == 63) scan[wave] = upto;
-    __syncthreads();
-    int chunks = 0;
+    int chunks = __builtin_amdgcn_readlane(upto, 63);
+    if (!few) {
+        if (lane == 63) scan[wave] = upto;
+        __syncthreads();
+        chunks = 0;
 #pragma unroll
-    for (int w = 0; w < ATTEND_WAVES; ++w) {
-        if (w < wave) upto += scan[w];
-        chunks += scan[w];
+        for (int w = 0; w < ATTEND_WAVES; ++w) {
+            if (w < wave) upto += scan[w];
+            chunks += scan[w];
+        }
     }
     const int before = upto - mine;
     const int64_t units = (int64_t)chunks * vheads;
     const int shares = (int)min((int64_t)pl.wgs, units);  // none is empty
     const int u0 = (int)blockIdx.x < shares ? (int)(units * blockIdx.x / shares) : 0;
     const int u1 = (int)blockIdx.x < shares ? (int)(units * (blockIdx.x + 1) / shares) : 0;
-    if (blockIdx.x == 0 && pl.before) {
+    if (blockIdx.x == 0 && pl.before && (!few || wave == 0)) {
         int at = before;
         for (int r = r0; r < r1; ++r) {
             pl.before[r] = at;
-            at += (kv_len(a.lens, r, a.max_len) + CHUNK - 1) / CHUNK;
+            if (!few) at += chunks_of(kv_len(a.lens, r, a.max_len));
         }
         if (tid == 0) pl.before[c.rows] = chunks;
     }
     // Rows without a slot: zeros.
     for (int r = blockIdx.x; r < c.rows; r += pl.wgs) {
-        if (kv_len(a.lens, r, a.max_len)) continue;
+        if (few ? __builtin_amdgcn_readlane(first_len, r) : kv_len(a.lens, r, a.max_len)) continue;
         for (int i = tid; i < a.q_heads * DIM / 8; i += ATTEND_THREADS)
             reinterpret_cast<u32x4_kv *>(a.out + (int64_t)r * a.out_ld)[i] = u32x4_kv{0, 0, 0, 0};
     }
     if (u0 >= u1) return;
-    {
-        const int64_t lo = (int64_t)before * vheads, hi = (int64_t)(before + mine) * vheads;
-        if (lo <= u0 && u0 < hi) {
+    int row, row_at, len;
+    const bool here = (int64_t)before * vheads <= u0 && u0 < (int64_t)upto * vheads;
+    if (few) {
+        row = __builtin_ctzll(__ballot(here));
+        row_at = __builtin_amdgcn_readlane(before, row);
+        len = __builtin_amdgcn_readlane(first_len, row);
+    } else {
+        if (here) {
             int at = before, r = r0;
             for (;; ++r) {
-                const int n = (kv_len(a.lens, r, a.max_len) + CHUNK - 1) / CHUNK;
+                const int n = chunks_of(kv_len(a.lens, r, a.max_len));
                 if (u0 < (int64_t)(at + n) * vheads) break;
                 at += n;
             }
             found[0] = r;
             found[1] = at;
         }
+        __syncthreads();
+        row = __builtin_amdgcn_readfirstlane(found[0]);
+        row_at = __builtin_amdgcn_readfirstlane(found[1]);
+        len = __builtin_amdgcn_readfirstlane(kv_len(a.lens, row, a.max_len));
     }
-    __syncthreads();
-    int row = __builtin_amdgcn_readfirstlane(found[0]);
-    int row_at = __builtin_amdgcn_readfirstlane(found[1]);
-    int len = __builtin_amdgcn_readfirstlane(kv_len(a.lens, row, a.max_len));
-    int row_chunks = (len + CHUNK - 1) / CHUNK;
+    int row_chunks = chunks_of(len);
     int vh = (u0 - row_at * vheads) / row_chunks;
 
     for (int u = u0; u < u1;) {
@@ -222,7 +247,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    r.p[h] = slot + 16 * h < len && chunk < c1 ? table[(slot + 16 * h) >> c.page_log2] : -1;
+                    r.p[h] = slot + 16 * h < len && chunk < c1 ? uniform_word(table + ((slot + 16 * h) >> c.page_log2)) : -1;
             }
             return r;
         };
@@ -377,22 +402,23 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
             }
         };
 
-        // Two tiles in turn; page numbers one tile further ahead.
+        // Two tiles in turn.  Page numbers are asked for one tile further ahead, and
+        // before the tile that they do not belong to: loads return in order, and
+        // waiting for them must not mean waiting for that tile.
         {
             T ta, tb;
-            Pages pg = pages_of(c0);
-            load(ta, pg, c0);
-            pg = pages_of(c0 + 1);
+            Pages pa = pages_of(c0), pb = pages_of(c0 + 1);
+            load(ta, pa, c0);
             for (int ch = c0; ch < c1; ch += 2) {
                 if (ch + 1 < c1) {
-                    load(tb, pg, ch + 1);
-                    pg = pages_of(ch + 2);
+                    pa = pages_of(ch + 2);
+                    load(tb, pb, ch + 1);
                 }
                 use(ta, ch);
                 if (ch + 1 < c1) {
                     if (ch + 2 < c1) {
-                        load(ta, pg, ch + 2);
-                        pg = pages_of(ch + 3);
+                        pb = pages_of(ch + 3);
+                        load(ta, pa, ch + 2);
                     }
                     use(tb, ch + 1);
                 }
@@ -481,7 +507,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
                     ++row;
                     len = __builtin_amdgcn_readfirstlane(kv_len(a.lens, row, a.max_len));
                 } while (len == 0);
-                row_chunks = (len + CHUNK - 1) / CHUNK;
+                row_chunks = chunks_of(len);
             }
         }
     }
@@ -588,19 +614,42 @@ __global__ __launch_bounds__(JOIN_THREADS) void kv_join_kernel(KvCache c, KvAtte
             head_inv[tid] = l == 0.f ? 0.f : 1.f / l;
         }
         __syncthreads();
-        for (int i = tid; i < (c1 - c0) * CHUNK; i += JOIN_THREADS) {
-            const int chunk = c0 + i / CHUNK, slot = chunk * CHUNK + i % CHUNK;
+        // Four slots of a thread, 32 threads of a unit.
+        const int64_t base = ((int64_t)row * c.heads + head) * c.cap;
+        const bool vec = pl.vec;
+        for (int i = tid; i < (c1 - c0) * (CHUNK / 4); i += JOIN_THREADS) {
+            const int chunk = c0 + i / (CHUNK / 4), in = i % (CHUNK / 4) * 4, slot = chunk * CHUNK + in;
             if (slot >= n) continue;
-            float w = 0.f;
+            f32x4_kv was = {0.f, 0.f, 0.f, 0.f}, w = {0.f, 0.f, 0.f, 0.f};
+            const bool whole = vec && slot + 4 <= n;
+            if (whole) was = *reinterpret_cast<const f32x4_kv *>(a.acc + base + slot);
+            else
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (slot + e < n) was[e] = a.acc[base + slot + e];
             for (int b = 0; b < pl.blocks; ++b) {
                 const int heads = min(pl.block_heads, pl.group - b * pl.block_heads);
                 const int64_t unit = (int64_t)at * vheads + (int64_t)(head * pl.blocks + b) * chunks + chunk;
-                const float *s = pl.scores + unit * pl.block_heads * CHUNK + i % CHUNK;
-                for (int h = 0; h < heads; ++h)
-                    w += __builtin_amdgcn_exp2f(s[h * CHUNK] - head_m[b * pl.block_heads + h]) * head_inv[b * pl.block_heads + h];
+                const float *s = pl.scores + unit * pl.block_heads * CHUNK + in;
+                const float *hm = head_m + b * pl.block_heads, *hi = head_inv + b * pl.block_heads;
+                for (int h0 = 0; h0 < heads; h0 += 4) {  // four heads' scores in flight
+                    f32x4_kv x[4];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) x[h] = *reinterpret_cast<const f32x4_kv *>(s + min(h0 + h, heads - 1) * CHUNK);
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        if (h0 + h < heads)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) w[e] += __builtin_amdgcn_exp2f(x[h][e] - hm[h0 + h]) * hi[h0 + h];
+                }
             }
-            const int64_t j = ((int64_t)row * c.heads + head) * c.cap + slot;
-            a.acc_out[j] = a.decay * a.acc[j] + w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] += a.decay * was[e];
+            if (whole) *reinterpret_cast<f32x4_kv *>(a.acc_out + base + slot) = w;
+            else
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (slot + e < n) a.acc_out[base + slot + e] = w[e];
         }
         t += c1 - c0;
         if (head == c.heads - 1 && c1 == chunks) ++row;
@@ -618,6 +667,8 @@ static int64_t attend_plan(const KvCache &c, int q_heads, int max_len, bool weig
     if (most > INT32_MAX) return -1;
     // As many workgroups as run at once: two on a CU, one at 256 dims (registers).
     pl->wgs = (int)std::max<int64_t>(1, std::min<int64_t>(most, (int64_t)cu_count * (c.dim > 128 ? 1 : 2)));
+    // Totals: eight units for each step of a workgroup, and a few workgroups for each CU.
+    pl->sharers = weights ? (int)std::max<int64_t>(1, std::min<int64_t>((most + 7) / 8, (int64_t)cu_count * 8)) : 0;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         uint8_t *p = base ? base + at : nullptr;
@@ -652,7 +703,7 @@ static void launch_attend(const KvCache &c, const KvAttend &a, const AttendPlan 
     else hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, false, false>), grid, threads, 0, stream, c, a, pl);
     if (pl.before) {
         const int joins = c.rows * a.q_heads;
-        const dim3 both((unsigned)joins + (pl.scores ? pl.wgs : 0));
+        const dim3 both((unsigned)joins + pl.sharers);
         hipLaunchKernelGGL((kv_join_kernel<DIM>), both, dim3(JOIN_THREADS), 0, stream, c, a, pl, joins);
     }
 }
@@ -660,6 +711,7 @@ static void launch_attend(const KvCache &c, const KvAttend &a, const AttendPlan 
 hipError_t launch_kv_attend(const KvCache &c, const KvAttend &a, int cu_count, hipStream_t stream) {
     AttendPlan pl;
     attend_plan(c, a.q_heads, a.max_len, a.acc != nullptr, cu_count, a.ws, &pl);
+    pl.vec = c.cap % 4 == 0 && (((uintptr_t)a.acc | (uintptr_t)a.acc_out) & 15) == 0;
     switch (c.dim) {
     case 64:
         if (c.fp8) launch_attend<64, true>(c, a, pl, stream); else launch_attend<64, false>(c, a, pl, stream);
