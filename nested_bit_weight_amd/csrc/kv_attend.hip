@@ -243,11 +243,12 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
             const int slot = chunk * CHUNK + wave * TILE;
             if constexpr (SMALL) {
                 const int s = slot + (lane & 31);
-                r.p[0] = s < len && chunk < c1 ? table[s >> c.page_log2] : -1;
+                r.p[0] = table[min(s, len - 1) >> c.page_log2];
+                if (s >= len) r.p[0] = -1;
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    r.p[h] = slot + 16 * h < len && chunk < c1 ? uniform_word(table + ((slot + 16 * h) >> c.page_log2)) : -1;
+                    r.p[h] = uniform_word(table + (min(slot + 16 * h, len - 1) >> c.page_log2));
             }
             return r;
         };
@@ -281,7 +282,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int s = slot + 16 * h;
-                    const bool ok = pg.p[h] >= 0 && pg.p[h] < c.pages;
+                    const bool ok = s < len && (uint32_t)pg.p[h] < (uint32_t)c.pages;
                     const int left = ok ? min(len - s, 16) - quad * 4 : 0;
                     t.there |= (left >= 4 ? 15u : left <= 0 ? 0u : (1u << left) - 1) << (4 * h);
                     const int64_t base = ((((int64_t)(ok ? pg.p[h] : 0) * c.heads + head) << c.page_log2) + (s & mask)) * ROW_BYTES;
@@ -404,24 +405,28 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
 
         // Two tiles in turn.  Page numbers are asked for one tile further ahead, and
         // before the tile that they do not belong to: loads return in order, and
-        // waiting for them must not mean waiting for that tile.
+        // waiting for them must not mean waiting for that tile.  For the same reason
+        // the loop has no load that depends on a condition: how many are in flight
+        // when a tile is used is then known, and only its own are waited for.
         {
             T ta, tb;
             Pages pa = pages_of(c0), pb = pages_of(c0 + 1);
             load(ta, pa, c0);
-            for (int ch = c0; ch < c1; ch += 2) {
-                if (ch + 1 < c1) {
-                    pa = pages_of(ch + 2);
-                    load(tb, pb, ch + 1);
-                }
+            int ch = c0;
+            for (; ch + 2 < c1; ch += 2) {
+                pa = pages_of(ch + 2);
+                load(tb, pb, ch + 1);
                 use(ta, ch);
-                if (ch + 1 < c1) {
-                    if (ch + 2 < c1) {
-                        pb = pages_of(ch + 3);
-                        load(ta, pa, ch + 2);
-                    }
-                    use(tb, ch + 1);
-                }
+                pb = pages_of(ch + 3);
+                load(ta, pa, ch + 2);
+                use(tb, ch + 1);
+            }
+            if (ch + 1 < c1) {
+                load(tb, pb, ch + 1);
+                use(ta, ch);
+                use(tb, ch + 1);
+            } else {
+                use(ta, ch);
             }
         }
 
