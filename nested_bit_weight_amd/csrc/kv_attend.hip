@@ -10,14 +10,12 @@
 // around keeping loads in flight.
 //
 // Work: units of CHUNK = 128 slots of one (row, head) in the order (row, head,
-// chunk).  The launch is as many workgroups as the device holds at once, and
-// workgroup w takes the w-th equal share of all units, whatever the rows'
-// lengths are: one long row is spread over the whole device, many short ones
-// are packed.  The lengths stay on the device; each workgroup finds its share
-// from their running sum.  A run of units within one (row, head) is a piece;
-// a (row, head) that lies in one share is finished there, others leave their
-// parts (m, sum, o) in the workspace, which a second launch joins in a fixed
-// order.
+// chunk), divided among as many workgroups as the device holds at once, whatever
+// the rows' lengths are: one long row is spread over the whole device, many short
+// ones are packed.  The lengths stay on the device; each workgroup finds its units
+// from their running sum.  A run of units within one (row, head) is a piece; a
+// (row, head) that is one piece is finished there, others leave their parts (m,
+// sum, o) in the workspace, which a second launch joins in a fixed order.
 //
 // A piece: wave w takes the 32-slot tile w of each unit, everything in its
 // registers, with the next tile's keys and values loading while this one's are
@@ -66,24 +64,44 @@ __device__ __forceinline__ int32_t uniform_word(const int32_t *p) {
 
 // The launch's division of work and its scratch, the same for both kernels.
 struct AttendPlan {
-    int wgs;             // workgroups that share the units
+    int wgs;             // workgroups of the first launch
     int group;           // query heads of a head
     int blocks;          // blocks of up to 16 query heads that a head's are taken in
     int block_heads;     // query heads of a block (the last may have fewer)
+    int undivided;       // every (row, head, block) has a workgroup of its own
     int32_t *before;     // [rows + 1] units of one (head, block) before each row
+    int32_t *pieces;     // [rows + 1] pieces of one (head, block) before each row, then their units
     float *whole;        // [rows][heads * blocks][16][2]: m and sum where one workgroup had it all
     float *part_ml;      // [2 * wgs][16][2]: m and sum of a piece
     float *part_o;       // [2 * wgs][block_heads][dim]
-    float *scores;       // [unit][block_heads][CHUNK], with totals only
+    float *scores;       // [unit][wave][half][quarter][block_heads][4], with totals only
     int sharers;         // workgroups that add to the totals
     int vec;             // totals may be read and written 16 bytes at a time
 };
 
-// The workgroup whose share a unit is in.  Workgroup w leaves the part of a
-// (row, head) that began in an earlier share at place 2 w, and of one that
-// begins in its own and goes on past it at 2 w + 1.
+// The workgroup whose share a unit is in.
 __device__ __forceinline__ int owner_of(int64_t unit, int64_t units, int shares) {
     return (int)(((unit + 1) * shares - 1) / units);
+}
+
+// The parts of one (row, head, block): n of them, part i at place(i).  With equal
+// shares workgroup w leaves what began in an earlier share at place 2 w, and what
+// begins in its own and goes on past it at 2 w + 1; pieces of equal length are at
+// twice their number.
+struct Parts {
+    int n, first, odd;
+    __device__ __forceinline__ int place(int i) const { return 2 * (first + i) + (i == 0 ? odd : 0); }
+};
+__device__ __forceinline__ Parts parts_of(const KvCache &c, const AttendPlan &pl, int row, int vh, int at, int chunks) {
+    const int vheads = c.heads * pl.blocks, k = pl.pieces[c.rows + 1];
+    if (k) {
+        const int n = (chunks + k - 1) / k;
+        return {n, pl.pieces[row] * vheads + vh * n, 0};
+    }
+    const int64_t units = (int64_t)pl.before[c.rows] * vheads, seg0 = (int64_t)at * vheads + (int64_t)vh * chunks;
+    const int shares = (int)min((int64_t)pl.wgs, units);
+    const int w0 = owner_of(seg0, units, shares);
+    return {owner_of(seg0 + chunks - 1, units, shares) - w0 + 1, w0, 1};
 }
 
 // One wave's tile: keys and values as loaded, and which slots count.
@@ -98,16 +116,22 @@ struct Tile {
     uint32_t there;  // bit 4 h + i: slot 4 (lane / 16) + i of half h
 };
 
-template <int W>
+template <bool NT, class V>
+__device__ __forceinline__ V load_as(const uint8_t *p) {
+    if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const V *>(p));
+    else return *reinterpret_cast<const V *>(p);
+}
+
+template <bool NT, int W>
 __device__ __forceinline__ void load_words(uint32_t *out, const uint8_t *p) {
     if constexpr (W == 4) {
-        const u32x4_kv x = *reinterpret_cast<const u32x4_kv *>(p);
+        const u32x4_kv x = load_as<NT, u32x4_kv>(p);
         out[0] = x[0], out[1] = x[1], out[2] = x[2], out[3] = x[3];
     } else if constexpr (W == 2) {
-        const u32x2_kv x = *reinterpret_cast<const u32x2_kv *>(p);
+        const u32x2_kv x = load_as<NT, u32x2_kv>(p);
         out[0] = x[0], out[1] = x[1];
     } else {
-        out[0] = *reinterpret_cast<const uint32_t *>(p);
+        out[0] = load_as<NT, uint32_t>(p);
     }
 }
 
@@ -122,7 +146,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, p);
 }
 
-template <int DIM, bool FP8, bool PACK, bool SMALL>
+template <int DIM, bool FP8, bool PACK, bool SMALL, bool NT, bool WEIGHTS>
 __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_kernel(KvCache c, KvAttend a, AttendPlan pl) {
     using T = Tile<DIM, FP8>;
     constexpr int HR = PACK ? 8 : 16;                 // heads a workgroup holds
@@ -137,86 +161,137 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
     const int quad = lane >> 4, col = lane & 15;
     const int vheads = c.heads * pl.blocks;
 
-    // Units of one (head, block) before this workgroup's rows.  Up to 64 rows: lane r
-    // of every wave has row r, and no wave waits for another.  More: strips of rows
-    // for each thread, summed over the workgroup.
     auto chunks_of = [&](int n) { return (n + CHUNK - 1) / CHUNK; };
-    const bool few = c.rows <= 64;
-    const int strip = few ? 1 : (c.rows + ATTEND_THREADS - 1) / ATTEND_THREADS;
-    const int r0 = few ? lane : tid * strip, r1 = min(r0 + strip, c.rows);
-    int mine = 0, first_len = 0;
-    if (few) {
-        if (r0 < r1) first_len = kv_len(a.lens, r0, a.max_len);
-        mine = chunks_of(first_len);
-    } else {
-        for (int r = r0; r < r1; ++r) mine += chunks_of(kv_len(a.lens, r, a.max_len));
-    }
-    int upto = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int x = __shfl_up(upto, d);
-        if (lane >= d) upto += x;
-    }
-    int chunks = __builtin_amdgcn_readlane(upto, 63);
-    if (!few) {
-        if (lane == 63) scan[wave] = upto;
-        __syncthreads();
-        chunks = 0;
-#pragma unroll
-        for (int w = 0; w < ATTEND_WAVES; ++w) {
-            if (w < wave) upto += scan[w];
-            chunks += scan[w];
-        }
-    }
-    const int before = upto - mine;
-    const int64_t units = (int64_t)chunks * vheads;
-    const int shares = (int)min((int64_t)pl.wgs, units);  // none is empty
-    const int u0 = (int)blockIdx.x < shares ? (int)(units * blockIdx.x / shares) : 0;
-    const int u1 = (int)blockIdx.x < shares ? (int)(units * (blockIdx.x + 1) / shares) : 0;
-    if (blockIdx.x == 0 && pl.before && (!few || wave == 0)) {
-        int at = before;
-        for (int r = r0; r < r1; ++r) {
-            pl.before[r] = at;
-            if (!few) at += chunks_of(kv_len(a.lens, r, a.max_len));
-        }
-        if (tid == 0) pl.before[c.rows] = chunks;
-    }
-    // Rows without a slot: zeros.
-    for (int r = blockIdx.x; r < c.rows; r += pl.wgs) {
-        if (few ? __builtin_amdgcn_readlane(first_len, r) : kv_len(a.lens, r, a.max_len)) continue;
-        for (int i = tid; i < a.q_heads * DIM / 8; i += ATTEND_THREADS)
-            reinterpret_cast<u32x4_kv *>(a.out + (int64_t)r * a.out_ld)[i] = u32x4_kv{0, 0, 0, 0};
-    }
-    if (u0 >= u1) return;
-    int row, row_at, len;
-    const bool here = (int64_t)before * vheads <= u0 && u0 < (int64_t)upto * vheads;
-    if (few) {
-        row = __builtin_ctzll(__ballot(here));
-        row_at = __builtin_amdgcn_readlane(before, row);
-        len = __builtin_amdgcn_readlane(first_len, row);
-    } else {
-        if (here) {
-            int at = before, r = r0;
-            for (;; ++r) {
-                const int n = chunks_of(kv_len(a.lens, r, a.max_len));
-                if (u0 < (int64_t)(at + n) * vheads) break;
-                at += n;
-            }
-            found[0] = r;
-            found[1] = at;
-        }
-        __syncthreads();
-        row = __builtin_amdgcn_readfirstlane(found[0]);
-        row_at = __builtin_amdgcn_readfirstlane(found[1]);
-        len = __builtin_amdgcn_readfirstlane(kv_len(a.lens, row, a.max_len));
-    }
-    int row_chunks = chunks_of(len);
-    int vh = (u0 - row_at * vheads) / row_chunks;
+    auto zeros = [&](int row, int from, int to) {  // query heads from .. to - 1 of a row without a slot
+        for (int i = from * DIM / 8 + tid; i < to * DIM / 8; i += ATTEND_THREADS)
+            reinterpret_cast<u32x4_kv *>(a.out + (int64_t)row * a.out_ld)[i] = u32x4_kv{0, 0, 0, 0};
+    };
 
-    for (int u = u0; u < u1;) {
-        // The piece: chunks [c0, c1) of (row, vh).
-        const int seg0 = row_at * vheads + vh * row_chunks, seg1 = seg0 + row_chunks;
-        const int c0 = u - seg0, c1 = min(u1, seg1) - seg0;
+    // This workgroup's first piece, and with equal shares its units [u, u1).
+    int row, row_at = 0, len, row_chunks, vh, c0, c1, part = 0, u = 0, u1 = 0;
+    if (pl.undivided) {
+        row = blockIdx.x / vheads;
+        vh = blockIdx.x % vheads;
+        len = __builtin_amdgcn_readfirstlane(kv_len(a.lens, row, a.max_len));
+        row_chunks = chunks_of(len);
+        c0 = 0;
+        c1 = row_chunks;
+        if (len == 0) {
+            const int from = vh / pl.blocks * pl.group + vh % pl.blocks * pl.block_heads;
+            zeros(row, from, from + min(pl.block_heads, pl.group - vh % pl.blocks * pl.block_heads));
+            return;
+        }
+    } else {
+        // Units of one (head, block) before this workgroup's rows.  Up to 64 rows: lane
+        // r of every wave has row r, and no wave waits for another.  More: strips of
+        // rows for each thread, summed over the workgroup.
+        const bool few = c.rows <= 64;
+        const int strip = few ? 1 : (c.rows + ATTEND_THREADS - 1) / ATTEND_THREADS;
+        const int r0 = few ? lane : tid * strip, r1 = min(r0 + strip, c.rows);
+        int mine = 0, first_len = 0;
+        if (few) {
+            if (r0 < r1) first_len = kv_len(a.lens, r0, a.max_len);
+            mine = chunks_of(first_len);
+        } else {
+            for (int r = r0; r < r1; ++r) mine += chunks_of(kv_len(a.lens, r, a.max_len));
+        }
+        auto running = [&](int x) {  // the sum over this lane and those before it
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int y = __shfl_up(x, d);
+                if (lane >= d) x += y;
+            }
+            return x;
+        };
+        int upto = running(mine), chunks = __builtin_amdgcn_readlane(upto, 63);
+        if (!few) {
+            if (lane == 63) scan[wave] = upto;
+            __syncthreads();
+            chunks = 0;
+#pragma unroll
+            for (int w = 0; w < ATTEND_WAVES; ++w) {
+                if (w < wave) upto += scan[w];
+                chunks += scan[w];
+            }
+        }
+        const int before = upto - mine;
+        const int64_t units = (int64_t)chunks * vheads;
+
+        // Pieces of k units each, one for a workgroup, if k need be little more than an
+        // equal share: a share that runs over from one (row, head) into the next costs
+        // its workgroup a second start, about as long as a unit takes.
+        int k = 0, pieces = 0;
+        if (few && units) {
+            const int share = (int)((units + pl.wgs - 1) / pl.wgs);
+            for (int t = share; t <= share + 1 && !k; ++t) {
+                pieces = running((mine + t - 1) / t);
+                if ((int64_t)__builtin_amdgcn_readlane(pieces, 63) * vheads <= pl.wgs) k = t;
+            }
+        }
+        if (blockIdx.x == 0 && (!few || wave == 0)) {
+            int at = before;
+            for (int r = r0; r < r1; ++r) {
+                pl.before[r] = at;
+                if (few) pl.pieces[r] = k ? pieces - (mine + k - 1) / k : 0;
+                else at += chunks_of(kv_len(a.lens, r, a.max_len));
+            }
+            if (tid == 0) {
+                pl.before[c.rows] = chunks;
+                pl.pieces[c.rows + 1] = k;
+            }
+        }
+        for (int r = blockIdx.x; r < c.rows; r += pl.wgs)
+            if ((few ? __builtin_amdgcn_readlane(first_len, r) : kv_len(a.lens, r, a.max_len)) == 0) zeros(r, 0, a.q_heads);
+        if (k) {
+            const int mine_k = (mine + k - 1) / k;
+            const unsigned long long at = __ballot((int)blockIdx.x < pieces * vheads);
+            if (!at) return;
+            row = __builtin_ctzll(at);
+            row_at = __builtin_amdgcn_readlane(before, row);
+            len = __builtin_amdgcn_readlane(first_len, row);
+            row_chunks = chunks_of(len);
+            const int n = __builtin_amdgcn_readlane(mine_k, row);
+            const int in = (int)blockIdx.x - (__builtin_amdgcn_readlane(pieces, row) - n) * vheads;
+            vh = in / n;
+            c0 = in % n * k;
+            c1 = min(c0 + k, row_chunks);
+            part = 2 * blockIdx.x;
+        } else {
+            const int shares = (int)min((int64_t)pl.wgs, units);  // none is empty
+            if ((int)blockIdx.x >= shares) return;
+            u = (int)(units * blockIdx.x / shares);
+            u1 = (int)(units * (blockIdx.x + 1) / shares);
+            const bool here = (int64_t)before * vheads <= u && u < (int64_t)upto * vheads;
+            if (few) {
+                row = __builtin_ctzll(__ballot(here));
+                row_at = __builtin_amdgcn_readlane(before, row);
+                len = __builtin_amdgcn_readlane(first_len, row);
+            } else {
+                if (here) {
+                    int at = before, r = r0;
+                    for (;; ++r) {
+                        const int n = chunks_of(kv_len(a.lens, r, a.max_len));
+                        if (u < (int64_t)(at + n) * vheads) break;
+                        at += n;
+                    }
+                    found[0] = r;
+                    found[1] = at;
+                }
+                __syncthreads();
+                row = __builtin_amdgcn_readfirstlane(found[0]);
+                row_at = __builtin_amdgcn_readfirstlane(found[1]);
+                len = __builtin_amdgcn_readfirstlane(kv_len(a.lens, row, a.max_len));
+            }
+            row_chunks = chunks_of(len);
+            vh = (u - row_at * vheads) / row_chunks;
+            c0 = u - row_at * vheads - vh * row_chunks;
+            c1 = min(row_chunks, c0 + u1 - u);
+            part = 2 * blockIdx.x + (c0 == 0);
+        }
+    }
+
+    for (;;) {  // the piece: chunks [c0, c1) of (row, vh)
+        const int64_t seg0 = (int64_t)row_at * vheads + vh * row_chunks;  // its first unit
         const int head = vh / pl.blocks, block = vh % pl.blocks;
         const int g0 = block * pl.block_heads, heads = min(pl.block_heads, pl.group - g0);
         const int32_t *table = c.table + (int64_t)row * c.table_ld;
@@ -269,13 +344,13 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
                     bool ok;
                     const uint8_t *p = c.k + place(16 * h + col, ok) + quad * 16;
 #pragma unroll
-                    for (int f = 0; f < T::KV4; ++f) t.k[h][f] = *reinterpret_cast<const u32x4_kv *>(p + f * 64);
+                    for (int f = 0; f < T::KV4; ++f) t.k[h][f] = load_as<NT, u32x4_kv>(p + f * 64);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint8_t *q = c.v + place(16 * h + quad * 4 + i, ok) + col * T::VW * 4;
                         t.there |= (uint32_t)ok << (4 * h + i);
 #pragma unroll
-                        for (int n = 0; n < T::NC; ++n) load_words<T::VW>(t.v[h][i][n], q + n * (ROW_BYTES / T::NC));
+                        for (int n = 0; n < T::NC; ++n) load_words<NT, T::VW>(t.v[h][i][n], q + n * (ROW_BYTES / T::NC));
                     }
                 }
             } else {
@@ -289,12 +364,12 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
                     const uint8_t *kb = c.k + base, *vb = c.v + base;
                     const uint32_t ko = col * ROW_BYTES + quad * 16, vo = quad * 4 * ROW_BYTES + col * T::VW * 4;
 #pragma unroll
-                    for (int f = 0; f < T::KV4; ++f) t.k[h][f] = *reinterpret_cast<const u32x4_kv *>(kb + ko + f * 64);
+                    for (int f = 0; f < T::KV4; ++f) t.k[h][f] = load_as<NT, u32x4_kv>(kb + ko + f * 64);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int n = 0; n < T::NC; ++n)
-                            load_words<T::VW>(t.v[h][i][n], vb + vo + i * ROW_BYTES + n * (ROW_BYTES / T::NC));
+                            load_words<NT, T::VW>(t.v[h][i][n], vb + vo + i * ROW_BYTES + n * (ROW_BYTES / T::NC));
                 }
             }
         };
@@ -330,10 +405,19 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = t.there >> i & 1 ? x[i] : NEG_INF;
             }
-            if (pl.scores && col < heads) {
-                float *dst = pl.scores + ((int64_t)(seg0 + chunk) * pl.block_heads + col) * CHUNK + wave * TILE + quad * 4;
-                *reinterpret_cast<f32x4_kv *>(dst) = f32x4_kv{x[0], x[1], x[2], x[3]};
-                *reinterpret_cast<f32x4_kv *>(dst + 16) = f32x4_kv{x[4], x[5], x[6], x[7]};
+            if constexpr (WEIGHTS) {
+                // Stores through a descriptor of the tile's scores, which drops those of
+                // the lanes without a head: a branch around them would hide from the
+                // compiler how many operations follow a load, and every tile would wait
+                // for the last one's stores.
+                const int bytes = 8 * 16 * pl.block_heads;
+                auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+                    pl.scores + ((seg0 + chunk) * ATTEND_WAVES + wave) * (bytes / 4), 0, bytes, 0x00027000);
+                const int at = col < heads ? (quad * pl.block_heads + col) * 16 : bytes;
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    __builtin_bit_cast(u32x4_kv, f32x4_kv{x[0], x[1], x[2], x[3]}), rsrc, at, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    __builtin_bit_cast(u32x4_kv, f32x4_kv{x[4], x[5], x[6], x[7]}), rsrc, at + 64 * pl.block_heads, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
@@ -439,7 +523,6 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
         }
         __syncthreads();
         const bool whole = c0 == 0 && c1 == row_chunks;
-        const int part = 2 * blockIdx.x + (c0 > 0 ? 0 : 1);
         auto merged = [&](int h, float &top, float &total) {
             top = NEG_INF;
             total = 0.f;
@@ -466,7 +549,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
             if (!whole) {
                 pl.part_ml[(part * 16 + tid) * 2] = top;
                 pl.part_ml[(part * 16 + tid) * 2 + 1] = total;
-            } else if (pl.scores) {
+            } else if (WEIGHTS) {
                 float *w = pl.whole + (((int64_t)row * vheads + vh) * 16 + tid) * 2;
                 w[0] = top;
                 w[1] = total;
@@ -502,51 +585,49 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
                 }
             }
         }
-        u = seg0 + c1;
-        if (u < u1) {  // the next (row, head): wave_ml and wave_o are free once all have read them
-            __syncthreads();
-            if (++vh == vheads) {
-                vh = 0;
-                row_at += row_chunks;
-                do {
-                    ++row;
-                    len = __builtin_amdgcn_readfirstlane(kv_len(a.lens, row, a.max_len));
-                } while (len == 0);
-                row_chunks = chunks_of(len);
-            }
+        u += c1 - c0;
+        if (u >= u1) return;  // the only piece, or the share's last
+        __syncthreads();      // wave_ml and wave_o are free
+        if (++vh == vheads) {
+            vh = 0;
+            row_at += row_chunks;
+            do {
+                ++row;
+                len = __builtin_amdgcn_readfirstlane(kv_len(a.lens, row, a.max_len));
+            } while (len == 0);
+            row_chunks = chunks_of(len);
         }
+        c0 = 0;
+        c1 = min(row_chunks, u1 - u);
+        part = 2 * blockIdx.x + 1;
     }
 }
 
 constexpr int JOIN_THREADS = 256;
 
-// The second launch.  Workgroups 0 .. rows * q_heads - 1 join one query head's
-// parts; those after them add the weights to the totals, each for an equal
-// share of the units of (row, head, chunk).
+// The second launch.  The first `sharers` workgroups add the weights to the
+// totals, each for an equal share of the units of (row, head, chunk); the rows *
+// q_heads after them join one query head's parts each.
 template <int DIM>
-__global__ __launch_bounds__(JOIN_THREADS) void kv_join_kernel(KvCache c, KvAttend a, AttendPlan pl, int joins) {
+__global__ __launch_bounds__(JOIN_THREADS) void kv_join_kernel(KvCache c, KvAttend a, AttendPlan pl) {
     constexpr int LANES = DIM / 4, SLICES = JOIN_THREADS / LANES;
     __shared__ __align__(16) float slice_o[SLICES][DIM];
     __shared__ float slice_l[SLICES];
     __shared__ float head_m[256], head_inv[256];
     const int tid = threadIdx.x, vheads = c.heads * pl.blocks;
-    const int64_t units = (int64_t)pl.before[c.rows] * vheads;
-    if (units == 0) return;
-    const int shares = (int)min((int64_t)pl.wgs, units);
 
-    if ((int)blockIdx.x < joins) {
-        const int row = blockIdx.x / a.q_heads, qh = blockIdx.x % a.q_heads;
+    if ((int)blockIdx.x >= pl.sharers) {
+        const int which = blockIdx.x - pl.sharers, row = which / a.q_heads, qh = which % a.q_heads;
         const int head = qh / pl.group, block = qh % pl.group / pl.block_heads, h = qh % pl.group % pl.block_heads;
         const int at = pl.before[row], chunks = pl.before[row + 1] - at;
         if (chunks == 0) return;
-        const int64_t seg0 = (int64_t)at * vheads + (int64_t)(head * pl.blocks + block) * chunks;
-        const int w0 = owner_of(seg0, units, shares), w1 = owner_of(seg0 + chunks - 1, units, shares);
-        if (w0 == w1) return;  // written already
+        const Parts parts = parts_of(c, pl, row, head * pl.blocks + block, at, chunks);
+        if (parts.n == 1) return;  // written already
         const int d = tid % LANES * 4, slice = tid / LANES;
         float m = NEG_INF, l = 0.f;
         f32x4_kv o = {0.f, 0.f, 0.f, 0.f};
-        for (int w = w0 + slice; w <= w1; w += SLICES) {
-            const int part = w == w0 ? 2 * w + 1 : 2 * w;
+        for (int i = slice; i < parts.n; i += SLICES) {
+            const int part = parts.place(i);
             const float pm = pl.part_ml[(part * 16 + h) * 2], ps = pl.part_ml[(part * 16 + h) * 2 + 1];
             const f32x4_kv x = *reinterpret_cast<const f32x4_kv *>(pl.part_o + ((int64_t)part * pl.block_heads + h) * DIM + d);
             const float top = fmaxf(m, pm);
@@ -579,9 +660,8 @@ __global__ __launch_bounds__(JOIN_THREADS) void kv_join_kernel(KvCache c, KvAtte
         return;
     }
 
-    const int index = blockIdx.x - joins, sharers = gridDim.x - joins;
     const int64_t all = (int64_t)pl.before[c.rows] * c.heads;
-    const int64_t t0 = all * index / sharers, t1 = all * (index + 1) / sharers;
+    const int64_t t0 = all * blockIdx.x / pl.sharers, t1 = all * (blockIdx.x + 1) / pl.sharers;
     if (t0 >= t1) return;
     int row = 0;
     for (int r0 = 0; r0 < c.rows; r0 += JOIN_THREADS) {
@@ -601,17 +681,16 @@ __global__ __launch_bounds__(JOIN_THREADS) void kv_join_kernel(KvCache c, KvAtte
         __syncthreads();
         if (tid < pl.group) {  // each query head's m and 1 / sum over all of its parts
             const int block = tid / pl.block_heads, h = tid % pl.block_heads;
-            const int64_t seg0 = (int64_t)at * vheads + (int64_t)(head * pl.blocks + block) * chunks;
-            const int w0 = owner_of(seg0, units, shares), w1 = owner_of(seg0 + chunks - 1, units, shares);
+            const Parts parts = parts_of(c, pl, row, head * pl.blocks + block, at, chunks);
             float m = NEG_INF, l = 0.f;
-            if (w0 == w1) {
+            if (parts.n == 1) {
                 const float *w = pl.whole + (((int64_t)row * vheads + head * pl.blocks + block) * 16 + h) * 2;
                 m = w[0];
                 l = w[1];
             } else {
-                for (int w = w0; w <= w1; ++w) m = fmaxf(m, pl.part_ml[((w == w0 ? 2 * w + 1 : 2 * w) * 16 + h) * 2]);
-                for (int w = w0; w <= w1; ++w) {
-                    const float *p = pl.part_ml + ((w == w0 ? 2 * w + 1 : 2 * w) * 16 + h) * 2;
+                for (int i = 0; i < parts.n; ++i) m = fmaxf(m, pl.part_ml[(parts.place(i) * 16 + h) * 2]);
+                for (int i = 0; i < parts.n; ++i) {
+                    const float *p = pl.part_ml + (parts.place(i) * 16 + h) * 2;
                     l += p[1] * (p[0] == m ? 1.f : exp2f(p[0] - m));
                 }
             }
@@ -623,7 +702,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void kv_join_kernel(KvCache c, KvAtte
         const int64_t base = ((int64_t)row * c.heads + head) * c.cap;
         const bool vec = pl.vec;
         for (int i = tid; i < (c1 - c0) * (CHUNK / 4); i += JOIN_THREADS) {
-            const int chunk = c0 + i / (CHUNK / 4), in = i % (CHUNK / 4) * 4, slot = chunk * CHUNK + in;
+            const int chunk = c0 + i / (CHUNK / 4), in = i % (CHUNK / 4), slot = chunk * CHUNK + in * 4;
             if (slot >= n) continue;
             f32x4_kv was = {0.f, 0.f, 0.f, 0.f}, w = {0.f, 0.f, 0.f, 0.f};
             const bool whole = vec && slot + 4 <= n;
@@ -635,12 +714,12 @@ __global__ __launch_bounds__(JOIN_THREADS) void kv_join_kernel(KvCache c, KvAtte
             for (int b = 0; b < pl.blocks; ++b) {
                 const int heads = min(pl.block_heads, pl.group - b * pl.block_heads);
                 const int64_t unit = (int64_t)at * vheads + (int64_t)(head * pl.blocks + b) * chunks + chunk;
-                const float *s = pl.scores + unit * pl.block_heads * CHUNK + in;
+                const float *s = pl.scores + (unit * (CHUNK / 4) + in) * 4 * pl.block_heads;
                 const float *hm = head_m + b * pl.block_heads, *hi = head_inv + b * pl.block_heads;
                 for (int h0 = 0; h0 < heads; h0 += 4) {  // four heads' scores in flight
                     f32x4_kv x[4];
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) x[h] = *reinterpret_cast<const f32x4_kv *>(s + min(h0 + h, heads - 1) * CHUNK);
+                    for (int h = 0; h < 4; ++h) x[h] = *reinterpret_cast<const f32x4_kv *>(s + min(h0 + h, heads - 1) * 4);
 #pragma unroll
                     for (int h = 0; h < 4; ++h)
                         if (h0 + h < heads)
@@ -671,7 +750,11 @@ static int64_t attend_plan(const KvCache &c, int q_heads, int max_len, bool weig
     const int64_t most = c.rows * vheads * chunks;
     if (most > INT32_MAX) return -1;
     // As many workgroups as run at once: two on a CU, one at 256 dims (registers).
+    // Rows of up to four units are not divided: a workgroup's steps 2 to 4 take about
+    // as long as the second launch that joins parts.
+    pl->undivided = chunks <= 4 && !weights;
     pl->wgs = (int)std::max<int64_t>(1, std::min<int64_t>(most, (int64_t)cu_count * (c.dim > 128 ? 1 : 2)));
+    if (pl->undivided) pl->wgs = (int)(c.rows * vheads);
     // Totals: eight units for each step of a workgroup, and a few workgroups for each CU.
     pl->sharers = weights ? (int)std::max<int64_t>(1, std::min<int64_t>((most + 7) / 8, (int64_t)cu_count * 8)) : 0;
     int64_t at = 0;
@@ -682,8 +765,10 @@ static int64_t attend_plan(const KvCache &c, int q_heads, int max_len, bool weig
     };
     pl->before = nullptr;
     pl->whole = pl->part_ml = pl->part_o = pl->scores = nullptr;
-    if (chunks <= 1 && !weights) return 0;  // no (row, head) is divided
+    pl->pieces = nullptr;
+    if (pl->undivided) return 0;
     pl->before = (int32_t *)take((c.rows + 1) * 4);
+    pl->pieces = (int32_t *)take((c.rows + 2) * 4);
     pl->part_ml = (float *)take((int64_t)pl->wgs * 2 * 16 * 2 * 4);
     pl->part_o = (float *)take((int64_t)pl->wgs * 2 * pl->block_heads * c.dim * 4);
     if (weights) {
@@ -698,19 +783,29 @@ int64_t kv_attend_workspace_bytes(const KvCache &c, int q_heads, int max_len, bo
     return attend_plan(c, q_heads, max_len, weights, cu_count, nullptr, &pl);
 }
 
+template <int DIM, bool FP8, bool PACK, bool SMALL>
+static void launch_attend(const KvCache &c, const KvAttend &a, const AttendPlan &pl, bool once, hipStream_t stream) {
+    const dim3 grid(pl.wgs), threads(ATTEND_THREADS);
+    if (once && pl.scores) hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, PACK, SMALL, true, true>), grid, threads, 0, stream, c, a, pl);
+    else if (once) hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, PACK, SMALL, true, false>), grid, threads, 0, stream, c, a, pl);
+    else if (pl.scores) hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, PACK, SMALL, false, true>), grid, threads, 0, stream, c, a, pl);
+    else hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, PACK, SMALL, false, false>), grid, threads, 0, stream, c, a, pl);
+    if (!pl.undivided)
+        hipLaunchKernelGGL((kv_join_kernel<DIM>), dim3((unsigned)(c.rows * a.q_heads + pl.sharers)), dim3(JOIN_THREADS), 0,
+                           stream, c, a, pl);
+}
+
 template <int DIM, bool FP8>
 static void launch_attend(const KvCache &c, const KvAttend &a, const AttendPlan &pl, hipStream_t stream) {
-    const dim3 grid(pl.wgs), threads(ATTEND_THREADS);
+    // Loads that say their data is used once, if the rows may be too long for the
+    // last-level cache (256 MB) to hold them until the next call: 537 MB take 90 us
+    // with them and 102 without; 44 MB, called again, 22 and 21.
+    const bool once = (int64_t)c.rows * c.heads * a.max_len * c.dim * (c.fp8 ? 2 : 4) > ((int64_t)256 << 20);
     const bool pack = pl.block_heads <= 8, small = c.page_log2 < 4;
-    if (pack && small) hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, true, true>), grid, threads, 0, stream, c, a, pl);
-    else if (pack) hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, true, false>), grid, threads, 0, stream, c, a, pl);
-    else if (small) hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, false, true>), grid, threads, 0, stream, c, a, pl);
-    else hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, false, false>), grid, threads, 0, stream, c, a, pl);
-    if (pl.before) {
-        const int joins = c.rows * a.q_heads;
-        const dim3 both((unsigned)joins + pl.sharers);
-        hipLaunchKernelGGL((kv_join_kernel<DIM>), both, dim3(JOIN_THREADS), 0, stream, c, a, pl, joins);
-    }
+    if (pack && small) launch_attend<DIM, FP8, true, true>(c, a, pl, once, stream);
+    else if (pack) launch_attend<DIM, FP8, true, false>(c, a, pl, once, stream);
+    else if (small) launch_attend<DIM, FP8, false, true>(c, a, pl, once, stream);
+    else launch_attend<DIM, FP8, false, false>(c, a, pl, once, stream);
 }
 
 hipError_t launch_kv_attend(const KvCache &c, const KvAttend &a, int cu_count, hipStream_t stream) {
