@@ -51,6 +51,7 @@ constexpr int ATTEND_WAVES = 4;
 constexpr int ATTEND_THREADS = 64 * ATTEND_WAVES;
 constexpr int TILE = 32;                     // slots of one wave's step
 constexpr int CHUNK = TILE * ATTEND_WAVES;   // slots of a unit
+constexpr int HELD_SCORES = 3072;            // scores a wave holds back, 6 tiles' or more
 constexpr float RAISE = 8.f;                 // how far a score may pass the running maximum
 constexpr float TINY = 1.17549435e-38f;      // the smallest normal number, fp32's and bf16's
 
@@ -156,7 +157,12 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
     __shared__ int scan[ATTEND_WAVES];
     __shared__ int found[2];
     __shared__ float wave_ml[ATTEND_WAVES][HR][2];
-    __shared__ __align__(16) float wave_o[ATTEND_WAVES][HR][COLS];
+    // The waves' results at the end of a piece; before that, with totals, the scores
+    // of each wave's last tiles.
+    constexpr int POOL = WEIGHTS ? HELD_SCORES : HR * COLS;  // a wave's
+    static_assert(HELD_SCORES >= 16 * 128, "the results fit");
+    __shared__ __align__(16) float pool[ATTEND_WAVES * POOL];
+    auto wave_o = [&](int w, int h, int d) -> float & { return pool[(w * HR + h) * COLS + d]; };
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int quad = lane >> 4, col = lane & 15;
     const int vheads = c.heads * pl.blocks;
@@ -381,6 +387,23 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
             for (int t = 0; t < T::DPL; ++t) o[n][t] = f32x4_kv{0.f, 0.f, 0.f, 0.f};
         float m = NEG_INF, sum = 0.f;
 
+        // Scores wait in LDS and leave a few tiles at a time: a store counts among the
+        // operations in flight, in order, so that with one in every tile each tile
+        // waited for the last one's to reach memory (64 rows, 1.2 GB: 250 us, and 200
+        // without the stores).
+        float *scores = pool + wave * POOL;
+        const int most_held = HELD_SCORES / (TILE * pl.block_heads);
+        int held = 0;
+        auto put_scores = [&](int chunk) {  // up to this chunk's
+            const int each = TILE / 4 * pl.block_heads;  // 16-byte pieces of a tile
+            float *dst = pl.scores + ((seg0 + chunk - held + 1) * ATTEND_WAVES + wave) * each * 4;
+            __builtin_amdgcn_wave_barrier();
+            for (int i = lane; i < held * each; i += 64)
+                *reinterpret_cast<f32x4_kv *>(dst + ((int64_t)(i / each) * ATTEND_WAVES * each + i % each) * 4) =
+                    *reinterpret_cast<const f32x4_kv *>(scores + i * 4);
+            __builtin_amdgcn_wave_barrier();
+            held = 0;
+        };
         auto use = [&](T &t, int chunk) {
             f32x4_kv s[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
@@ -406,18 +429,12 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
                 for (int i = 0; i < 8; ++i) x[i] = t.there >> i & 1 ? x[i] : NEG_INF;
             }
             if constexpr (WEIGHTS) {
-                // Stores through a descriptor of the tile's scores, which drops those of
-                // the lanes without a head: a branch around them would hide from the
-                // compiler how many operations follow a load, and every tile would wait
-                // for the last one's stores.
-                const int bytes = 8 * 16 * pl.block_heads;
-                auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
-                    pl.scores + ((seg0 + chunk) * ATTEND_WAVES + wave) * (bytes / 4), 0, bytes, 0x00027000);
-                const int at = col < heads ? (quad * pl.block_heads + col) * 16 : bytes;
-                __builtin_amdgcn_raw_buffer_store_b128(
-                    __builtin_bit_cast(u32x4_kv, f32x4_kv{x[0], x[1], x[2], x[3]}), rsrc, at, 0, 0);
-                __builtin_amdgcn_raw_buffer_store_b128(
-                    __builtin_bit_cast(u32x4_kv, f32x4_kv{x[4], x[5], x[6], x[7]}), rsrc, at + 64 * pl.block_heads, 0, 0);
+                float *dst = scores + held * TILE * pl.block_heads + (quad * pl.block_heads + col) * 4;
+                if (col < heads) {
+                    *reinterpret_cast<f32x4_kv *>(dst) = f32x4_kv{x[0], x[1], x[2], x[3]};
+                    *reinterpret_cast<f32x4_kv *>(dst + 16 * pl.block_heads) = f32x4_kv{x[4], x[5], x[6], x[7]};
+                }
+                if (++held == most_held) put_scores(chunk);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
@@ -514,6 +531,8 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
             }
         }
 
+        if (WEIGHTS && held) put_scores(c1 - 1);
+
         // The four waves' results together.
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
@@ -565,14 +584,14 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
                     float x = o[n][e][i] * scale_o[i];
                     if (PACK) x += __shfl_xor(x, 32);  // the weights' lower parts
                     const int h = quad * 4 + i;
-                    if (h < HR) wave_o[wave][h][col * T::DPL + e] = x;
+                    if (h < HR) wave_o(wave, h, col * T::DPL + e) = x;
                 }
             __syncthreads();
             for (int i = tid; i < heads * (COLS / 4); i += ATTEND_THREADS) {
                 const int h = i / (COLS / 4), d = i % (COLS / 4) * 4;
-                f32x4_kv x = *reinterpret_cast<f32x4_kv *>(&wave_o[0][h][d]);
+                f32x4_kv x = *reinterpret_cast<f32x4_kv *>(&wave_o(0, h, d));
 #pragma unroll
-                for (int w = 1; w < ATTEND_WAVES; ++w) x += *reinterpret_cast<f32x4_kv *>(&wave_o[w][h][d]);
+                for (int w = 1; w < ATTEND_WAVES; ++w) x += *reinterpret_cast<f32x4_kv *>(&wave_o(w, h, d));
                 if (whole) {
                     float top, total;
                     merged(h, top, total);
@@ -587,7 +606,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
         }
         u += c1 - c0;
         if (u >= u1) return;  // the only piece, or the share's last
-        __syncthreads();      // wave_ml and wave_o are free
+        __syncthreads();      // wave_ml and pool are free
         if (++vh == vheads) {
             vh = 0;
             row_at += row_chunks;
