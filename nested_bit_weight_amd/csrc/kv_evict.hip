@@ -6,22 +6,26 @@
 // the places below it that became free.  Ranking reads 8 bytes a slot and
 // moves copy 4 * dim elements a moved row, so the two are separate problems:
 //
-//  - Ranking needs a whole (row, head) in one place: one workgroup takes it,
-//    with its keys in registers (up to 32 a thread; longer rows are walked in
-//    pieces of 32768, their keys in the workspace after the first walk).  The
-//    budget-th largest key is found by counting: a histogram of 2048 bins over
-//    the 11 bits below the leading bits that all candidates share, the bin that
-//    holds the wanted key, and again inside it, until a bin is wanted whole or
-//    holds one value.  On attention totals the first two passes do.  Protected
-//    slots, which all share the key +infinity, are only counted.  (Bins over
-//    fixed leading bits put most totals, alike in sign and exponent, into a few
-//    bins, whose atomics then wait for each other.)
+//  - Ranking.  Up to 16384 slots one workgroup takes a (row, head), with its keys
+//    in registers, 16 a thread.  The budget-th largest key is found by counting: a
+//    histogram of 2048 bins over the 11 bits below the leading bits that all
+//    candidates share, the bin that holds the wanted key, and again inside it,
+//    until a bin is wanted whole or holds one value.  On attention totals the first
+//    two passes do.  Protected slots, which all share the key +infinity, are only
+//    counted.  (Bins over fixed leading bits put most totals, alike in sign and
+//    exponent, into a few bins, whose atomics then wait for each other.)
 //    A slot's place in the list of gaps (below the budget, not kept) or movers
 //    (past it, kept) is the number of them in lower slots: ballots within a
 //    wave, and one running sum over the waves' counts.
-//  - Moves need the whole device: with more than a few a second launch makes
-//    them, 64 to a workgroup.  In the steady state of one token over the
-//    budget the ranking's workgroup makes its one move itself.
+//  - Longer rows are more than one CU reads in good time (one row of 120001 slots
+//    in 8 workgroups: 160 us).  There a workgroup takes 4096 slots of a (row, head)
+//    and the steps above are launches of their own: newest position, keys and a
+//    histogram over their upper 11 bits, two more over the next 11 and the last 10
+//    of those in the wanted bin, counts, lists.  Histograms meet in integer
+//    atomics, whose order does not matter.
+//  - Moves need the whole device: with more than a few a last launch makes them, 64
+//    to a workgroup.  In the steady state of one token over the budget the ranking's
+//    workgroup makes its one move itself.
 //
 // A move reads at or past the budget and writes below it, so moves never meet,
 // and no buffer that the ranking reads is written.
@@ -36,18 +40,24 @@ typedef int32_t i32x4_ev __attribute__((ext_vector_type(4)));
 
 constexpr int EVICT_BINS_LOG2 = 11, EVICT_BINS = 1 << EVICT_BINS_LOG2;
 constexpr uint32_t KEY_INF = 0xFF800000u, KEY_NEG_INF = 0x007FFFFFu;
-constexpr int EVICT_STEP = 32768;   // slots that one walk of the largest kernel holds
+constexpr int EVICT_ROW = 16384;     // the longest row that one workgroup ranks
+constexpr int PART_THREADS = 256, PART_GROUPS = 4, PART = PART_THREADS * PART_GROUPS * 4;  // longer ones: slots of a workgroup
 constexpr int MOVES = 64;           // moves of a workgroup of the second launch
 constexpr int FUSED_MOVES = 16;     // up to so many the ranking's workgroup makes itself
 
-// The workspace: keys of long rows, the lists of each (row, head), their lengths.
+// The workspace: the lists of each (row, head) and their lengths; for long rows,
+// what the launches leave each other.
 struct EvictPlan {
-    uint32_t *keys;   // [rows * heads][key_ld], or null
-    int64_t key_ld;
     int32_t *lists;   // [rows * heads][2][most]: places to move to, slots to move from
     int most;
     int32_t *counts;  // [rows * heads], or null where the ranking's workgroup moves
     int vec;          // totals and positions may be read 16 bytes at a time
+    int parts;        // parts of a long row; 0: one workgroup ranks
+    uint32_t *keys;   // [rows * heads][parts * PART]
+    int32_t *newest;  // [rows * heads][parts]
+    int32_t *hist;    // [rows * heads][3][EVICT_BINS]
+    int32_t *found;   // [rows * heads][3][3]: each histogram's bin, keys above it, keys in it
+    int32_t *tally;   // [rows * heads][parts][4]: keys above the limit and equal to it, below the budget and past it
 };
 
 // Keys as unsigned numbers of the same order.  -0 and +0 are equal.
@@ -100,231 +110,104 @@ __device__ __forceinline__ void make_moves(const KvCache &c, const KvEvict &a, i
     }
 }
 
-template <int THREADS, int GROUPS>
-__global__ __launch_bounds__(THREADS) void kv_evict_kernel(KvCache c, KvEvict a, EvictPlan pl) {
-    constexpr int WAVES = THREADS / 64, STEP = THREADS * GROUPS * 4;
-    constexpr int TAB = GROUPS * WAVES;  // the waves' counts of one walk, in the order of the slots
-    __shared__ int hist[EVICT_BINS];
-    __shared__ int red[3][WAVES];
-    __shared__ int tab[2][TAB + 1];
-    __shared__ int found[3];
+// Four values from j on (j a multiple of 4), those from `end` on as `none`.
+template <class V>
+struct Four { V v[4]; };
+template <class V>
+__device__ __forceinline__ Four<V> four(const V *p, int j, int end, V none, bool vec) {
+    typedef V vec_t __attribute__((ext_vector_type(4)));
+    Four<V> r = {{none, none, none, none}};
+    if (vec && j + 4 <= end) {
+        const vec_t w = *reinterpret_cast<const vec_t *>(p + j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r.v[e] = w[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (j + e < end) r.v[e] = p[j + e];
+    }
+    return r;
+}
+
+// The totals and positions of slots j .. j + 3 below `end`, from `base` on, to the outputs.
+__device__ __forceinline__ void copy_out(const KvEvict &a, int64_t base, int j, int end, bool vec) {
+    if (j >= end) return;
+    const Four<float> x = four(a.acc + base, j, end, 0.f, vec);
+    const Four<int32_t> y = four(a.pos + base, j, end, 0, vec);
+    if (vec && j + 4 <= end) {
+        *reinterpret_cast<f32x4_ev *>(a.acc_out + base + j) = f32x4_ev{x.v[0], x.v[1], x.v[2], x.v[3]};
+        *reinterpret_cast<i32x4_ev *>(a.pos_out + base + j) = i32x4_ev{y.v[0], y.v[1], y.v[2], y.v[3]};
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (j + e < end) {
+                a.acc_out[base + j + e] = x.v[e];
+                a.pos_out[base + j + e] = y.v[e];
+            }
+    }
+}
+
+// The bin of `hist` that the want-th largest key is in: found = {bin, keys above
+// it, keys in it}.  Every thread gets the same answer.
+template <int THREADS>
+__device__ __forceinline__ void find_bin(const int *hist, int want, int *red, int *found) {
+    constexpr int WAVES = THREADS / 64, PER = EVICT_BINS / THREADS;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int row = blockIdx.x / c.heads, head = blockIdx.x % c.heads;
-    const int n = kv_len(a.lens, row, a.max_len), b = a.budget;
-    const int64_t base = (int64_t)blockIdx.x * c.cap;
-    const float *acc = a.acc + base;
-    const int32_t *pos = a.pos + base;
-    float *acc_out = a.acc_out + base;
-    int32_t *pos_out = a.pos_out + base;
-    if (head == 0 && tid == 0) a.lens_out[row] = n < b ? n : b;
-    if (pl.counts && tid == 0 && n <= b) pl.counts[blockIdx.x] = 0;
-
-    // Four slots from j on (j a multiple of 4) of a tensor, those past the end as `none`.
-    auto four = [&](const auto *p, int j, int end, auto none) {
-        decltype(none) x[4] = {none, none, none, none};
-        if (pl.vec && j + 4 <= end) {
-            typedef decltype(none) vec_t __attribute__((ext_vector_type(4)));
-            const vec_t w = *reinterpret_cast<const vec_t *>(p + j);
+    // Bins from the top: this thread's are PER of them below tid * PER others.
+    int count[PER], mine = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = w[e];
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (j + e < end) x[e] = p[j + e];
-        }
-        struct R { decltype(none) v[4]; } r;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) r.v[e] = x[e];
-        return r;
-    };
-    // The first `end` totals and positions from slot j on to the outputs.
-    auto copy_out = [&](int j, int end) {
-        if (j >= end) return;
-        const auto x = four(acc, j, end, 0.f);
-        const auto y = four(pos, j, end, 0);
-        if (pl.vec && j + 4 <= end) {
-            *reinterpret_cast<f32x4_ev *>(acc_out + j) = f32x4_ev{x.v[0], x.v[1], x.v[2], x.v[3]};
-            *reinterpret_cast<i32x4_ev *>(pos_out + j) = i32x4_ev{y.v[0], y.v[1], y.v[2], y.v[3]};
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (j + e < end) {
-                    acc_out[j + e] = x.v[e];
-                    pos_out[j + e] = y.v[e];
-                }
-        }
-    };
-    if (n <= b) {
-        for (int j = tid * 4; j < n; j += THREADS * 4) copy_out(j, n);
-        return;
+    for (int i = 0; i < PER; ++i) {
+        count[i] = hist[EVICT_BINS - 1 - (tid * PER + i)];
+        mine += count[i];
     }
-
-    const int walks = (n + STEP - 1) / STEP;  // 1 but for rows longer than the largest kernel holds
-    uint32_t key[GROUPS][4];
-    auto slot_of = [&](int walk, int g) { return walk * STEP + (g * THREADS + tid) * 4; };
-    uint32_t *stored = pl.keys ? pl.keys + (int64_t)blockIdx.x * pl.key_ld : nullptr;
-    auto get_keys = [&](int walk) {  // of a later walk over a long row
-#pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-            const int j = slot_of(walk, g);
-            const i32x4_ev w = j < n ? *reinterpret_cast<const i32x4_ev *>(stored + j) : i32x4_ev{0, 0, 0, 0};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) key[g][e] = (uint32_t)w[e];
-        }
-    };
-
-    // The newest position, then the keys; how many are +infinity and the range of the rest.
-    int32_t newest = INT32_MIN;
-    int inf = 0;
-    uint32_t lo = 0xFFFFFFFFu, hi = 0;
-    {
-        float x[GROUPS][4];
-        int32_t y[GROUPS][4];
-        auto get = [&](int walk, bool totals) {
-#pragma unroll
-            for (int g = 0; g < GROUPS; ++g) {
-                const int j = slot_of(walk, g);
-                const auto p = four(pos, j, n, INT32_MIN);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[g][e] = p.v[e];
-            }
-            if (totals)
-#pragma unroll
-                for (int g = 0; g < GROUPS; ++g) {
-                    const auto p = four(acc, slot_of(walk, g), n, 0.f);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[g][e] = p.v[e];
-                }
-        };
-        for (int walk = 0; walk < walks; ++walk) {
-            get(walk, walks == 1);
-#pragma unroll
-            for (int g = 0; g < GROUPS; ++g)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) newest = max(newest, y[g][e]);
-        }
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) newest = max(newest, __shfl_xor(newest, d));
-        if (lane == 0) red[0][wave] = newest;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) newest = max(newest, red[0][w]);
-        for (int walk = 0; walk < walks; ++walk) {
-            if (walks > 1) get(walk, true);
-#pragma unroll
-            for (int g = 0; g < GROUPS; ++g) {
-                const int j = slot_of(walk, g);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const bool there = j + e < n;
-                    const uint32_t k = there ? evict_key(x[g][e], y[g][e], newest, a) : 0;  // 0: below every key
-                    key[g][e] = k;
-                    inf += k == KEY_INF;
-                    if (there && k != KEY_INF) {
-                        lo = min(lo, k);
-                        hi = max(hi, k);
-                    }
-                }
-                if (walks > 1 && j < n)
-                    *reinterpret_cast<i32x4_ev *>(stored + j) =
-                        i32x4_ev{(int)key[g][0], (int)key[g][1], (int)key[g][2], (int)key[g][3]};
-            }
-        }
-    }
-    __syncthreads();
+    int upto = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        inf += __shfl_xor(inf, d);
-        lo = min(lo, (uint32_t)__shfl_xor((int)lo, d));
-        hi = max(hi, (uint32_t)__shfl_xor((int)hi, d));
+        const int x = __shfl_up(upto, d);
+        if (lane >= d) upto += x;
     }
-    if (lane == 0) {
-        red[0][wave] = inf;
-        red[1][wave] = (int)lo;
-        red[2][wave] = (int)hi;
-    }
+    if (lane == 63) red[wave] = upto;
     __syncthreads();
-    inf = 0;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-        inf += red[0][w];
-        lo = min(lo, (uint32_t)red[1][w]);
-        hi = max(hi, (uint32_t)red[2][w]);
-    }
-
-    // All keys above `limit` stay, and of the equals the first `want`; with `all`, every equal.
-    uint32_t limit = KEY_INF;
-    int want = b;
-    bool all = inf == b;
-    if (inf < b) {
-        want = b - inf;
-        for (;;) {  // the want-th largest of the keys within [lo, hi]
-            const int bits = lo == hi ? 0 : 32 - __builtin_clz(lo ^ hi);
-            if (bits == 0) {
-                limit = lo;
-                break;
+    for (int w = 0; w < WAVES; ++w)
+        if (w < wave) upto += red[w];
+    int above = upto - mine;
+    if (above < want && want <= upto) {
+        bool open = true;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (open && want <= above + count[i]) {
+                found[0] = EVICT_BINS - 1 - (tid * PER + i);
+                found[1] = above;
+                found[2] = count[i];
+                open = false;
             }
-            const int shift = bits > EVICT_BINS_LOG2 ? bits - EVICT_BINS_LOG2 : 0;
-            for (int i = tid; i < EVICT_BINS; i += THREADS) hist[i] = 0;
-            __syncthreads();
-            for (int walk = 0; walk < walks; ++walk) {
-                if (walks > 1) get_keys(walk);
-#pragma unroll
-                for (int g = 0; g < GROUPS; ++g)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t k = key[g][e];
-                        if (k >= lo && k <= hi) atomicAdd(&hist[(k >> shift) & (EVICT_BINS - 1)], 1);
-                    }
-            }
-            __syncthreads();
-            // Bins from the top: this thread's are PER of them below tid * PER others.
-            constexpr int PER = EVICT_BINS / THREADS;
-            int mine = 0;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) mine += hist[EVICT_BINS - 1 - (tid * PER + i)];
-            int upto = mine;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int x = __shfl_up(upto, d);
-                if (lane >= d) upto += x;
-            }
-            if (lane == 63) red[0][wave] = upto;
-            __syncthreads();
-#pragma unroll
-            for (int w = 0; w < WAVES; ++w)
-                if (w < wave) upto += red[0][w];
-            int above = upto - mine;
-            if (above < want && want <= upto) {
-                for (int i = 0; i < PER; ++i) {
-                    const int bin = EVICT_BINS - 1 - (tid * PER + i);
-                    if (want <= above + hist[bin]) {
-                        found[0] = bin;
-                        found[1] = above;
-                        found[2] = hist[bin];
-                        break;
-                    }
-                    above += hist[bin];
-                }
-            }
-            __syncthreads();
-            const uint32_t low = (uint32_t)(((uint64_t)(hi >> shift) & ~(uint64_t)(EVICT_BINS - 1)) | (uint32_t)found[0]) << shift;
-            const uint32_t high = low + ((1u << shift) - 1);
-            want -= found[1];
-            const bool whole = found[2] == want;
-            lo = max(lo, low);
-            hi = min(hi, high);
-            if (whole || shift == 0) {
-                limit = lo;
-                all = whole;
-                break;
-            }
-            __syncthreads();  // found and hist are free
+            above += count[i];
         }
     }
+    __syncthreads();
+}
 
-    // Gaps and movers.
-    int32_t *to = pl.lists + (int64_t)blockIdx.x * 2 * pl.most, *of = to + pl.most;
+// What stays: the keys above `limit`, and of its equals the first `want` in the
+// order of the slots; with `all`, every one.
+struct Limit {
+    uint32_t key;
+    int want;
+    bool all;
+};
+
+// The lists' entries of one workgroup's keys, slots first .. first + THREADS *
+// GROUPS * 4 - 1 (thread t has four from first + 4 (g THREADS + t) on), and their
+// totals and positions below the budget to the outputs (the gaps' too: their movers
+// overwrite them).  equals, gaps, movers: how many there are in lower slots;
+// returns the movers up to and with these.
+template <int THREADS, int GROUPS>
+__device__ __forceinline__ int list_moves(const KvEvict &a, const EvictPlan &pl, int64_t base, const uint32_t (&key)[GROUPS][4],
+                                          int first, const Limit &lim, int equals, int gaps, int movers, int32_t *to,
+                                          int32_t *of) {
+    constexpr int WAVES = THREADS / 64, TAB = GROUPS * WAVES;  // the waves' counts in the order of the slots
+    __shared__ int tab[2][TAB + 1];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = a.budget;
     const uint64_t lower = (1ull << lane) - 1;
     // The running sums over `tab`: entry i becomes the sum of those before it, the last one the total.
     auto sums = [&]() {
@@ -347,82 +230,390 @@ __global__ __launch_bounds__(THREADS) void kv_evict_kernel(KvCache c, KvEvict a,
         }
         __syncthreads();
     };
-    int equals = 0, gaps = 0, movers = 0;
-    for (int walk = 0; walk < walks; ++walk) {
-        if (walks > 1) get_keys(walk);
-        uint32_t keep = 0;  // bit 4 g + e
+    uint32_t keep = 0;  // bit 4 g + e
 #pragma unroll
-        for (int g = 0; g < GROUPS; ++g)
+    for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                keep |= (uint32_t)(key[g][e] > limit || (all && key[g][e] == limit)) << (4 * g + e);
-        if (!all) {
-#pragma unroll
-            for (int g = 0; g < GROUPS; ++g) {
-                int count = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) count += __popcll(__ballot(key[g][e] == limit));
-                if (lane == 0) tab[0][g * WAVES + wave] = tab[1][g * WAVES + wave] = count;
-            }
-            sums();
-#pragma unroll
-            for (int g = 0; g < GROUPS; ++g) {
-                int r = equals + tab[0][g * WAVES + wave];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) r += __popcll(__ballot(key[g][e] == limit) & lower);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (key[g][e] == limit) keep |= (uint32_t)(r++ < want) << (4 * g + e);
-            }
-            equals += tab[0][TAB];
-            __syncthreads();
-        }
-        auto is_gap = [&](int g, int e) { return !(keep >> (4 * g + e) & 1) && slot_of(walk, g) + e < b; };
-        auto is_mover = [&](int g, int e) { return (keep >> (4 * g + e) & 1) && slot_of(walk, g) + e >= b; };
+        for (int e = 0; e < 4; ++e)
+            keep |= (uint32_t)(key[g][e] > lim.key || (lim.all && key[g][e] == lim.key)) << (4 * g + e);
+    if (!lim.all) {
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            int count_g = 0, count_m = 0;
+            int count = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                count_g += __popcll(__ballot(is_gap(g, e)));
-                count_m += __popcll(__ballot(is_mover(g, e)));
-            }
-            if (lane == 0) {
-                tab[0][g * WAVES + wave] = count_g;
-                tab[1][g * WAVES + wave] = count_m;
-            }
+            for (int e = 0; e < 4; ++e) count += __popcll(__ballot(key[g][e] == lim.key));
+            if (lane == 0) tab[0][g * WAVES + wave] = tab[1][g * WAVES + wave] = count;
         }
         sums();
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            const int j = slot_of(walk, g);
-            int rg = gaps + tab[0][g * WAVES + wave], rm = movers + tab[1][g * WAVES + wave];
+            int r = equals + tab[0][g * WAVES + wave];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                rg += __popcll(__ballot(is_gap(g, e)) & lower);
-                rm += __popcll(__ballot(is_mover(g, e)) & lower);
-            }
+            for (int e = 0; e < 4; ++e) r += __popcll(__ballot(key[g][e] == lim.key) & lower);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (is_gap(g, e)) to[rg++] = j + e;
-                if (is_mover(g, e)) of[rm++] = j + e;
-            }
-            copy_out(j, b);  // gaps' entries too: their movers overwrite them
+            for (int e = 0; e < 4; ++e)
+                if (key[g][e] == lim.key) keep |= (uint32_t)(r++ < lim.want) << (4 * g + e);
         }
-        gaps += tab[0][TAB];
-        movers += tab[1][TAB];
         __syncthreads();
     }
+    auto slot_of = [&](int g) { return first + (g * THREADS + tid) * 4; };
+    auto is_gap = [&](int g, int e) { return !(keep >> (4 * g + e) & 1) && slot_of(g) + e < b; };
+    auto is_mover = [&](int g, int e) { return (keep >> (4 * g + e) & 1) && slot_of(g) + e >= b; };
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+        int count_g = 0, count_m = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            count_g += __popcll(__ballot(is_gap(g, e)));
+            count_m += __popcll(__ballot(is_mover(g, e)));
+        }
+        if (lane == 0) {
+            tab[0][g * WAVES + wave] = count_g;
+            tab[1][g * WAVES + wave] = count_m;
+        }
+    }
+    sums();
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+        int rg = gaps + tab[0][g * WAVES + wave], rm = movers + tab[1][g * WAVES + wave];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            rg += __popcll(__ballot(is_gap(g, e)) & lower);
+            rm += __popcll(__ballot(is_mover(g, e)) & lower);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (is_gap(g, e)) to[rg++] = slot_of(g) + e;
+            if (is_mover(g, e)) of[rm++] = slot_of(g) + e;
+        }
+        copy_out(a, base, slot_of(g), b, pl.vec);
+    }
+    return movers + tab[1][TAB];
+}
+
+// Rows of up to THREADS * GROUPS * 4 slots: one workgroup for each (row, head).
+template <int THREADS, int GROUPS>
+__global__ __launch_bounds__(THREADS) void kv_evict_kernel(KvCache c, KvEvict a, EvictPlan pl) {
+    constexpr int WAVES = THREADS / 64;
+    __shared__ int hist[EVICT_BINS];
+    __shared__ int red[3][WAVES];
+    __shared__ int found[3];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int row = blockIdx.x / c.heads, head = blockIdx.x % c.heads;
+    const int n = kv_len(a.lens, row, a.max_len), b = a.budget;
+    const int64_t base = (int64_t)blockIdx.x * c.cap;
+    if (head == 0 && tid == 0) a.lens_out[row] = n < b ? n : b;
+    if (n <= b) {
+        if (pl.counts && tid == 0) pl.counts[blockIdx.x] = 0;
+        for (int j = tid * 4; j < n; j += THREADS * 4) copy_out(a, base, j, n, pl.vec);
+        return;
+    }
+
+    // The newest position, then the keys; how many are +infinity and the range of the rest.
+    uint32_t key[GROUPS][4];
+    auto slot_of = [&](int g) { return (g * THREADS + tid) * 4; };
+    int32_t newest = INT32_MIN;
+    int inf = 0;
+    uint32_t lo = 0xFFFFFFFFu, hi = 0;
+    {
+        Four<float> x[GROUPS];
+        Four<int32_t> y[GROUPS];
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) y[g] = four(a.pos + base, slot_of(g), n, INT32_MIN, pl.vec);
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) x[g] = four(a.acc + base, slot_of(g), n, 0.f, pl.vec);
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) newest = max(newest, y[g].v[e]);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) newest = max(newest, __shfl_xor(newest, d));
+        if (lane == 0) red[0][wave] = newest;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) newest = max(newest, red[0][w]);
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool there = slot_of(g) + e < n;
+                const uint32_t k = there ? evict_key(x[g].v[e], y[g].v[e], newest, a) : 0;  // 0: below every key
+                key[g][e] = k;
+                inf += k == KEY_INF;
+                if (there && k != KEY_INF) {
+                    lo = min(lo, k);
+                    hi = max(hi, k);
+                }
+            }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        inf += __shfl_xor(inf, d);
+        lo = min(lo, (uint32_t)__shfl_xor((int)lo, d));
+        hi = max(hi, (uint32_t)__shfl_xor((int)hi, d));
+    }
+    if (lane == 0) {
+        red[0][wave] = inf;
+        red[1][wave] = (int)lo;
+        red[2][wave] = (int)hi;
+    }
+    __syncthreads();
+    inf = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+        inf += red[0][w];
+        lo = min(lo, (uint32_t)red[1][w]);
+        hi = max(hi, (uint32_t)red[2][w]);
+    }
+
+    Limit lim = {KEY_INF, b, inf == b};
+    if (inf < b) {
+        lim.want = b - inf;
+        while (lo != hi) {  // the want-th largest of the keys within [lo, hi]
+            const int bits = 32 - __builtin_clz(lo ^ hi);
+            const int shift = bits > EVICT_BINS_LOG2 ? bits - EVICT_BINS_LOG2 : 0;
+            for (int i = tid; i < EVICT_BINS; i += THREADS) hist[i] = 0;
+            __syncthreads();
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t k = key[g][e];
+                    if (k >= lo && k <= hi) atomicAdd(&hist[(k >> shift) & (EVICT_BINS - 1)], 1);
+                }
+            __syncthreads();
+            find_bin<THREADS>(hist, lim.want, red[0], found);
+            const uint32_t low = (((hi >> shift) & ~(uint32_t)(EVICT_BINS - 1)) | (uint32_t)found[0]) << shift;
+            const uint32_t high = low + ((1u << shift) - 1);
+            lim.want -= found[1];
+            lim.all = found[2] == lim.want;
+            lo = max(lo, low);
+            hi = min(hi, high);
+            if (lim.all || shift == 0) break;
+            __syncthreads();  // found and hist are free
+        }
+        lim.key = lo;
+    }
+
+    int32_t *to = pl.lists + (int64_t)blockIdx.x * 2 * pl.most, *of = to + pl.most;
+    const int movers = list_moves<THREADS, GROUPS>(a, pl, base, key, 0, lim, 0, 0, 0, to, of);
     if (pl.counts) {
         if (tid == 0) pl.counts[blockIdx.x] = movers;
         return;
     }
+    __syncthreads();  // the lists are written
     switch (c.fp8 ? c.dim : 2 * c.dim) {
     case 64: make_moves<64, THREADS>(c, a, row, head, to, of, movers); break;
     case 128: make_moves<128, THREADS>(c, a, row, head, to, of, movers); break;
     case 256: make_moves<256, THREADS>(c, a, row, head, to, of, movers); break;
     default: make_moves<512, THREADS>(c, a, row, head, to, of, movers); break;
     }
+}
+
+// The bits of a key that histogram `level` of a long row counts, and those above them.
+__device__ __forceinline__ int level_shift(int level) { return level == 0 ? 21 : level == 1 ? 10 : 0; }
+
+// A long row's limit after `levels` histograms: found[level] holds each one's bin,
+// the keys above it and the keys in it.  The prefix of the keys still wanted and how
+// many of them; all: they are wanted whole (later histograms are then not made).
+__device__ __forceinline__ Limit limit_after(const int32_t *found, int levels, int budget) {
+    Limit lim = {0, budget, false};
+    for (int l = 0; l < levels && !lim.all; ++l) {
+        lim.key |= (uint32_t)found[3 * l] << level_shift(l);
+        lim.want -= found[3 * l + 1];
+        lim.all = found[3 * l + 2] == lim.want;
+    }
+    return lim;
+}
+
+enum EvictStage { NEWEST, COUNT0, COUNT1, COUNT2, TALLY, LIST };
+
+// One step of a long row's ranking: workgroup = (row, head, part of PART slots).
+template <int STAGE>
+__global__ __launch_bounds__(PART_THREADS) void kv_evict_part_kernel(KvCache c, KvEvict a, EvictPlan pl) {
+    constexpr int THREADS = PART_THREADS, GROUPS = PART_GROUPS, WAVES = THREADS / 64;
+    __shared__ int hist[EVICT_BINS];
+    __shared__ int red[4][WAVES];
+    __shared__ int found[3];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int which = blockIdx.x / pl.parts, part = blockIdx.x % pl.parts, first = part * PART;
+    const int row = which / c.heads, head = which % c.heads;
+    const int n = kv_len(a.lens, row, a.max_len), b = a.budget;
+    const int64_t base = (int64_t)which * c.cap;
+    int32_t *ghist = pl.hist + (int64_t)which * 3 * EVICT_BINS, *gfound = pl.found + (int64_t)which * 9;
+    auto slot_of = [&](int g) { return first + (g * THREADS + tid) * 4; };
+    if (STAGE == LIST && part == 0 && tid == 0) {
+        if (head == 0) a.lens_out[row] = n < b ? n : b;
+        if (n <= b && pl.counts) pl.counts[which] = 0;
+    }
+    if (n <= b) {
+        if (STAGE == LIST)
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) copy_out(a, base, slot_of(g), n, pl.vec);
+        return;
+    }
+    if (STAGE == NEWEST) {  // and the histograms' first zeros
+        for (int i = part * THREADS + tid; i < 3 * EVICT_BINS; i += pl.parts * THREADS) ghist[i] = 0;
+    }
+    if (first >= n) {
+        if (STAGE == NEWEST && tid == 0) pl.newest[(int64_t)which * pl.parts + part] = INT32_MIN;
+        return;
+    }
+    if (STAGE == NEWEST) {
+        int32_t newest = INT32_MIN;
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            const Four<int32_t> y = four(a.pos + base, slot_of(g), n, INT32_MIN, pl.vec);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) newest = max(newest, y.v[e]);
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) newest = max(newest, __shfl_xor(newest, d));
+        if (lane == 0) red[0][wave] = newest;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) newest = max(newest, red[0][w]);
+        if (tid == 0) pl.newest[(int64_t)which * pl.parts + part] = newest;
+        return;
+    }
+
+    uint32_t key[GROUPS][4];
+    uint32_t *stored = pl.keys + (int64_t)which * pl.parts * PART;
+    if (STAGE == COUNT0) {
+        Four<float> x[GROUPS];
+        Four<int32_t> y[GROUPS];
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) y[g] = four(a.pos + base, slot_of(g), n, INT32_MIN, pl.vec);
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) x[g] = four(a.acc + base, slot_of(g), n, 0.f, pl.vec);
+        int32_t newest = INT32_MIN;
+        for (int i = tid; i < pl.parts; i += THREADS) newest = max(newest, pl.newest[(int64_t)which * pl.parts + i]);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) newest = max(newest, __shfl_xor(newest, d));
+        if (lane == 0) red[0][wave] = newest;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) newest = max(newest, red[0][w]);
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            const int j = slot_of(g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) key[g][e] = j + e < n ? evict_key(x[g].v[e], y[g].v[e], newest, a) : 0;
+            *reinterpret_cast<i32x4_ev *>(stored + j) = i32x4_ev{(int)key[g][0], (int)key[g][1], (int)key[g][2], (int)key[g][3]};
+        }
+    } else {
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            const i32x4_ev w = *reinterpret_cast<const i32x4_ev *>(stored + slot_of(g));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) key[g][e] = (uint32_t)w[e];
+        }
+    }
+
+    // The last histogram's bin (part 0 leaves it for the launches after this one).
+    constexpr int LEVEL = STAGE == COUNT0 ? 0 : STAGE == COUNT1 ? 1 : STAGE == COUNT2 ? 2 : 3;  // histograms made before
+    Limit lim = limit_after(gfound, LEVEL - 1, b);
+    if (STAGE != COUNT0 && STAGE != LIST && !lim.all) {
+        for (int i = tid; i < EVICT_BINS; i += THREADS) hist[i] = ghist[(LEVEL - 1) * EVICT_BINS + i];
+        __syncthreads();
+        find_bin<THREADS>(hist, lim.want, red[0], found);
+        lim.key |= (uint32_t)found[0] << level_shift(LEVEL - 1);
+        lim.want -= found[1];
+        lim.all = found[2] == lim.want;
+        if (part == 0 && tid < 3) gfound[3 * (LEVEL - 1) + tid] = found[tid];
+        __syncthreads();
+    }
+    if (STAGE == LIST) lim = limit_after(gfound, 3, b);
+
+    if (STAGE == COUNT0 || STAGE == COUNT1 || STAGE == COUNT2) {
+        if (lim.all) return;
+        for (int i = tid; i < EVICT_BINS; i += THREADS) hist[i] = 0;
+        __syncthreads();
+        int inf = 0;
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t k = key[g][e];
+                if (STAGE == COUNT0) {  // +infinity, all protected slots' key, is counted apart
+                    if (k == KEY_INF) ++inf;
+                    else if (k) atomicAdd(&hist[k >> 21], 1);
+                } else if (k >> level_shift(LEVEL - 1) == lim.key >> level_shift(LEVEL - 1)) {
+                    atomicAdd(&hist[(k >> level_shift(LEVEL)) & (STAGE == COUNT1 ? 2047 : 1023)], 1);
+                }
+            }
+        if (STAGE == COUNT0) {
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) inf += __shfl_xor(inf, d);
+            if (lane == 0 && inf) atomicAdd(&hist[KEY_INF >> 21], inf);
+        }
+        __syncthreads();
+        for (int i = tid; i < EVICT_BINS; i += THREADS)
+            if (hist[i]) atomicAdd(&ghist[LEVEL * EVICT_BINS + i], hist[i]);
+        return;
+    }
+
+    if (STAGE == TALLY) {
+        int count[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool past = slot_of(g) + e >= b;
+                if (key[g][e] > lim.key) ++count[past];
+                else if (key[g][e] == lim.key) ++count[2 + past];
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) count[i] += __shfl_xor(count[i], d);
+            if (lane == 0) red[i][wave] = count[i];
+        }
+        __syncthreads();
+        if (tid < 4) {
+            int sum = 0;
+            for (int w = 0; w < WAVES; ++w) sum += red[tid][w];
+            pl.tally[((int64_t)which * pl.parts + part) * 4 + tid] = sum;
+        }
+        return;
+    }
+
+    // LIST: what the parts before this one keep.
+    if (wave == 0) {
+        int equals = 0, below = 0, past = 0;  // equals, and kept below the budget and past it, in earlier parts
+        for (int i0 = 0; i0 < part; i0 += 64) {
+            const int i = i0 + lane;
+            i32x4_ev t = {0, 0, 0, 0};
+            if (i < part) t = *reinterpret_cast<const i32x4_ev *>(pl.tally + ((int64_t)which * pl.parts + i) * 4);
+            int upto = t[2] + t[3];
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int x = __shfl_up(upto, d);
+                if (lane >= d) upto += x;
+            }
+            const int left = lim.all ? INT32_MAX : max(0, lim.want - (equals + upto - t[2] - t[3]));  // for this part's equals
+            const int low = min(t[2], left), high = min(t[3], left - low);
+            int kb = t[0] + low, kp = t[1] + high;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                kb += __shfl_xor(kb, d);
+                kp += __shfl_xor(kp, d);
+            }
+            below += kb;
+            past += kp;
+            equals += __builtin_amdgcn_readlane(upto, 63);
+        }
+        if (lane == 0) {
+            found[0] = equals;
+            found[1] = min(first, b) - below;
+            found[2] = past;
+        }
+    }
+    __syncthreads();
+    int32_t *to = pl.lists + (int64_t)which * 2 * pl.most, *of = to + pl.most;
+    const int movers = list_moves<THREADS, GROUPS>(a, pl, base, key, first, lim, found[0], found[1], found[2], to, of);
+    if (first + PART >= n && tid == 0) pl.counts[which] = movers;
 }
 
 template <int ROW_BYTES>
@@ -443,16 +634,21 @@ static int64_t evict_plan(const KvCache &c, int budget, int max_len, uint8_t *ba
         at += (bytes + 255) / 256 * 256;
         return p;
     };
+    *pl = EvictPlan{};
     pl->most = std::max(0, std::min(budget, max_len - budget));
-    pl->keys = nullptr;
-    pl->key_ld = (max_len + 3) / 4 * 4;
-    pl->counts = nullptr;
-    pl->lists = nullptr;
-    if (pl->most == 0) return 0;  // no row is over the budget
-    if (lists * ((pl->most + MOVES - 1) / MOVES) > INT32_MAX) return -1;
-    pl->lists = (int32_t *)take(lists * 2 * pl->most * 4);
-    if (pl->most > FUSED_MOVES) pl->counts = (int32_t *)take(lists * 4);
-    if (max_len > EVICT_STEP) pl->keys = (uint32_t *)take(lists * pl->key_ld * 4);
+    if (max_len > EVICT_ROW) pl->parts = (max_len + PART - 1) / PART;
+    if (lists * std::max(pl->parts, (pl->most + MOVES - 1) / MOVES) > INT32_MAX) return -1;
+    if (pl->most) {
+        pl->lists = (int32_t *)take(lists * 2 * pl->most * 4);
+        if (pl->parts || pl->most > FUSED_MOVES) pl->counts = (int32_t *)take(lists * 4);
+    }
+    if (pl->parts) {
+        pl->keys = (uint32_t *)take(lists * pl->parts * PART * 4);
+        pl->newest = (int32_t *)take(lists * pl->parts * 4);
+        pl->hist = (int32_t *)take(lists * 3 * EVICT_BINS * 4);
+        pl->found = (int32_t *)take(lists * 9 * 4);
+        pl->tally = (int32_t *)take(lists * pl->parts * 4 * 4);
+    }
     return at;
 }
 
@@ -467,18 +663,31 @@ hipError_t launch_kv_evict(const KvCache &c, const KvEvict &a, hipStream_t strea
     pl.vec = c.cap % 4 == 0 && (((uintptr_t)a.acc | (uintptr_t)a.pos | (uintptr_t)a.acc_out | (uintptr_t)a.pos_out) & 15) == 0;
     const dim3 grid((unsigned)c.rows * c.heads);
     // The smallest workgroup that holds the longest row's keys in its registers.
-    if (a.max_len <= 1024) hipLaunchKernelGGL((kv_evict_kernel<256, 1>), grid, dim3(256), 0, stream, c, a, pl);
-    else if (a.max_len <= 4096) hipLaunchKernelGGL((kv_evict_kernel<1024, 1>), grid, dim3(1024), 0, stream, c, a, pl);
-    else if (a.max_len <= 16384) hipLaunchKernelGGL((kv_evict_kernel<1024, 4>), grid, dim3(1024), 0, stream, c, a, pl);
-    else hipLaunchKernelGGL((kv_evict_kernel<1024, 8>), grid, dim3(1024), 0, stream, c, a, pl);
+    if (a.max_len <= 1024) {
+        hipLaunchKernelGGL((kv_evict_kernel<256, 1>), grid, dim3(256), 0, stream, c, a, pl);
+    } else if (a.max_len <= 4096) {
+        hipLaunchKernelGGL((kv_evict_kernel<1024, 1>), grid, dim3(1024), 0, stream, c, a, pl);
+    } else if (!pl.parts) {
+        hipLaunchKernelGGL((kv_evict_kernel<1024, 4>), grid, dim3(1024), 0, stream, c, a, pl);
+    } else {
+        const dim3 parts((unsigned)((int64_t)grid.x * pl.parts)), threads(PART_THREADS);
+        if (pl.most) {
+            hipLaunchKernelGGL(kv_evict_part_kernel<NEWEST>, parts, threads, 0, stream, c, a, pl);
+            hipLaunchKernelGGL(kv_evict_part_kernel<COUNT0>, parts, threads, 0, stream, c, a, pl);
+            hipLaunchKernelGGL(kv_evict_part_kernel<COUNT1>, parts, threads, 0, stream, c, a, pl);
+            hipLaunchKernelGGL(kv_evict_part_kernel<COUNT2>, parts, threads, 0, stream, c, a, pl);
+            hipLaunchKernelGGL(kv_evict_part_kernel<TALLY>, parts, threads, 0, stream, c, a, pl);
+        }
+        hipLaunchKernelGGL(kv_evict_part_kernel<LIST>, parts, threads, 0, stream, c, a, pl);
+    }
     if (pl.counts) {
-        const int parts = (pl.most + MOVES - 1) / MOVES;
-        const dim3 moves((unsigned)((int64_t)grid.x * parts));
+        const int each = (pl.most + MOVES - 1) / MOVES;
+        const dim3 moves((unsigned)((int64_t)grid.x * each));
         switch (c.fp8 ? c.dim : 2 * c.dim) {
-        case 64: hipLaunchKernelGGL(kv_move_kernel<64>, moves, dim3(256), 0, stream, c, a, pl, parts); break;
-        case 128: hipLaunchKernelGGL(kv_move_kernel<128>, moves, dim3(256), 0, stream, c, a, pl, parts); break;
-        case 256: hipLaunchKernelGGL(kv_move_kernel<256>, moves, dim3(256), 0, stream, c, a, pl, parts); break;
-        default: hipLaunchKernelGGL(kv_move_kernel<512>, moves, dim3(256), 0, stream, c, a, pl, parts); break;
+        case 64: hipLaunchKernelGGL(kv_move_kernel<64>, moves, dim3(256), 0, stream, c, a, pl, each); break;
+        case 128: hipLaunchKernelGGL(kv_move_kernel<128>, moves, dim3(256), 0, stream, c, a, pl, each); break;
+        case 256: hipLaunchKernelGGL(kv_move_kernel<256>, moves, dim3(256), 0, stream, c, a, pl, each); break;
+        default: hipLaunchKernelGGL(kv_move_kernel<512>, moves, dim3(256), 0, stream, c, a, pl, each); break;
         }
     }
     return hipGetLastError();

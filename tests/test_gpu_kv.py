@@ -365,6 +365,11 @@ EVICT = [
     ([400, 90], 80, 80, 0, 2, 4, 128, BF16, "ties"), ([1030, 2000], 512, 16, 100, 2, 128, 128, FP8, "spread"),
     ([90, 64, 300], 33, 3, 5, 2, 16, 64, FP8, "odd"), ([129], 128, 0, 1, 4, 2, 256, FP8, "equal"),
     ([6000, 5000], 1500, 4, 200, 1, 64, 64, BF16, "ties"), ([70] * 40, 50, 2, 10, 2, 16, 64, BF16, "spread"),
+    # longer than one workgroup ranks
+    ([20000, 40001, 9000, 16384, 0], 12000, 4, 1000, 2, 64, 64, BF16, "spread"),
+    ([70000, 30001], 30000, 16, 3000, 1, 128, 64, FP8, "ties"), ([33000, 21000], 20999, 0, 64, 1, 32, 64, BF16, "odd"),
+    ([18001], 17990, 2, 0, 2, 16, 128, BF16, "equal"), ([17000, 25000], 25000, 0, 0, 1, 64, 64, BF16, "spread"),
+    ([50000], 900, 4, 896, 1, 1, 64, FP8, "spread"),
 ]
 
 
