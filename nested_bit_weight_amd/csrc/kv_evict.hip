@@ -44,13 +44,14 @@ constexpr int EVICT_ROW = 16384;     // the longest row that one workgroup ranks
 constexpr int PART_THREADS = 256, PART_GROUPS = 4, PART = PART_THREADS * PART_GROUPS * 4;  // longer ones: slots of a workgroup
 constexpr int MOVES = 64;           // moves of a workgroup of the second launch
 constexpr int FUSED_MOVES = 16;     // up to so many the ranking's workgroup makes itself
+constexpr int FEW_OUT = 4;          // up to so many slots over the budget are found one by one
 
 // The workspace: the lists of each (row, head) and their lengths; for long rows,
 // what the launches leave each other.
 struct EvictPlan {
     int32_t *lists;   // [rows * heads][2][most]: places to move to, slots to move from
     int most;
-    int32_t *counts;  // [rows * heads], or null where the ranking's workgroup moves
+    int32_t *counts;  // [rows * heads]; both null where the ranking's workgroup moves
     int vec;          // totals and positions may be read 16 bytes at a time
     int parts;        // parts of a long row; 0: one workgroup ranks
     uint32_t *keys;   // [rows * heads][parts * PART]
@@ -97,8 +98,9 @@ __device__ __forceinline__ void make_moves(const KvCache &c, const KvEvict &a, i
         for (int j = 0; j < AT_ONCE; ++j)
             if (src[j] >= 0 && dst[j] >= 0) {
                 const int64_t at = src[j] * ROW_BYTES + (i0 + j * THREADS) % VECS * 16;
-                k[j] = *reinterpret_cast<const u32x4_kv *>(c.k + at);
-                v[j] = *reinterpret_cast<const u32x4_kv *>(c.v + at);
+                // read for the last time (12 rows, 16384 -> 4096: 77 us so, 85 otherwise)
+                k[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_kv *>(c.k + at));
+                v[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_kv *>(c.v + at));
             }
 #pragma unroll
         for (int j = 0; j < AT_ONCE; ++j)
@@ -129,11 +131,9 @@ __device__ __forceinline__ Four<V> four(const V *p, int j, int end, V none, bool
     return r;
 }
 
-// The totals and positions of slots j .. j + 3 below `end`, from `base` on, to the outputs.
-__device__ __forceinline__ void copy_out(const KvEvict &a, int64_t base, int j, int end, bool vec) {
-    if (j >= end) return;
-    const Four<float> x = four(a.acc + base, j, end, 0.f, vec);
-    const Four<int32_t> y = four(a.pos + base, j, end, 0, vec);
+// Totals x and positions y of slots j .. j + 3 below `end`, of the (row, head) at `base`, to the outputs.
+__device__ __forceinline__ void put_out(const KvEvict &a, int64_t base, int j, int end, const Four<float> &x,
+                                        const Four<int32_t> &y, bool vec) {
     if (vec && j + 4 <= end) {
         *reinterpret_cast<f32x4_ev *>(a.acc_out + base + j) = f32x4_ev{x.v[0], x.v[1], x.v[2], x.v[3]};
         *reinterpret_cast<i32x4_ev *>(a.pos_out + base + j) = i32x4_ev{y.v[0], y.v[1], y.v[2], y.v[3]};
@@ -145,6 +145,9 @@ __device__ __forceinline__ void copy_out(const KvEvict &a, int64_t base, int j, 
                 a.pos_out[base + j + e] = y.v[e];
             }
     }
+}
+__device__ __forceinline__ void copy_out(const KvEvict &a, int64_t base, int j, int end, bool vec) {
+    if (j < end) put_out(a, base, j, end, four(a.acc + base, j, end, 0.f, vec), four(a.pos + base, j, end, 0, vec), vec);
 }
 
 // The bin of `hist` that the want-th largest key is in: found = {bin, keys above
@@ -197,17 +200,15 @@ struct Limit {
 };
 
 // The lists' entries of one workgroup's keys, slots first .. first + THREADS *
-// GROUPS * 4 - 1 (thread t has four from first + 4 (g THREADS + t) on), and their
-// totals and positions below the budget to the outputs (the gaps' too: their movers
-// overwrite them).  equals, gaps, movers: how many there are in lower slots;
-// returns the movers up to and with these.
+// GROUPS * 4 - 1 (thread t has four from first + 4 (g THREADS + t) on).  equals,
+// gaps, movers: how many there are in lower slots; returns the movers up to and
+// with these.
 template <int THREADS, int GROUPS>
-__device__ __forceinline__ int list_moves(const KvEvict &a, const EvictPlan &pl, int64_t base, const uint32_t (&key)[GROUPS][4],
-                                          int first, const Limit &lim, int equals, int gaps, int movers, int32_t *to,
-                                          int32_t *of) {
+__device__ __forceinline__ int list_moves(const uint32_t (&key)[GROUPS][4], int b, int first, const Limit &lim, int equals,
+                                          int gaps, int movers, int32_t *to, int32_t *of) {
     constexpr int WAVES = THREADS / 64, TAB = GROUPS * WAVES;  // the waves' counts in the order of the slots
     __shared__ int tab[2][TAB + 1];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = a.budget;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const uint64_t lower = (1ull << lane) - 1;
     // The running sums over `tab`: entry i becomes the sum of those before it, the last one the total.
     auto sums = [&]() {
@@ -286,7 +287,6 @@ __device__ __forceinline__ int list_moves(const KvEvict &a, const EvictPlan &pl,
             if (is_gap(g, e)) to[rg++] = slot_of(g) + e;
             if (is_mover(g, e)) of[rm++] = slot_of(g) + e;
         }
-        copy_out(a, base, slot_of(g), b, pl.vec);
     }
     return movers + tab[1][TAB];
 }
@@ -333,6 +333,9 @@ __global__ __launch_bounds__(THREADS) void kv_evict_kernel(KvCache c, KvEvict a,
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) newest = max(newest, red[0][w]);
 #pragma unroll
+        for (int g = 0; g < GROUPS; ++g)  // what goes is overwritten when its place is taken
+            if (slot_of(g) < b) put_out(a, base, slot_of(g), b, x[g], y[g], pl.vec);
+#pragma unroll
         for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -346,58 +349,114 @@ __global__ __launch_bounds__(THREADS) void kv_evict_kernel(KvCache c, KvEvict a,
                 }
             }
     }
-    __syncthreads();
+    __shared__ int32_t few[2][FUSED_MOVES];
+    int32_t *to = pl.counts ? pl.lists + (int64_t)blockIdx.x * 2 * pl.most : few[0], *of = pl.counts ? to + pl.most : few[1];
+    int movers;
+    if (n - b <= FEW_OUT) {
+        // The few that go, one after the other: the smallest key, among equals the
+        // highest slot.
+        __shared__ uint64_t least[FEW_OUT][WAVES];
+        int out[FEW_OUT];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        inf += __shfl_xor(inf, d);
-        lo = min(lo, (uint32_t)__shfl_xor((int)lo, d));
-        hi = max(hi, (uint32_t)__shfl_xor((int)hi, d));
-    }
-    if (lane == 0) {
-        red[0][wave] = inf;
-        red[1][wave] = (int)lo;
-        red[2][wave] = (int)hi;
-    }
-    __syncthreads();
-    inf = 0;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-        inf += red[0][w];
-        lo = min(lo, (uint32_t)red[1][w]);
-        hi = max(hi, (uint32_t)red[2][w]);
-    }
-
-    Limit lim = {KEY_INF, b, inf == b};
-    if (inf < b) {
-        lim.want = b - inf;
-        while (lo != hi) {  // the want-th largest of the keys within [lo, hi]
-            const int bits = 32 - __builtin_clz(lo ^ hi);
-            const int shift = bits > EVICT_BINS_LOG2 ? bits - EVICT_BINS_LOG2 : 0;
-            for (int i = tid; i < EVICT_BINS; i += THREADS) hist[i] = 0;
-            __syncthreads();
+        for (int i = 0; i < FEW_OUT; ++i) {
+            out[i] = INT32_MAX;
+            if (i >= n - b) continue;
+            uint64_t m = ~0ull;
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint32_t k = key[g][e];
-                    if (k >= lo && k <= hi) atomicAdd(&hist[(k >> shift) & (EVICT_BINS - 1)], 1);
+                    const int j = slot_of(g) + e;
+                    if (key[g][e]) m = min(m, (uint64_t)key[g][e] << 32 | (uint32_t)(INT32_MAX - j));
                 }
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) m = min(m, (uint64_t)__shfl_xor((unsigned long long)m, d));
+            if (lane == 0) least[i][wave] = m;
             __syncthreads();
-            find_bin<THREADS>(hist, lim.want, red[0], found);
-            const uint32_t low = (((hi >> shift) & ~(uint32_t)(EVICT_BINS - 1)) | (uint32_t)found[0]) << shift;
-            const uint32_t high = low + ((1u << shift) - 1);
-            lim.want -= found[1];
-            lim.all = found[2] == lim.want;
-            lo = max(lo, low);
-            hi = min(hi, high);
-            if (lim.all || shift == 0) break;
-            __syncthreads();  // found and hist are free
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) m = min(m, least[i][w]);
+            out[i] = INT32_MAX - (int)(uint32_t)m;
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (slot_of(g) + e == out[i]) key[g][e] = 0;
         }
-        lim.key = lo;
-    }
+        movers = 0;  // as many as gaps
+#pragma unroll
+        for (int i = 0; i < FEW_OUT; ++i) movers += out[i] < b;
+        if (tid == 0) {
+            int gaps = 0, from = b;
+            for (int last = -1; gaps < movers;) {  // the gaps in ascending order, each with the next slot that stays
+                int next = INT32_MAX;
+#pragma unroll
+                for (int i = 0; i < FEW_OUT; ++i)
+                    if (out[i] > last) next = min(next, out[i]);
+                last = next;
+                bool goes;
+                do {
+                    goes = false;
+#pragma unroll
+                    for (int i = 0; i < FEW_OUT; ++i) goes |= out[i] == from;
+                    from += goes;
+                } while (goes);
+                to[gaps] = next;
+                of[gaps++] = from++;
+            }
+        }
+    } else {
+        __syncthreads();
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            inf += __shfl_xor(inf, d);
+            lo = min(lo, (uint32_t)__shfl_xor((int)lo, d));
+            hi = max(hi, (uint32_t)__shfl_xor((int)hi, d));
+        }
+        if (lane == 0) {
+            red[0][wave] = inf;
+            red[1][wave] = (int)lo;
+            red[2][wave] = (int)hi;
+        }
+        __syncthreads();
+        inf = 0;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            inf += red[0][w];
+            lo = min(lo, (uint32_t)red[1][w]);
+            hi = max(hi, (uint32_t)red[2][w]);
+        }
 
-    int32_t *to = pl.lists + (int64_t)blockIdx.x * 2 * pl.most, *of = to + pl.most;
-    const int movers = list_moves<THREADS, GROUPS>(a, pl, base, key, 0, lim, 0, 0, 0, to, of);
+        Limit lim = {KEY_INF, b, inf == b};
+        if (inf < b) {
+            lim.want = b - inf;
+            while (lo != hi) {  // the want-th largest of the keys within [lo, hi]
+                const int bits = 32 - __builtin_clz(lo ^ hi);
+                const int shift = bits > EVICT_BINS_LOG2 ? bits - EVICT_BINS_LOG2 : 0;
+                for (int i = tid; i < EVICT_BINS; i += THREADS) hist[i] = 0;
+                __syncthreads();
+#pragma unroll
+                for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t k = key[g][e];
+                        if (k >= lo && k <= hi) atomicAdd(&hist[(k >> shift) & (EVICT_BINS - 1)], 1);
+                    }
+                __syncthreads();
+                find_bin<THREADS>(hist, lim.want, red[0], found);
+                const uint32_t low = (((hi >> shift) & ~(uint32_t)(EVICT_BINS - 1)) | (uint32_t)found[0]) << shift;
+                const uint32_t high = low + ((1u << shift) - 1);
+                lim.want -= found[1];
+                lim.all = found[2] == lim.want;
+                lo = max(lo, low);
+                hi = min(hi, high);
+                if (lim.all || shift == 0) break;
+                __syncthreads();  // found and hist are free
+            }
+            lim.key = lo;
+        }
+
+        movers = list_moves<THREADS, GROUPS>(key, b, 0, lim, 0, 0, 0, to, of);
+    }
     if (pl.counts) {
         if (tid == 0) pl.counts[blockIdx.x] = movers;
         return;
@@ -500,6 +559,7 @@ __global__ __launch_bounds__(PART_THREADS) void kv_evict_part_kernel(KvCache c, 
             const int j = slot_of(g);
 #pragma unroll
             for (int e = 0; e < 4; ++e) key[g][e] = j + e < n ? evict_key(x[g].v[e], y[g].v[e], newest, a) : 0;
+            if (j < b) put_out(a, base, j, b, x[g], y[g], pl.vec);  // what goes is overwritten when its place is taken
             *reinterpret_cast<i32x4_ev *>(stored + j) = i32x4_ev{(int)key[g][0], (int)key[g][1], (int)key[g][2], (int)key[g][3]};
         }
     } else {
@@ -612,7 +672,7 @@ __global__ __launch_bounds__(PART_THREADS) void kv_evict_part_kernel(KvCache c, 
     }
     __syncthreads();
     int32_t *to = pl.lists + (int64_t)which * 2 * pl.most, *of = to + pl.most;
-    const int movers = list_moves<THREADS, GROUPS>(a, pl, base, key, first, lim, found[0], found[1], found[2], to, of);
+    const int movers = list_moves<THREADS, GROUPS>(key, b, first, lim, found[0], found[1], found[2], to, of);
     if (first + PART >= n && tid == 0) pl.counts[which] = movers;
 }
 
@@ -639,8 +699,10 @@ static int64_t evict_plan(const KvCache &c, int budget, int max_len, uint8_t *ba
     if (max_len > EVICT_ROW) pl->parts = (max_len + PART - 1) / PART;
     if (lists * std::max(pl->parts, (pl->most + MOVES - 1) / MOVES) > INT32_MAX) return -1;
     if (pl->most) {
-        pl->lists = (int32_t *)take(lists * 2 * pl->most * 4);
-        if (pl->parts || pl->most > FUSED_MOVES) pl->counts = (int32_t *)take(lists * 4);
+        if (pl->parts || pl->most > FUSED_MOVES) {
+            pl->lists = (int32_t *)take(lists * 2 * pl->most * 4);
+            pl->counts = (int32_t *)take(lists * 4);
+        }
     }
     if (pl->parts) {
         pl->keys = (uint32_t *)take(lists * pl->parts * PART * 4);
@@ -657,16 +719,20 @@ int64_t kv_evict_workspace_bytes(const KvCache &c, int budget, int max_len) {
     return evict_plan(c, budget, max_len, nullptr, &pl);
 }
 
-hipError_t launch_kv_evict(const KvCache &c, const KvEvict &a, hipStream_t stream) {
+hipError_t launch_kv_evict(const KvCache &c, const KvEvict &a, int cu_count, hipStream_t stream) {
     EvictPlan pl;
     evict_plan(c, a.budget, a.max_len, a.ws, &pl);
     pl.vec = c.cap % 4 == 0 && (((uintptr_t)a.acc | (uintptr_t)a.pos | (uintptr_t)a.acc_out | (uintptr_t)a.pos_out) & 15) == 0;
     const dim3 grid((unsigned)c.rows * c.heads);
-    // The smallest workgroup that holds the longest row's keys in its registers.
+    // Up to 4096 slots: with a CU for each (row, head), many waves with few keys each;
+    // with more of them than CUs, few waves with many keys each, whose barriers cost
+    // less.  (256 rows x heads of 2049 slots: 13.1 us and 15.7; 768 of 1025: 26 and 20.)
     if (a.max_len <= 1024) {
         hipLaunchKernelGGL((kv_evict_kernel<256, 1>), grid, dim3(256), 0, stream, c, a, pl);
+    } else if (a.max_len <= 4096 && (int)grid.x <= cu_count) {
+        hipLaunchKernelGGL((kv_evict_kernel<512, 2>), grid, dim3(512), 0, stream, c, a, pl);
     } else if (a.max_len <= 4096) {
-        hipLaunchKernelGGL((kv_evict_kernel<1024, 1>), grid, dim3(1024), 0, stream, c, a, pl);
+        hipLaunchKernelGGL((kv_evict_kernel<256, 4>), grid, dim3(256), 0, stream, c, a, pl);
     } else if (!pl.parts) {
         hipLaunchKernelGGL((kv_evict_kernel<1024, 4>), grid, dim3(1024), 0, stream, c, a, pl);
     } else {

@@ -365,6 +365,10 @@ EVICT = [
     ([400, 90], 80, 80, 0, 2, 4, 128, BF16, "ties"), ([1030, 2000], 512, 16, 100, 2, 128, 128, FP8, "spread"),
     ([90, 64, 300], 33, 3, 5, 2, 16, 64, FP8, "odd"), ([129], 128, 0, 1, 4, 2, 256, FP8, "equal"),
     ([6000, 5000], 1500, 4, 200, 1, 64, 64, BF16, "ties"), ([70] * 40, 50, 2, 10, 2, 16, 64, BF16, "spread"),
+    # a few over the budget, one more than those, all of them equal or among equals
+    ([66, 67, 68, 69, 64, 65], 64, 0, 3, 2, 16, 64, BF16, "ties"), ([68, 69, 67], 65, 1, 0, 2, 16, 64, BF16, "equal"),
+    ([3000, 2003, 1999], 2000, 0, 1, 1, 64, 64, BF16, "odd"), ([5] * 300, 3, 0, 0, 1, 8, 64, BF16, "ties"),
+    ([2900] * 150, 2600, 4, 40, 2, 64, 64, BF16, "spread"),
     # longer than one workgroup ranks
     ([20000, 40001, 9000, 16384, 0], 12000, 4, 1000, 2, 64, 64, BF16, "spread"),
     ([70000, 30001], 30000, 16, 3000, 1, 128, 64, FP8, "ties"), ([33000, 21000], 20999, 0, 64, 1, 32, 64, BF16, "odd"),
