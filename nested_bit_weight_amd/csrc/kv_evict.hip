@@ -71,7 +71,7 @@ __device__ __forceinline__ uint32_t evict_key(float acc, int32_t pos, int32_t ne
 
 // `count` moves of one (row, head): the 16-byte pieces of each move's key and
 // value, and its total and position.
-template <int ROW_BYTES, int THREADS>
+template <int ROW_BYTES, int THREADS, bool NT>
 __device__ __forceinline__ void make_moves(const KvCache &c, const KvEvict &a, int row, int head, const int32_t *to,
                                            const int32_t *of, int count) {
     constexpr int VECS = ROW_BYTES / 16, AT_ONCE = 4;
@@ -98,9 +98,9 @@ __device__ __forceinline__ void make_moves(const KvCache &c, const KvEvict &a, i
         for (int j = 0; j < AT_ONCE; ++j)
             if (src[j] >= 0 && dst[j] >= 0) {
                 const int64_t at = src[j] * ROW_BYTES + (i0 + j * THREADS) % VECS * 16;
-                // read for the last time (12 rows, 16384 -> 4096: 77 us so, 85 otherwise)
-                k[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_kv *>(c.k + at));
-                v[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_kv *>(c.v + at));
+                const u32x4_kv *kp = reinterpret_cast<const u32x4_kv *>(c.k + at), *vp = reinterpret_cast<const u32x4_kv *>(c.v + at);
+                k[j] = NT ? __builtin_nontemporal_load(kp) : *kp;
+                v[j] = NT ? __builtin_nontemporal_load(vp) : *vp;
             }
 #pragma unroll
         for (int j = 0; j < AT_ONCE; ++j)
@@ -463,10 +463,10 @@ __global__ __launch_bounds__(THREADS) void kv_evict_kernel(KvCache c, KvEvict a,
     }
     __syncthreads();  // the lists are written
     switch (c.fp8 ? c.dim : 2 * c.dim) {
-    case 64: make_moves<64, THREADS>(c, a, row, head, to, of, movers); break;
-    case 128: make_moves<128, THREADS>(c, a, row, head, to, of, movers); break;
-    case 256: make_moves<256, THREADS>(c, a, row, head, to, of, movers); break;
-    default: make_moves<512, THREADS>(c, a, row, head, to, of, movers); break;
+    case 64: make_moves<64, THREADS, false>(c, a, row, head, to, of, movers); break;
+    case 128: make_moves<128, THREADS, false>(c, a, row, head, to, of, movers); break;
+    case 256: make_moves<256, THREADS, false>(c, a, row, head, to, of, movers); break;
+    default: make_moves<512, THREADS, false>(c, a, row, head, to, of, movers); break;
     }
 }
 
@@ -676,13 +676,13 @@ __global__ __launch_bounds__(PART_THREADS) void kv_evict_part_kernel(KvCache c, 
     if (first + PART >= n && tid == 0) pl.counts[which] = movers;
 }
 
-template <int ROW_BYTES>
+template <int ROW_BYTES, bool NT>
 __global__ __launch_bounds__(256) void kv_move_kernel(KvCache c, KvEvict a, EvictPlan pl, int parts) {
     const int which = blockIdx.x / parts, first = blockIdx.x % parts * MOVES;
     const int count = pl.counts[which];
     if (first >= count) return;
     const int32_t *to = pl.lists + (int64_t)which * 2 * pl.most;
-    make_moves<ROW_BYTES, 256>(c, a, which / c.heads, which % c.heads, to + first, to + pl.most + first,
+    make_moves<ROW_BYTES, 256, NT>(c, a, which / c.heads, which % c.heads, to + first, to + pl.most + first,
                                min(MOVES, count - first));
 }
 
@@ -719,6 +719,19 @@ int64_t kv_evict_workspace_bytes(const KvCache &c, int budget, int max_len) {
     return evict_plan(c, budget, max_len, nullptr, &pl);
 }
 
+template <int ROW_BYTES>
+static void launch_moves(const KvCache &c, const KvEvict &a, const EvictPlan &pl, hipStream_t stream) {
+    const int64_t lists = (int64_t)c.rows * c.heads, each = (pl.most + MOVES - 1) / MOVES;
+    const dim3 moves((unsigned)(lists * each)), threads(256);
+    // The rows are read for the last time.  Saying so pays where they are many, and
+    // costs where the caches still hold them: up to 201 MB of them 77 us so and 85
+    // otherwise, up to 34 MB 55 and 51.
+    if (lists * pl.most * 2 * ROW_BYTES > (int64_t)64 << 20)
+        hipLaunchKernelGGL((kv_move_kernel<ROW_BYTES, true>), moves, threads, 0, stream, c, a, pl, (int)each);
+    else
+        hipLaunchKernelGGL((kv_move_kernel<ROW_BYTES, false>), moves, threads, 0, stream, c, a, pl, (int)each);
+}
+
 hipError_t launch_kv_evict(const KvCache &c, const KvEvict &a, int cu_count, hipStream_t stream) {
     EvictPlan pl;
     evict_plan(c, a.budget, a.max_len, a.ws, &pl);
@@ -747,13 +760,11 @@ hipError_t launch_kv_evict(const KvCache &c, const KvEvict &a, int cu_count, hip
         hipLaunchKernelGGL(kv_evict_part_kernel<LIST>, parts, threads, 0, stream, c, a, pl);
     }
     if (pl.counts) {
-        const int each = (pl.most + MOVES - 1) / MOVES;
-        const dim3 moves((unsigned)((int64_t)grid.x * each));
         switch (c.fp8 ? c.dim : 2 * c.dim) {
-        case 64: hipLaunchKernelGGL(kv_move_kernel<64>, moves, dim3(256), 0, stream, c, a, pl, each); break;
-        case 128: hipLaunchKernelGGL(kv_move_kernel<128>, moves, dim3(256), 0, stream, c, a, pl, each); break;
-        case 256: hipLaunchKernelGGL(kv_move_kernel<256>, moves, dim3(256), 0, stream, c, a, pl, each); break;
-        default: hipLaunchKernelGGL(kv_move_kernel<512>, moves, dim3(256), 0, stream, c, a, pl, each); break;
+        case 64: launch_moves<64>(c, a, pl, stream); break;
+        case 128: launch_moves<128>(c, a, pl, stream); break;
+        case 256: launch_moves<256>(c, a, pl, stream); break;
+        default: launch_moves<512>(c, a, pl, stream); break;
         }
     }
     return hipGetLastError();

@@ -63,17 +63,23 @@ def declare(lib) -> None:
     lib.nbw_kv_evict_workspace_bytes.restype = _i64
 
 
-def _is(t, name: str, dtype, shape, device) -> int:
-    """Address of a contiguous tensor of this type, shape and device."""
+_BF16, _F32, _INT32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _is(t, name: str, dtype, shape, index: int) -> int:
+    """Address of a contiguous tensor of this type and shape on GPU number ``index``."""
+    try:
+        if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on GPU {index}, got {t.device}")
+    raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 class KVCache:
@@ -85,7 +91,7 @@ class KVCache:
     they live.  The numbers in the table may change between calls."""
 
     __slots__ = ("k", "v", "table", "k_scale", "v_scale", "view", "_ref", "rows", "heads", "page", "dim", "width",
-                 "capacity", "pages", "device", "_dev", "_track")
+                 "capacity", "pages", "device", "_dev", "_row", "_track", "_sizes")
 
     def __init__(self, k, v, table, k_scale=None, v_scale=None):
         for t, name in ((k, "k"), (v, "v"), (table, "table")):
@@ -98,8 +104,9 @@ class KVCache:
         if k.dim() != 4:
             raise ValueError("k must be [pages][heads][page][dim]")
         device = k.device
-        _is(k, "k", k.dtype, k.shape, device)
-        _is(v, "v", k.dtype, k.shape, device)
+        index = k.get_device()
+        _is(k, "k", k.dtype, k.shape, index)
+        _is(v, "v", k.dtype, k.shape, index)
         if table.dtype != torch.int32 or table.dim() != 2 or table.device != device:
             raise ValueError("table must be an int32 [rows][width] tensor on the pools' GPU")
         rows, width = table.shape
@@ -111,11 +118,12 @@ class KVCache:
             if fp8 != (t is not None):
                 raise ValueError(f"{name} goes with an 8-bit cache, and with no other")
             if fp8:
-                _is(t, name, torch.float32, (heads,), device)
+                _is(t, name, _F32, (heads,), index)
         self.k, self.v, self.table, self.k_scale, self.v_scale = k, v, table, k_scale, v_scale
         self.rows, self.width, self.pages, self.heads, self.page, self.dim = rows, width, pages, heads, page, dim
         self.capacity, self.device = width * page, device
-        self._dev = device.index if device.index is not None else torch.cuda.current_device()
+        self._dev, self._row = index, (rows,)
+        self._sizes = {}  # workspace bytes by the sizes that they depend on
         self._track = (rows, heads, self.capacity)
         self.view = KVView(k.data_ptr(), v.data_ptr(), pages, heads, page, dim, KV_DTYPES[k.dtype],
                            k_scale.data_ptr() if fp8 else None, v_scale.data_ptr() if fp8 else None,
@@ -126,23 +134,37 @@ class KVCache:
                              f"{rows} x {width} is outside what the library takes (dim 64, 128 or 256; pages of a "
                              f"power of two up to 4096 slots, 16-byte aligned; a row of at most 2^30 slots)")
 
-    def _heads(self, t, name: str, n: int, heads=None):
-        """Address, stride from one token to the next, and heads of a bf16 [n][heads][dim]
-        tensor, whose tokens may lie apart (a slice of a wider product)."""
+    def _heads(self, t, name: str, n: int, heads: int):
+        """Address of a bf16 [n][heads][dim] tensor and its stride from one token to the
+        next (0: dense); tokens may lie apart, as in a slice of a wider product."""
+        try:
+            if t.dtype is _BF16 and t.get_device() == self._dev and t.shape == (n, heads, self.dim):
+                if t.is_contiguous():
+                    return t.data_ptr(), 0
+                s0, s1, s2 = t.stride()
+                if s2 == 1 and (s1 == self.dim or heads == 1) and (s0 >= heads * self.dim or n == 1):
+                    return t.data_ptr(), s0 if n > 1 else 0
+        except AttributeError:
+            pass
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.dtype != torch.bfloat16:
             raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-        if t.device != self.device:
+        if t.get_device() != self._dev:
             raise ValueError(f"{name} must be on {self.device}, got {t.device}")
-        if t.dim() != 3 or t.shape[0] != n or t.shape[2] != self.dim or (heads is not None and t.shape[1] != heads):
-            raise ValueError(f"{name} must be [{n}][{'heads' if heads is None else heads}][{self.dim}], "
-                             f"got {tuple(t.shape)}")
-        s0, s1, s2 = t.stride()
-        h = t.shape[1]
-        if s2 != 1 or (h > 1 and s1 != self.dim) or (n > 1 and s0 < h * self.dim):
-            raise ValueError(f"{name} must have contiguous heads, one after the other")
-        return t.data_ptr(), s0 if n > 1 else 0, h
+        if t.shape != (n, heads, self.dim):
+            raise ValueError(f"{name} must be [{n}][{heads}][{self.dim}], got {tuple(t.shape)}")
+        raise ValueError(f"{name} must have contiguous heads, one after the other")
+
+    def _q_heads(self, q) -> int:
+        """Query heads of [tokens][q_heads][dim]: a multiple of the cache's."""
+        if not isinstance(q, torch.Tensor):
+            raise TypeError("q must be a torch.Tensor")
+        n = q.size(1) if q.dim() == 3 else 0
+        if n == 0 or n % self.heads:
+            raise ValueError(f"q must be [tokens][q_heads][{self.dim}] with q_heads a multiple of {self.heads}, "
+                             f"got {tuple(q.shape)}")
+        return n
 
     def attend_workspace_bytes(self, q_heads: int, max_len: int = 0, weights: bool = False) -> int:
         """Bytes of scratch kv_attend needs."""
@@ -152,14 +174,20 @@ class KVCache:
         """Bytes of scratch kv_evict needs."""
         return _bytes(_lib().nbw_kv_evict_workspace_bytes(self._ref, budget, max_len))
 
-    def _scratch(self, workspace, nbytes: int, stream: int):
+    def _scratch(self, workspace, query, sizes, stream: int):
+        """Address and size of a call's workspace; "auto": the binding's buffer, of the
+        bytes that ``query`` gives for ``sizes``."""
+        if workspace is None:
+            return None, 0
         if isinstance(workspace, str):
             if workspace != "auto":
                 raise ValueError("workspace must be 'auto', a tensor or None")
+            nbytes = self._sizes.get(sizes)
+            if nbytes is None:
+                nbytes = self._sizes[sizes] = _bytes(query(self._ref, *sizes))
             workspace = _workspace(self._dev, stream, nbytes)
-        if workspace is None:
-            return None, 0
-        if workspace.device != self.device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+        if workspace.get_device() != self._dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 tensor on the cache's GPU")
         return workspace.data_ptr(), workspace.numel()
 
@@ -182,45 +210,41 @@ def kv_append(cache: KVCache, k, v, lens, positions, *, q=None, cu=None, rope=No
     [tokens][q_heads][dim], normalised and rotated alongside into ``q_out`` (which may be q).
     ``pos`` and ``acc`` ([rows][heads][capacity], int32 and fp32) get the tokens' positions
     and zeros.  Returns (q_out or None, lens + new tokens)."""
-    tokens = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 3 else -1
-    device = cache.device
-    kp, k_ld, _ = cache._heads(k, "k", tokens, cache.heads)
-    vp, v_ld, _ = cache._heads(v, "v", tokens, cache.heads)
-    lens_p = _is(lens, "lens", torch.int32, (cache.rows,), device)
-    pos_p = _is(positions, "positions", torch.int32, (tokens,), device)
-    if cu is None:
-        if tokens != cache.rows:
-            raise ValueError(f"without cu there is one token for each of the {cache.rows} rows, got {tokens}")
-        cu_p = None
-    else:
-        cu_p = _is(cu, "cu", torch.int32, (cache.rows + 1,), device)
-    qp = qo = None
-    q_ld = qo_ld = q_heads = 0
+    if not isinstance(k, torch.Tensor):
+        raise TypeError("k must be a torch.Tensor")
+    tokens, rows, heads, index = k.size(0) if k.dim() else 0, cache.rows, cache.heads, cache._dev
+    kp, k_ld = cache._heads(k, "k", tokens, heads)
+    vp, v_ld = cache._heads(v, "v", tokens, heads)
+    qp = qo = cu_p = None
+    q_ld = qo_ld = q_heads = rope_rows = 0
+    if cu is not None:
+        cu_p = _is(cu, "cu", _INT32, (rows + 1,), index)
+    elif tokens != rows:
+        raise ValueError(f"without cu there is one token for each of the {rows} rows, got {tokens}")
     if q is not None:
-        qp, q_ld, q_heads = cache._heads(q, "q", tokens)
-        if q_heads == 0 or q_heads % cache.heads:
-            raise ValueError(f"q has {q_heads} heads, the cache {cache.heads}")
+        q_heads = cache._q_heads(q)
+        qp, q_ld = cache._heads(q, "q", tokens, q_heads)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
-        qo, qo_ld, _ = cache._heads(q_out, "q_out", tokens, q_heads)
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        qo, qo_ld = cache._heads(q_out, "q_out", tokens, q_heads)
     elif q_out is not None or q_norm is not None:
         raise ValueError("q_out and q_norm go with q")
-    rope_rows = 0
     if rope is not None:
-        rope_rows = rope.shape[0] if isinstance(rope, torch.Tensor) and rope.dim() == 2 else 0
+        rope_rows = rope.size(0) if isinstance(rope, torch.Tensor) and rope.dim() == 2 else 0
         if rope_rows < 1:
             raise ValueError("rope must be an fp32 [positions][dim] tensor")
     if lens_out is None:
-        lens_out = torch.empty(cache.rows, dtype=torch.int32, device=device)
+        lens_out = torch.empty(rows, dtype=_INT32, device=k.device)
     args = AppendArgs(
-        kp, vp, qp, qo, k_ld, v_ld, q_ld, qo_ld, tokens, q_heads, eps, cu_p, lens_p, pos_p,
-        None if rope is None else _is(rope, "rope", torch.float32, (rope_rows, cache.dim), device), rope_rows,
-        None if q_norm is None else _is(q_norm, "q_norm", torch.bfloat16, (cache.dim,), device),
-        None if k_norm is None else _is(k_norm, "k_norm", torch.bfloat16, (cache.dim,), device),
-        None if pos is None else _is(pos, "pos", torch.int32, cache._track, device),
-        None if acc is None else _is(acc, "acc", torch.float32, cache._track, device),
-        _is(lens_out, "lens_out", torch.int32, (cache.rows,), device))
-    st = _lib().nbw_kv_append(cache._ref, ctypes.byref(args), _raw_stream(cache._dev))
+        kp, vp, qp, qo, k_ld, v_ld, q_ld, qo_ld, tokens, q_heads, eps, cu_p, _is(lens, "lens", _INT32, cache._row, index),
+        _is(positions, "positions", _INT32, (tokens,), index),
+        None if rope is None else _is(rope, "rope", _F32, (rope_rows, cache.dim), index), rope_rows,
+        None if q_norm is None else _is(q_norm, "q_norm", _BF16, (cache.dim,), index),
+        None if k_norm is None else _is(k_norm, "k_norm", _BF16, (cache.dim,), index),
+        None if pos is None else _is(pos, "pos", _INT32, cache._track, index),
+        None if acc is None else _is(acc, "acc", _F32, cache._track, index),
+        _is(lens_out, "lens_out", _INT32, cache._row, index))
+    st = _lib().nbw_kv_append(cache._ref, ctypes.byref(args), _raw_stream(index))
     if st:
         _check(st, "nbw_kv_append")
     return q_out, lens_out
@@ -237,33 +261,30 @@ def kv_attend(cache: KVCache, q, lens, *, scale: float | None = None, out=None, 
     a bound of the lengths, if one below the capacity is known.  ``workspace``: "auto" (the
     binding's buffer of this device and stream), or a uint8 tensor of at least
     ``cache.attend_workspace_bytes(...)`` bytes, as a captured graph should have."""
-    rows, device = cache.rows, cache.device
-    qp, q_ld, q_heads = cache._heads(q, "q", rows)
-    if q_heads == 0 or q_heads % cache.heads:
-        raise ValueError(f"q has {q_heads} heads, the cache {cache.heads}")
-    if scale is not None and not 0.0 < abs(scale) < 3e38:
+    index = cache._dev
+    q_heads = cache._q_heads(q)
+    qp, q_ld = cache._heads(q, "q", cache.rows, q_heads)
+    if scale is None:
+        scale = 0.0
+    elif not 0.0 < abs(scale) < 3e38:
         raise ValueError("scale must be finite and not 0")
-    lens_p = _is(lens, "lens", torch.int32, (rows,), device)
+    if max_len is None:
+        max_len = 0
+    elif max_len < 1:
+        raise ValueError("max_len must be at least 1")
     if out is None:
-        out = torch.empty((rows, q_heads, cache.dim), dtype=torch.bfloat16, device=device)
-    op, out_ld, _ = cache._heads(out, "out", rows, q_heads)
+        out = torch.empty(q.shape, dtype=_BF16, device=q.device)
+    op, out_ld = cache._heads(out, "out", cache.rows, q_heads)
     acc_p = acc_o = None
     if acc is not None:
-        acc_p = _is(acc, "acc", torch.float32, cache._track, device)
-        acc_o = acc_p if acc_out is None else _is(acc_out, "acc_out", torch.float32, cache._track, device)
+        acc_p = _is(acc, "acc", _F32, cache._track, index)
+        acc_o = acc_p if acc_out is None else _is(acc_out, "acc_out", _F32, cache._track, index)
     elif acc_out is not None:
         raise ValueError("acc_out goes with acc")
-    most = 0
-    if max_len is not None:
-        if max_len < 1:
-            raise ValueError("max_len must be at least 1")
-        most = max_len
-    stream = _raw_stream(cache._dev)
-    lib = _lib()
-    nbytes = lib.nbw_kv_attend_workspace_bytes(cache._ref, q_heads, most, acc is not None)
-    ws, ws_bytes = cache._scratch(workspace, nbytes, stream)
-    args = AttendArgs(qp, op, q_ld, out_ld, q_heads, 0.0 if scale is None else scale, lens_p, most, acc_p, acc_o,
-                      decay, ws, ws_bytes)
+    lib, stream = _lib(), _raw_stream(index)
+    ws, ws_bytes = cache._scratch(workspace, lib.nbw_kv_attend_workspace_bytes, (q_heads, max_len, acc is not None), stream)
+    args = AttendArgs(qp, op, q_ld, out_ld, q_heads, scale, _is(lens, "lens", _INT32, cache._row, index), max_len, acc_p,
+                      acc_o, decay, ws, ws_bytes)
     st = lib.nbw_kv_attend(cache._ref, ctypes.byref(args), stream)
     if st:
         _check(st, "nbw_kv_attend")
@@ -279,29 +300,23 @@ def kv_evict(cache: KVCache, acc, pos, lens, budget: int, *, sink: int = 0, rece
     into the ones below it that go, in the pools, in ``acc_out`` and in ``pos_out`` (buffers
     of their own, of the same shapes).  Returns min(lens, budget) in ``lens_out``.
     ``max_len`` and ``workspace`` as for :func:`kv_attend`."""
-    device = cache.device
-    most = 0
-    if max_len is not None:
-        if max_len < 1:
-            raise ValueError("max_len must be at least 1")
-        most = max_len
+    index, track = cache._dev, cache._track
+    if max_len is None:
+        max_len = 0
+    elif max_len < 1:
+        raise ValueError("max_len must be at least 1")
     if not 1 <= budget <= cache.capacity:
         raise ValueError(f"budget must be within 1..{cache.capacity}, got {budget}")
     if sink < 0 or recent < 0 or sink + recent > budget:
         raise ValueError("sink and recent must not be negative, nor more than the budget together")
-    acc_p = _is(acc, "acc", torch.float32, cache._track, device)
-    pos_p = _is(pos, "pos", torch.int32, cache._track, device)
-    lens_p = _is(lens, "lens", torch.int32, (cache.rows,), device)
-    acc_o = _is(acc_out, "acc_out", torch.float32, cache._track, device)
-    pos_o = _is(pos_out, "pos_out", torch.int32, cache._track, device)
     if lens_out is None:
-        lens_out = torch.empty(cache.rows, dtype=torch.int32, device=device)
-    lens_o = _is(lens_out, "lens_out", torch.int32, (cache.rows,), device)
-    stream = _raw_stream(cache._dev)
-    lib = _lib()
-    nbytes = lib.nbw_kv_evict_workspace_bytes(cache._ref, budget, most)
-    ws, ws_bytes = cache._scratch(workspace, nbytes, stream)
-    args = EvictArgs(acc_p, pos_p, lens_p, budget, sink, recent, acc_o, pos_o, lens_o, most, ws, ws_bytes)
+        lens_out = torch.empty(cache.rows, dtype=_INT32, device=cache.device)
+    lib, stream = _lib(), _raw_stream(index)
+    ws, ws_bytes = cache._scratch(workspace, lib.nbw_kv_evict_workspace_bytes, (budget, max_len), stream)
+    args = EvictArgs(_is(acc, "acc", _F32, track, index), _is(pos, "pos", _INT32, track, index),
+                     _is(lens, "lens", _INT32, cache._row, index), budget, sink, recent,
+                     _is(acc_out, "acc_out", _F32, track, index), _is(pos_out, "pos_out", _INT32, track, index),
+                     _is(lens_out, "lens_out", _INT32, cache._row, index), max_len, ws, ws_bytes)
     st = lib.nbw_kv_evict(cache._ref, ctypes.byref(args), stream)
     if st:
         _check(st, "nbw_kv_evict")
