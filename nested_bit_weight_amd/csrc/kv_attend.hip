@@ -105,6 +105,9 @@ __device__ __forceinline__ Parts parts_of(const KvCache &c, const AttendPlan &pl
     return {owner_of(seg0 + chunks - 1, units, shares) - w0 + 1, w0, 1};
 }
 
+// Tiles whose scores a wave holds back.
+__host__ __device__ constexpr int most_held(int block_heads) { return HELD_SCORES / (TILE * block_heads); }
+
 // One wave's tile: keys and values as loaded, and which slots count.
 template <int DIM, bool FP8>
 struct Tile {
@@ -147,6 +150,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, p);
 }
 
+// acc_out = decay * acc + w for slots slot .. slot + 3 below n of the (row, head) at `base`.
+__device__ __forceinline__ void add_totals(const KvAttend &a, int64_t base, int slot, int n, f32x4_kv w, bool vec) {
+    const float *acc = a.acc + base + slot;
+    float *out = a.acc_out + base + slot;
+    if (vec && slot + 4 <= n) {
+        const f32x4_kv was = *reinterpret_cast<const f32x4_kv *>(acc);
+        *reinterpret_cast<f32x4_kv *>(out) = was * a.decay + w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (slot + e < n) out[e] = a.decay * acc[e] + w[e];
+    }
+}
+
 template <int DIM, bool FP8, bool PACK, bool SMALL, bool NT, bool WEIGHTS>
 __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_kernel(KvCache c, KvAttend a, AttendPlan pl) {
     using T = Tile<DIM, FP8>;
@@ -156,13 +173,13 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
     constexpr int QF = DIM / 32;                      // Q operands
     __shared__ int scan[ATTEND_WAVES];
     __shared__ int found[2];
-    __shared__ float wave_ml[ATTEND_WAVES][HR][2];
-    // The waves' results at the end of a piece; before that, with totals, the scores
-    // of each wave's last tiles.
+    __shared__ float wave_ml[ATTEND_WAVES][HR][2], head_ml[HR][2];
+    // Each wave's results at the end of a piece; before that, with totals, the scores
+    // of its last tiles.
     constexpr int POOL = WEIGHTS ? HELD_SCORES : HR * COLS;  // a wave's
     static_assert(HELD_SCORES >= 16 * 128, "the results fit");
     __shared__ __align__(16) float pool[ATTEND_WAVES * POOL];
-    auto wave_o = [&](int w, int h, int d) -> float & { return pool[(w * HR + h) * COLS + d]; };
+    auto wave_o = [&](int w, int h, int d) -> float & { return pool[w * POOL + h * COLS + d]; };
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int quad = lane >> 4, col = lane & 15;
     const int vheads = c.heads * pl.blocks;
@@ -178,7 +195,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
     if (pl.undivided) {
         row = blockIdx.x / vheads;
         vh = blockIdx.x % vheads;
-        len = __builtin_amdgcn_readfirstlane(kv_len(a.lens, row, a.max_len));
+        len = min(max(uniform_word(a.lens + row), 0), a.max_len);
         row_chunks = chunks_of(len);
         c0 = 0;
         c1 = row_chunks;
@@ -316,20 +333,22 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
             }
         }
 
-        // Page numbers of the tile at `slot`.  Pages of 16 slots and more: one for
-        // each half, the same in all lanes; smaller ones: lane l has slot l % 32's.
+        // Page numbers of a chunk's tile.  Pages of 16 slots and more: one for each
+        // half, the same in all lanes; smaller ones: lane l has slot l % 32's.  Past the
+        // row's length they are whatever the table holds, and what is loaded by them
+        // (from a page of the pool in any case) is left out: the first tile's loads
+        // need not wait for the length.
         struct Pages { int32_t p[SMALL ? 1 : 2]; };
         auto pages_of = [&](int chunk) {
             Pages r;
             const int slot = chunk * CHUNK + wave * TILE;
             if constexpr (SMALL) {
                 const int s = slot + (lane & 31);
-                r.p[0] = table[min(s, len - 1) >> c.page_log2];
-                if (s >= len) r.p[0] = -1;
+                r.p[0] = table[min(s, c.cap - 1) >> c.page_log2];
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    r.p[h] = uniform_word(table + (min(slot + 16 * h, len - 1) >> c.page_log2));
+                    r.p[h] = uniform_word(table + (min(slot + 16 * h, c.cap - 1) >> c.page_log2));
             }
             return r;
         };
@@ -354,7 +373,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint8_t *q = c.v + place(16 * h + quad * 4 + i, ok) + col * T::VW * 4;
-                        t.there |= (uint32_t)ok << (4 * h + i);
+                        t.there |= (uint32_t)(ok && slot + 16 * h + quad * 4 + i < len) << (4 * h + i);
 #pragma unroll
                         for (int n = 0; n < T::NC; ++n) load_words<NT, T::VW>(t.v[h][i][n], q + n * (ROW_BYTES / T::NC));
                     }
@@ -363,7 +382,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int s = slot + 16 * h;
-                    const bool ok = s < len && (uint32_t)pg.p[h] < (uint32_t)c.pages;
+                    const bool ok = (uint32_t)pg.p[h] < (uint32_t)c.pages;
                     const int left = ok ? min(len - s, 16) - quad * 4 : 0;
                     t.there |= (left >= 4 ? 15u : left <= 0 ? 0u : (1u << left) - 1) << (4 * h);
                     const int64_t base = ((((int64_t)(ok ? pg.p[h] : 0) * c.heads + head) << c.page_log2) + (s & mask)) * ROW_BYTES;
@@ -392,7 +411,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
         // waited for the last one's to reach memory (64 rows, 1.2 GB: 250 us, and 200
         // without the stores).
         float *scores = pool + wave * POOL;
-        const int most_held = HELD_SCORES / (TILE * pl.block_heads);
+        const int most_held = nbw::most_held(pl.block_heads);
         int held = 0;
         auto put_scores = [&](int chunk) {  // up to this chunk's
             const int each = TILE / 4 * pl.block_heads;  // 16-byte pieces of a tile
@@ -434,7 +453,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
                     *reinterpret_cast<f32x4_kv *>(dst) = f32x4_kv{x[0], x[1], x[2], x[3]};
                     *reinterpret_cast<f32x4_kv *>(dst + 16 * pl.block_heads) = f32x4_kv{x[4], x[5], x[6], x[7]};
                 }
-                if (++held == most_held) put_scores(chunk);
+                if (++held == most_held && chunk + 1 < c1) put_scores(chunk);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
@@ -531,7 +550,10 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
             }
         }
 
-        if (WEIGHTS && held) put_scores(c1 - 1);
+        // With all of its row's scores still in LDS a workgroup adds to the totals itself.
+        const bool whole = c0 == 0 && c1 == row_chunks;
+        const bool totals = WEIGHTS && whole && pl.blocks == 1 && c1 <= most_held;
+        if (WEIGHTS && !totals) put_scores(c1 - 1);
 
         // The four waves' results together.
         sum += __shfl_xor(sum, 16);
@@ -541,7 +563,6 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
             wave_ml[wave][lane][1] = sum;
         }
         __syncthreads();
-        const bool whole = c0 == 0 && c1 == row_chunks;
         auto merged = [&](int h, float &top, float &total) {
             top = NEG_INF;
             total = 0.f;
@@ -568,10 +589,30 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
             if (!whole) {
                 pl.part_ml[(part * 16 + tid) * 2] = top;
                 pl.part_ml[(part * 16 + tid) * 2 + 1] = total;
+            } else if (totals) {
+                head_ml[tid][0] = top == NEG_INF ? 0.f : top;
+                head_ml[tid][1] = total == 0.f ? 0.f : 1.f / total;
             } else if (WEIGHTS) {
                 float *w = pl.whole + (((int64_t)row * vheads + vh) * 16 + tid) * 2;
                 w[0] = top;
                 w[1] = total;
+            }
+        }
+        if (totals) {
+            __syncthreads();
+            const int64_t base = ((int64_t)row * c.heads + head) * c.cap;
+            for (int i = lane; i < c1 * 8; i += 64) {  // four slots of this wave's tiles
+                const int slot = i / 8 * CHUNK + wave * TILE + i % 8 * 4;
+                if (slot >= len) continue;
+                const float *s = scores + i * 4 * pl.block_heads;
+                f32x4_kv w = {0.f, 0.f, 0.f, 0.f};
+                for (int h = 0; h < heads; ++h) {
+                    const f32x4_kv x = *reinterpret_cast<const f32x4_kv *>(s + h * 4);
+                    const float hm = head_ml[h][0], hi = head_ml[h][1];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] += __builtin_amdgcn_exp2f(x[e] - hm) * hi;
+                }
+                add_totals(a, base, slot, len, w, pl.vec);
             }
         }
 #pragma unroll
@@ -623,6 +664,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
 }
 
 constexpr int JOIN_THREADS = 256;
+constexpr int FEW_PARTS = 6;
 
 // The second launch.  The first `sharers` workgroups add the weights to the
 // totals, each for an equal share of the units of (row, head, chunk); the rows *
@@ -697,39 +739,54 @@ __global__ __launch_bounds__(JOIN_THREADS) void kv_join_kernel(KvCache c, KvAtte
         const int head = (int)((t - row0) / chunks), c0 = (int)((t - row0) % chunks);
         const int c1 = (int)min((int64_t)chunks, c0 + (t1 - t));
         const int n = kv_len(a.lens, row, a.max_len);
+        if (pl.blocks == 1 && chunks <= most_held(pl.block_heads) && parts_of(c, pl, row, head, at, chunks).n == 1) {
+            t += c1 - c0;  // its workgroup did it
+            if (head == c.heads - 1 && c1 == chunks) ++row;
+            continue;
+        }
         __syncthreads();
-        if (tid < pl.group) {  // each query head's m and 1 / sum over all of its parts
-            const int block = tid / pl.block_heads, h = tid % pl.block_heads;
-            const Parts parts = parts_of(c, pl, row, head * pl.blocks + block, at, chunks);
+        // Each query head's m and 1 / sum over all of its parts: a thread for a head where
+        // there are few parts, else a wave.  (4 rows of up to 4000 slots, 16 parts and
+        // more: 23 us with waves, 35 with threads.)
+        const Parts some = parts_of(c, pl, row, head * pl.blocks, at, chunks);
+        const bool few = some.n <= FEW_PARTS;
+        const int lane = tid & 63, width = few ? 1 : 64;
+        for (int g = few ? tid : tid >> 6; g < pl.group; g += JOIN_THREADS / width) {
+            const int block = g / pl.block_heads, h = g % pl.block_heads;
+            const Parts parts = block ? parts_of(c, pl, row, head * pl.blocks + block, at, chunks) : some;
+            const float *one = pl.whole + (((int64_t)row * vheads + head * pl.blocks + block) * 16 + h) * 2;
             float m = NEG_INF, l = 0.f;
-            if (parts.n == 1) {
-                const float *w = pl.whole + (((int64_t)row * vheads + head * pl.blocks + block) * 16 + h) * 2;
-                m = w[0];
-                l = w[1];
+            auto take = [&](int i) {
+                const float *p = parts.n == 1 ? one : pl.part_ml + (parts.place(i) * 16 + h) * 2;
+                const float pm = p[0], ps = p[1], top = fmaxf(m, pm);
+                l = l * (m == top ? 1.f : exp2f(m - top)) + ps * (pm == top ? 1.f : exp2f(pm - top));
+                m = top;
+            };
+            float top;
+            if (few) {
+                for (int i = 0; i < parts.n; ++i) take(i);
+                top = m;
             } else {
-                for (int i = 0; i < parts.n; ++i) m = fmaxf(m, pl.part_ml[(parts.place(i) * 16 + h) * 2]);
-                for (int i = 0; i < parts.n; ++i) {
-                    const float *p = pl.part_ml + (parts.place(i) * 16 + h) * 2;
-                    l += p[1] * (p[0] == m ? 1.f : exp2f(p[0] - m));
-                }
+                for (int i = lane; i < parts.n; i += 64) take(i);
+                top = m;
+#pragma unroll
+                for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+                l *= m == top ? 1.f : exp2f(m - top);
+#pragma unroll
+                for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
             }
-            head_m[tid] = m == NEG_INF ? 0.f : m;
-            head_inv[tid] = l == 0.f ? 0.f : 1.f / l;
+            if (few || lane == 0) {
+                head_m[g] = top == NEG_INF ? 0.f : top;
+                head_inv[g] = l == 0.f ? 0.f : 1.f / l;
+            }
         }
         __syncthreads();
         // Four slots of a thread, 32 threads of a unit.
         const int64_t base = ((int64_t)row * c.heads + head) * c.cap;
-        const bool vec = pl.vec;
         for (int i = tid; i < (c1 - c0) * (CHUNK / 4); i += JOIN_THREADS) {
             const int chunk = c0 + i / (CHUNK / 4), in = i % (CHUNK / 4), slot = chunk * CHUNK + in * 4;
             if (slot >= n) continue;
-            f32x4_kv was = {0.f, 0.f, 0.f, 0.f}, w = {0.f, 0.f, 0.f, 0.f};
-            const bool whole = vec && slot + 4 <= n;
-            if (whole) was = *reinterpret_cast<const f32x4_kv *>(a.acc + base + slot);
-            else
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (slot + e < n) was[e] = a.acc[base + slot + e];
+            f32x4_kv w = {0.f, 0.f, 0.f, 0.f};
             for (int b = 0; b < pl.blocks; ++b) {
                 const int heads = min(pl.block_heads, pl.group - b * pl.block_heads);
                 const int64_t unit = (int64_t)at * vheads + (int64_t)(head * pl.blocks + b) * chunks + chunk;
@@ -746,13 +803,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void kv_join_kernel(KvCache c, KvAtte
                             for (int e = 0; e < 4; ++e) w[e] += __builtin_amdgcn_exp2f(x[h][e] - hm[h0 + h]) * hi[h0 + h];
                 }
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] += a.decay * was[e];
-            if (whole) *reinterpret_cast<f32x4_kv *>(a.acc_out + base + slot) = w;
-            else
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (slot + e < n) a.acc_out[base + slot + e] = w[e];
+            add_totals(a, base, slot, n, w, pl.vec);
         }
         t += c1 - c0;
         if (head == c.heads - 1 && c1 == chunks) ++row;
@@ -769,13 +820,18 @@ static int64_t attend_plan(const KvCache &c, int q_heads, int max_len, bool weig
     const int64_t most = c.rows * vheads * chunks;
     if (most > INT32_MAX) return -1;
     // As many workgroups as run at once: two on a CU, one at 256 dims (registers).
-    // Rows of up to four units are not divided: a workgroup's steps 2 to 4 take about
-    // as long as the second launch that joins parts.
-    pl->undivided = chunks <= 4 && !weights;
     pl->wgs = (int)std::max<int64_t>(1, std::min<int64_t>(most, (int64_t)cu_count * (c.dim > 128 ? 1 : 2)));
+    // One workgroup for each (row, head), undivided, where rows are short: up to four
+    // units, whose steps 2 to 4 take about as long as the second launch that joins
+    // parts; and up to about eight for each time that the workgroups fill the device,
+    // when the last ones to run are a small share of all.  (96 rows of up to 600 slots,
+    // 8 heads: 30 us so, 49 us in equal shares.)  With totals the scores of a row have
+    // to stay in LDS.
+    pl->undivided = chunks <= 4 || (c.rows * vheads >= pl->wgs && chunks <= 8 * c.rows * vheads / pl->wgs);
+    if (weights && (pl->blocks > 1 || chunks > most_held(pl->block_heads))) pl->undivided = 0;
     if (pl->undivided) pl->wgs = (int)(c.rows * vheads);
     // Totals: eight units for each step of a workgroup, and a few workgroups for each CU.
-    pl->sharers = weights ? (int)std::max<int64_t>(1, std::min<int64_t>((most + 7) / 8, (int64_t)cu_count * 8)) : 0;
+    pl->sharers = weights ? (int)std::max<int64_t>(1, std::min<int64_t>((most + 7) / 8, (int64_t)cu_count * 4)) : 0;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         uint8_t *p = base ? base + at : nullptr;
@@ -805,9 +861,9 @@ int64_t kv_attend_workspace_bytes(const KvCache &c, int q_heads, int max_len, bo
 template <int DIM, bool FP8, bool PACK, bool SMALL>
 static void launch_attend(const KvCache &c, const KvAttend &a, const AttendPlan &pl, bool once, hipStream_t stream) {
     const dim3 grid(pl.wgs), threads(ATTEND_THREADS);
-    if (once && pl.scores) hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, PACK, SMALL, true, true>), grid, threads, 0, stream, c, a, pl);
+    if (once && a.acc) hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, PACK, SMALL, true, true>), grid, threads, 0, stream, c, a, pl);
     else if (once) hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, PACK, SMALL, true, false>), grid, threads, 0, stream, c, a, pl);
-    else if (pl.scores) hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, PACK, SMALL, false, true>), grid, threads, 0, stream, c, a, pl);
+    else if (a.acc) hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, PACK, SMALL, false, true>), grid, threads, 0, stream, c, a, pl);
     else hipLaunchKernelGGL((kv_attend_kernel<DIM, FP8, PACK, SMALL, false, false>), grid, threads, 0, stream, c, a, pl);
     if (!pl.undivided)
         hipLaunchKernelGGL((kv_join_kernel<DIM>), dim3((unsigned)(c.rows * a.q_heads + pl.sharers)), dim3(JOIN_THREADS), 0,

@@ -131,6 +131,9 @@ ATTEND = [
     ([1, 0, 33, 200], 2, 4, 16, 128, FP8), ([999, 64], 8, 8, 64, 128, FP8), ([300, 129], 2, 12, 32, 64, FP8),
     ([257, 31], 2, 2, 8, 256, FP8), ([222], 1, 17, 1, 128, FP8), ([4000, 5, 2500], 2, 8, 128, 128, BF16),
     ([64] * 70, 1, 2, 16, 64, BF16), ([150, 0] * 150, 1, 1, 32, 128, BF16),
+    # every (row, head) a workgroup's, with and without its totals; more rows than a wave has lanes, divided
+    ([700, 20, 300] * 33, 8, 2, 16, 64, BF16), ([900] * 30, 20, 1, 64, 64, FP8), ([1500, 70] * 5, 2, 16, 64, 64, BF16),
+    ([3000] + [10] * 69, 2, 3, 32, 64, BF16), ([2000, 0, 900], 1, 40, 128, 64, BF16),
 ]
 
 
@@ -501,8 +504,11 @@ def test_refusals(nbw):
         nbw.kv_attend(s.cache, q.transpose(0, 1).contiguous().transpose(0, 1), s.lens)
     with pytest.raises(ValueError):
         nbw.kv_attend(s.cache, q, s.lens, scale=0.0)
+    long = Setup(nbw, [3000, 30], heads=2, page=64)
     with pytest.raises(nbw.NBWError):
-        nbw.kv_attend(s.cache, q, s.lens, acc=acc, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+        nbw.kv_attend(long.cache, q, long.lens, acc=long.totals(), workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(nbw.NBWError):
+        nbw.kv_attend(long.cache, q, long.lens, workspace=None)
     with pytest.raises(ValueError):
         nbw.kv_append(s.cache, k[:1], k[:1], s.lens, positions[:1])
     with pytest.raises(ValueError):
