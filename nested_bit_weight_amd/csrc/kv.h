@@ -90,6 +90,37 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // fp32 to bf16, to nearest even; a NaN stays one.
 __device__ __forceinline__ uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
+// Sums and other reductions over the 64 lanes of a wave, in six register-to-register
+// steps: within rows of 16 lanes, from each row into the next, from the lower half
+// into the upper.  (These sit on paths that small calls wait for; general shuffles go
+// through LDS.  16 rows' attention 18.3 -> 17.8 us, ranking 120001 slots 56 -> 53.)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int32_t from_lane(int32_t none, int32_t x) {
+    return __builtin_amdgcn_update_dpp(none, x, CTRL, ROWS, 0xF, false);
+}
+template <class Op>
+__device__ __forceinline__ int32_t wave_running(int32_t x, int32_t none, Op op) {  // over this lane and those before it
+    x = op(x, from_lane<0x111, 0xF>(none, x));
+    x = op(x, from_lane<0x112, 0xF>(none, x));
+    x = op(x, from_lane<0x114, 0xF>(none, x));
+    x = op(x, from_lane<0x118, 0xF>(none, x));
+    x = op(x, from_lane<0x142, 0xA>(none, x));
+    return op(x, from_lane<0x143, 0xC>(none, x));
+}
+template <class Op>
+__device__ __forceinline__ int32_t wave_all(int32_t x, int32_t none, Op op) {  // over all lanes, in each of them
+    return __builtin_amdgcn_readlane(wave_running(x, none, op), 63);
+}
+struct OpSum { __device__ __forceinline__ int32_t operator()(int32_t a, int32_t b) const { return a + b; } };
+struct OpMax { __device__ __forceinline__ int32_t operator()(int32_t a, int32_t b) const { return a > b ? a : b; } };
+struct OpMaxU { __device__ __forceinline__ int32_t operator()(int32_t a, int32_t b) const { return (uint32_t)a > (uint32_t)b ? a : b; } };
+struct OpMinU { __device__ __forceinline__ int32_t operator()(int32_t a, int32_t b) const { return (uint32_t)a < (uint32_t)b ? a : b; } };
+__device__ __forceinline__ int32_t wave_running_sum(int32_t x) { return wave_running(x, 0, OpSum()); }
+__device__ __forceinline__ int32_t wave_sum(int32_t x) { return wave_all(x, 0, OpSum()); }
+__device__ __forceinline__ int32_t wave_max(int32_t x) { return wave_all(x, INT32_MIN, OpMax()); }
+__device__ __forceinline__ uint32_t wave_max_u(uint32_t x) { return (uint32_t)wave_all((int32_t)x, 0, OpMaxU()); }
+__device__ __forceinline__ uint32_t wave_min_u(uint32_t x) { return (uint32_t)wave_all((int32_t)x, -1, OpMinU()); }
+
 // Four fp32 values, already divided by the head's factor, to the cache's 8 bits:
 // limited to the largest finite value and rounded to nearest even, NaN kept.
 __device__ __forceinline__ uint32_t to_fp8x4(float a, float b, float c, float d) {

@@ -218,15 +218,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
         } else {
             for (int r = r0; r < r1; ++r) mine += chunks_of(kv_len(a.lens, r, a.max_len));
         }
-        auto running = [&](int x) {  // the sum over this lane and those before it
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int y = __shfl_up(x, d);
-                if (lane >= d) x += y;
-            }
-            return x;
-        };
-        int upto = running(mine), chunks = __builtin_amdgcn_readlane(upto, 63);
+        int upto = wave_running_sum(mine), chunks = __builtin_amdgcn_readlane(upto, 63);
         if (!few) {
             if (lane == 63) scan[wave] = upto;
             __syncthreads();
@@ -247,7 +239,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
         if (few && units) {
             const int share = (int)((units + pl.wgs - 1) / pl.wgs);
             for (int t = share; t <= share + 1 && !k; ++t) {
-                pieces = running((mine + t - 1) / t);
+                pieces = wave_running_sum((mine + t - 1) / t);
                 if ((int64_t)__builtin_amdgcn_readlane(pieces, 63) * vheads <= pl.wgs) k = t;
             }
         }

@@ -163,12 +163,7 @@ __device__ __forceinline__ void find_bin(const int *hist, int want, int *red, in
         count[i] = hist[EVICT_BINS - 1 - (tid * PER + i)];
         mine += count[i];
     }
-    int upto = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int x = __shfl_up(upto, d);
-        if (lane >= d) upto += x;
-    }
+    int upto = wave_running_sum(mine);
     if (lane == 63) red[wave] = upto;
     __syncthreads();
 #pragma unroll
@@ -218,14 +213,9 @@ __device__ __forceinline__ int list_moves(const uint32_t (&key)[GROUPS][4], int 
 #pragma unroll
             for (int i0 = 0; i0 < TAB; i0 += 64) {
                 const int i = i0 + lane, x = i < TAB ? tab[wave][i] : 0;
-                int s = x;
-#pragma unroll
-                for (int d = 1; d < 64; d <<= 1) {
-                    const int up = __shfl_up(s, d);
-                    if (lane >= d) s += up;
-                }
+                const int s = wave_running_sum(x);
                 if (i < TAB) tab[wave][i] = carry + s - x;
-                carry += __shfl(s, 63);
+                carry += __builtin_amdgcn_readlane(s, 63);
             }
             if (lane == 0) tab[wave][TAB] = carry;
         }
@@ -326,8 +316,7 @@ __global__ __launch_bounds__(THREADS) void kv_evict_kernel(KvCache c, KvEvict a,
         for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
             for (int e = 0; e < 4; ++e) newest = max(newest, y[g].v[e]);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) newest = max(newest, __shfl_xor(newest, d));
+        newest = wave_max(newest);
         if (lane == 0) red[0][wave] = newest;
         __syncthreads();
 #pragma unroll
@@ -361,16 +350,19 @@ __global__ __launch_bounds__(THREADS) void kv_evict_kernel(KvCache c, KvEvict a,
         for (int i = 0; i < FEW_OUT; ++i) {
             out[i] = INT32_MAX;
             if (i >= n - b) continue;
-            uint64_t m = ~0ull;
+            uint32_t low = ~0u, rest = ~0u;  // the key, and how far its slot is from the end
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = slot_of(g) + e;
-                    if (key[g][e]) m = min(m, (uint64_t)key[g][e] << 32 | (uint32_t)(INT32_MAX - j));
-                }
+                for (int e = 0; e < 4; ++e)
+                    if (key[g][e]) low = min(low, key[g][e]);
+            low = wave_min_u(low);
 #pragma unroll
-            for (int d = 1; d < 64; d <<= 1) m = min(m, (uint64_t)__shfl_xor((unsigned long long)m, d));
+            for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (key[g][e] == low) rest = (uint32_t)(INT32_MAX - (slot_of(g) + e));  // slots ascend
+            uint64_t m = (uint64_t)low << 32 | wave_min_u(rest);
             if (lane == 0) least[i][wave] = m;
             __syncthreads();
 #pragma unroll
@@ -406,12 +398,9 @@ __global__ __launch_bounds__(THREADS) void kv_evict_kernel(KvCache c, KvEvict a,
         }
     } else {
         __syncthreads();
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            inf += __shfl_xor(inf, d);
-            lo = min(lo, (uint32_t)__shfl_xor((int)lo, d));
-            hi = max(hi, (uint32_t)__shfl_xor((int)hi, d));
-        }
+        inf = wave_sum(inf);
+        lo = wave_min_u(lo);
+        hi = wave_max_u(hi);
         if (lane == 0) {
             red[0][wave] = inf;
             red[1][wave] = (int)lo;
@@ -527,8 +516,7 @@ __global__ __launch_bounds__(PART_THREADS) void kv_evict_part_kernel(KvCache c, 
 #pragma unroll
             for (int e = 0; e < 4; ++e) newest = max(newest, y.v[e]);
         }
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) newest = max(newest, __shfl_xor(newest, d));
+        newest = wave_max(newest);
         if (lane == 0) red[0][wave] = newest;
         __syncthreads();
 #pragma unroll
@@ -548,8 +536,7 @@ __global__ __launch_bounds__(PART_THREADS) void kv_evict_part_kernel(KvCache c, 
         for (int g = 0; g < GROUPS; ++g) x[g] = four(a.acc + base, slot_of(g), n, 0.f, pl.vec);
         int32_t newest = INT32_MIN;
         for (int i = tid; i < pl.parts; i += THREADS) newest = max(newest, pl.newest[(int64_t)which * pl.parts + i]);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) newest = max(newest, __shfl_xor(newest, d));
+        newest = wave_max(newest);
         if (lane == 0) red[0][wave] = newest;
         __syncthreads();
 #pragma unroll
@@ -604,8 +591,7 @@ __global__ __launch_bounds__(PART_THREADS) void kv_evict_part_kernel(KvCache c, 
                 }
             }
         if (STAGE == COUNT0) {
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) inf += __shfl_xor(inf, d);
+            inf = wave_sum(inf);
             if (lane == 0 && inf) atomicAdd(&hist[KEY_INF >> 21], inf);
         }
         __syncthreads();
@@ -626,8 +612,7 @@ __global__ __launch_bounds__(PART_THREADS) void kv_evict_part_kernel(KvCache c, 
             }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) count[i] += __shfl_xor(count[i], d);
+            count[i] = wave_sum(count[i]);
             if (lane == 0) red[i][wave] = count[i];
         }
         __syncthreads();
@@ -646,22 +631,11 @@ __global__ __launch_bounds__(PART_THREADS) void kv_evict_part_kernel(KvCache c, 
             const int i = i0 + lane;
             i32x4_ev t = {0, 0, 0, 0};
             if (i < part) t = *reinterpret_cast<const i32x4_ev *>(pl.tally + ((int64_t)which * pl.parts + i) * 4);
-            int upto = t[2] + t[3];
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int x = __shfl_up(upto, d);
-                if (lane >= d) upto += x;
-            }
+            const int upto = wave_running_sum(t[2] + t[3]);
             const int left = lim.all ? INT32_MAX : max(0, lim.want - (equals + upto - t[2] - t[3]));  // for this part's equals
             const int low = min(t[2], left), high = min(t[3], left - low);
-            int kb = t[0] + low, kp = t[1] + high;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                kb += __shfl_xor(kb, d);
-                kp += __shfl_xor(kp, d);
-            }
-            below += kb;
-            past += kp;
+            below += wave_sum(t[0] + low);
+            past += wave_sum(t[1] + high);
             equals += __builtin_amdgcn_readlane(upto, 63);
         }
         if (lane == 0) {
