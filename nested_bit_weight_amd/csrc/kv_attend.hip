@@ -51,7 +51,6 @@ constexpr int ATTEND_WAVES = 4;
 constexpr int ATTEND_THREADS = 64 * ATTEND_WAVES;
 constexpr int TILE = 32;                     // slots of one wave's step
 constexpr int CHUNK = TILE * ATTEND_WAVES;   // slots of a unit
-constexpr int HELD_SCORES = 3072;            // scores a wave holds back, 6 tiles' or more
 constexpr float RAISE = 8.f;                 // how far a score may pass the running maximum
 constexpr float TINY = 1.17549435e-38f;      // the smallest normal number, fp32's and bf16's
 
@@ -105,8 +104,10 @@ __device__ __forceinline__ Parts parts_of(const KvCache &c, const AttendPlan &pl
     return {owner_of(seg0 + chunks - 1, units, shares) - w0 + 1, w0, 1};
 }
 
-// Tiles whose scores a wave holds back.
-__host__ __device__ constexpr int most_held(int block_heads) { return HELD_SCORES / (TILE * block_heads); }
+// Scores that a wave holds back (what leaves two workgroups room on a CU), and
+// their tiles: 12 of eight heads, 5 of sixteen.
+__host__ __device__ constexpr int held_scores(bool pack) { return pack ? 3072 : 2560; }
+__host__ __device__ constexpr int most_held(int block_heads) { return held_scores(block_heads <= 8) / (TILE * block_heads); }
 
 // One wave's tile: keys and values as loaded, and which slots count.
 template <int DIM, bool FP8>
@@ -173,13 +174,13 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
     constexpr int QF = DIM / 32;                      // Q operands
     __shared__ int scan[ATTEND_WAVES];
     __shared__ int found[2];
-    __shared__ float wave_ml[ATTEND_WAVES][HR][2], head_ml[HR][2];
-    // Each wave's results at the end of a piece; before that, with totals, the scores
-    // of its last tiles.
-    constexpr int POOL = WEIGHTS ? HELD_SCORES : HR * COLS;  // a wave's
-    static_assert(HELD_SCORES >= 16 * 128, "the results fit");
+    __shared__ __align__(16) float wave_m[HR][ATTEND_WAVES], wave_l[HR][ATTEND_WAVES];
+    __shared__ float head_ml[HR][2];
+    // Each wave's results at the end of a piece and, with totals, the scores of its
+    // last tiles.
+    constexpr int HELD = WEIGHTS ? held_scores(PACK) : 0, POOL = HELD + HR * COLS;  // a wave's
     __shared__ __align__(16) float pool[ATTEND_WAVES * POOL];
-    auto wave_o = [&](int w, int h, int d) -> float & { return pool[w * POOL + h * COLS + d]; };
+    auto wave_o = [&](int w, int h, int d) -> float * { return pool + w * POOL + HELD + h * COLS + d; };
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int quad = lane >> 4, col = lane & 15;
     const int vheads = c.heads * pl.blocks;
@@ -310,7 +311,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
         const int head = vh / pl.blocks, block = vh % pl.blocks;
         const int g0 = block * pl.block_heads, heads = min(pl.block_heads, pl.group - g0);
         const int32_t *table = c.table + (int64_t)row * c.table_ld;
-        const float by = a.scale * 1.44269504088896340736f * (FP8 ? c.k_scale[head] : 1.f);
+        const float by = a.scale * 1.44269504088896340736f * (FP8 ? c.k_scale[head] : 1.f), v_by = FP8 ? c.v_scale[head] : 1.f;
 
         // Q as the first product's B operand: column `col`'s head, the dims that
         // the key operand of the same number holds in this lane.
@@ -547,47 +548,84 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
         const bool totals = WEIGHTS && whole && pl.blocks == 1 && c1 <= most_held;
         if (WEIGHTS && !totals) put_scores(c1 - 1);
 
-        // The four waves' results together.
+        // The four waves' results together: each one's o as it stands, and what to
+        // multiply it by.
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
         if (lane < HR) {
-            wave_ml[wave][lane][0] = m;
-            wave_ml[wave][lane][1] = sum;
+            wave_m[lane][wave] = m;
+            wave_l[lane][wave] = sum;
         }
-        __syncthreads();
-        auto merged = [&](int h, float &top, float &total) {
-            top = NEG_INF;
-            total = 0.f;
+        auto put_o = [&](int n) {
 #pragma unroll
-            for (int w = 0; w < ATTEND_WAVES; ++w) top = fmaxf(top, wave_ml[w][h][0]);
+            for (int i = 0; i < 4; ++i) {
+                const int h = quad * 4 + i;
+                float x[T::DPL];
 #pragma unroll
-            for (int w = 0; w < ATTEND_WAVES; ++w) {
-                const float mw = wave_ml[w][h][0];
-                total += wave_ml[w][h][1] * (mw == top ? 1.f : exp2f(mw - top));
+                for (int e = 0; e < T::DPL; ++e) {
+                    x[e] = o[n][e][i];
+                    if (PACK) {  // rows 8..15, in the upper half of the wave, are the weights' lower parts
+                        const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(x[e]), __float_as_uint(x[e]), false, false);
+                        x[e] = __uint_as_float(both[0]) + __uint_as_float(both[1]);
+                    }
+                }
+                if (h < HR)
+#pragma unroll
+                    for (int e = 0; e < T::DPL; e += 4)
+                        *reinterpret_cast<f32x4_kv *>(wave_o(wave, h, col * T::DPL + e)) = f32x4_kv{x[e], x[e + 1], x[e + 2], x[e + 3]};
             }
         };
-        float scale_o[4];  // of this lane's rows of o
+        put_o(0);
+        __syncthreads();
+        auto merged = [&](int h, f32x4_kv &fade, float &top, float &total) {
+            const f32x4_kv mw = *reinterpret_cast<const f32x4_kv *>(wave_m[h]), lw = *reinterpret_cast<const f32x4_kv *>(wave_l[h]);
+            top = fmaxf(fmaxf(mw[0], mw[1]), fmaxf(mw[2], mw[3]));
+            total = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float top, total;
-            const int h = (quad * 4 + i) & (HR - 1);
-            merged(h, top, total);
-            const float mw = wave_ml[wave][h][0];
-            scale_o[i] = mw == top ? 1.f : exp2f(mw - top);
-        }
-        if (tid < heads) {
-            float top, total;
-            merged(tid, top, total);
-            if (!whole) {
-                pl.part_ml[(part * 16 + tid) * 2] = top;
-                pl.part_ml[(part * 16 + tid) * 2 + 1] = total;
-            } else if (totals) {
-                head_ml[tid][0] = top == NEG_INF ? 0.f : top;
-                head_ml[tid][1] = total == 0.f ? 0.f : 1.f / total;
-            } else if (WEIGHTS) {
-                float *w = pl.whole + (((int64_t)row * vheads + vh) * 16 + tid) * 2;
-                w[0] = top;
-                w[1] = total;
+            for (int w = 0; w < ATTEND_WAVES; ++w) {
+                fade[w] = mw[w] == top ? 1.f : __builtin_amdgcn_exp2f(mw[w] - top);
+                total += lw[w] * fade[w];
+            }
+        };
+        if (WEIGHTS || !whole)
+            if (tid < heads) {
+                f32x4_kv fade;
+                float top, total;
+                merged(tid, fade, top, total);
+                if (!whole) {
+                    pl.part_ml[(part * 16 + tid) * 2] = top;
+                    pl.part_ml[(part * 16 + tid) * 2 + 1] = total;
+                } else if (totals) {
+                    head_ml[tid][0] = top == NEG_INF ? 0.f : top;
+                    head_ml[tid][1] = total == 0.f ? 0.f : 1.f / total;
+                } else {
+                    float *w = pl.whole + (((int64_t)row * vheads + vh) * 16 + tid) * 2;
+                    w[0] = top;
+                    w[1] = total;
+                }
+            }
+#pragma unroll
+        for (int n = 0; n < T::NC; ++n) {
+            if (n) {
+                __syncthreads();
+                put_o(n);
+                __syncthreads();
+            }
+            for (int i = tid; i < heads * (COLS / 4); i += ATTEND_THREADS) {
+                const int h = i / (COLS / 4), d = i % (COLS / 4) * 4;
+                f32x4_kv fade, x = {0.f, 0.f, 0.f, 0.f};
+                float top, total;
+                merged(h, fade, top, total);
+#pragma unroll
+                for (int w = 0; w < ATTEND_WAVES; ++w) x += *reinterpret_cast<const f32x4_kv *>(wave_o(w, h, d)) * fade[w];
+                if (whole) {
+                    const float inv = total == 0.f ? 0.f : v_by / total;
+                    uint16_t *dst = a.out + (int64_t)row * a.out_ld + ((int64_t)head * pl.group + g0 + h) * DIM + n * COLS + d;
+                    *reinterpret_cast<u32x2_kv *>(dst) = u32x2_kv{pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv)};
+                } else {
+                    float *dst = pl.part_o + ((int64_t)part * pl.block_heads + h) * DIM + n * COLS + d;
+                    *reinterpret_cast<f32x4_kv *>(dst) = x;
+                }
             }
         }
         if (totals) {
@@ -607,39 +645,9 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
                 add_totals(a, base, slot, len, w, pl.vec);
             }
         }
-#pragma unroll
-        for (int n = 0; n < T::NC; ++n) {
-            if (n) __syncthreads();
-#pragma unroll
-            for (int e = 0; e < T::DPL; ++e)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float x = o[n][e][i] * scale_o[i];
-                    if (PACK) x += __shfl_xor(x, 32);  // the weights' lower parts
-                    const int h = quad * 4 + i;
-                    if (h < HR) wave_o(wave, h, col * T::DPL + e) = x;
-                }
-            __syncthreads();
-            for (int i = tid; i < heads * (COLS / 4); i += ATTEND_THREADS) {
-                const int h = i / (COLS / 4), d = i % (COLS / 4) * 4;
-                f32x4_kv x = *reinterpret_cast<f32x4_kv *>(&wave_o(0, h, d));
-#pragma unroll
-                for (int w = 1; w < ATTEND_WAVES; ++w) x += *reinterpret_cast<f32x4_kv *>(&wave_o(w, h, d));
-                if (whole) {
-                    float top, total;
-                    merged(h, top, total);
-                    const float inv = total == 0.f ? 0.f : (FP8 ? c.v_scale[head] : 1.f) / total;
-                    uint16_t *dst = a.out + (int64_t)row * a.out_ld + ((int64_t)head * pl.group + g0 + h) * DIM + n * COLS + d;
-                    *reinterpret_cast<u32x2_kv *>(dst) = u32x2_kv{pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv)};
-                } else {
-                    float *dst = pl.part_o + ((int64_t)part * pl.block_heads + h) * DIM + n * COLS + d;
-                    *reinterpret_cast<f32x4_kv *>(dst) = x;
-                }
-            }
-        }
         u += c1 - c0;
         if (u >= u1) return;  // the only piece, or the share's last
-        __syncthreads();      // wave_ml and pool are free
+        __syncthreads();      // wave_m, wave_l and pool are free
         if (++vh == vheads) {
             vh = 0;
             row_at += row_chunks;
