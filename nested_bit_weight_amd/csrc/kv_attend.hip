@@ -193,10 +193,19 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
 
     // This workgroup's first piece, and with equal shares its units [u, u1).
     int row, row_at = 0, len, row_chunks, vh, c0, c1, part = 0, u = 0, u1 = 0;
+    int32_t early[4];
     if (pl.undivided) {
         row = blockIdx.x / vheads;
         vh = blockIdx.x % vheads;
-        len = min(max(uniform_word(a.lens + row), 0), a.max_len);
+        len = uniform_word(a.lens + row);
+        if (!SMALL) {  // the first page numbers are asked for along with the length
+            const int32_t *table = c.table + (int64_t)row * c.table_ld;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                early[i] = uniform_word(table + (min(i / 2 * CHUNK + wave * TILE + i % 2 * 16, c.cap - 1) >> c.page_log2));
+            asm volatile("" : "+s"(len), "+s"(early[0]), "+s"(early[1]), "+s"(early[2]), "+s"(early[3]));
+        }
+        len = min(max(len, 0), a.max_len);
         row_chunks = chunks_of(len);
         c0 = 0;
         c1 = row_chunks;
@@ -523,7 +532,17 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
         // when a tile is used is then known, and only its own are waited for.
         {
             T ta, tb;
-            Pages pa = pages_of(c0), pb = pages_of(c0 + 1);
+            Pages pa, pb;
+            if (!SMALL && pl.undivided) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    pa.p[h * !SMALL] = early[h];
+                    pb.p[h * !SMALL] = early[2 + h];
+                }
+            } else {
+                pa = pages_of(c0);
+                pb = pages_of(c0 + 1);
+            }
             load(ta, pa, c0);
             int ch = c0;
             for (; ch + 2 < c1; ch += 2) {
