@@ -134,15 +134,16 @@ class KVCache:
                              f"{rows} x {width} is outside what the library takes (dim 64, 128 or 256; pages of a "
                              f"power of two up to 4096 slots, 16-byte aligned; a row of at most 2^30 slots)")
 
-    def _heads(self, t, name: str, n: int, heads: int):
-        """Address of a bf16 [n][heads][dim] tensor and its stride from one token to the
-        next (0: dense); tokens may lie apart, as in a slice of a wider product."""
+    def _heads(self, t, name: str, shape):
+        """Address of a bf16 tensor of shape [n][heads][dim] and its stride from one token
+        to the next (0: dense); tokens may lie apart, as in a slice of a wider product."""
         try:
-            if t.dtype is _BF16 and t.get_device() == self._dev and t.shape == (n, heads, self.dim):
+            if t.dtype is _BF16 and t.get_device() == self._dev and t.shape == shape:
                 if t.is_contiguous():
                     return t.data_ptr(), 0
+                n, heads, dim = shape
                 s0, s1, s2 = t.stride()
-                if s2 == 1 and (s1 == self.dim or heads == 1) and (s0 >= heads * self.dim or n == 1):
+                if s2 == 1 and (s1 == dim or heads == 1) and (s0 >= heads * dim or n == 1):
                     return t.data_ptr(), s0 if n > 1 else 0
         except AttributeError:
             pass
@@ -152,19 +153,19 @@ class KVCache:
             raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
         if t.get_device() != self._dev:
             raise ValueError(f"{name} must be on {self.device}, got {t.device}")
-        if t.shape != (n, heads, self.dim):
-            raise ValueError(f"{name} must be [{n}][{heads}][{self.dim}], got {tuple(t.shape)}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
         raise ValueError(f"{name} must have contiguous heads, one after the other")
 
-    def _q_heads(self, q) -> int:
-        """Query heads of [tokens][q_heads][dim]: a multiple of the cache's."""
+    def _queries(self, q, tokens: int):
+        """Shape of q: [tokens][q_heads][dim], q_heads a multiple of the cache's heads."""
         if not isinstance(q, torch.Tensor):
             raise TypeError("q must be a torch.Tensor")
-        n = q.size(1) if q.dim() == 3 else 0
-        if n == 0 or n % self.heads:
-            raise ValueError(f"q must be [tokens][q_heads][{self.dim}] with q_heads a multiple of {self.heads}, "
-                             f"got {tuple(q.shape)}")
-        return n
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != tokens or shape[2] != self.dim or not shape[1] or shape[1] % self.heads:
+            raise ValueError(f"q must be [{tokens}][q_heads][{self.dim}] with q_heads a multiple of {self.heads}, "
+                             f"got {tuple(shape)}")
+        return shape
 
     def attend_workspace_bytes(self, q_heads: int, max_len: int = 0, weights: bool = False) -> int:
         """Bytes of scratch kv_attend needs."""
@@ -185,8 +186,10 @@ class KVCache:
             nbytes = self._sizes.get(sizes)
             if nbytes is None:
                 nbytes = self._sizes[sizes] = _bytes(query(self._ref, *sizes))
+            if nbytes == 0:
+                return None, 0
             workspace = _workspace(self._dev, stream, nbytes)
-            return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+            return workspace.data_ptr(), workspace.numel()
         if workspace.get_device() != self._dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 tensor on the cache's GPU")
         return workspace.data_ptr(), workspace.numel()
@@ -213,8 +216,9 @@ def kv_append(cache: KVCache, k, v, lens, positions, *, q=None, cu=None, rope=No
     if not isinstance(k, torch.Tensor):
         raise TypeError("k must be a torch.Tensor")
     tokens, rows, heads, index = k.size(0) if k.dim() else 0, cache.rows, cache.heads, cache._dev
-    kp, k_ld = cache._heads(k, "k", tokens, heads)
-    vp, v_ld = cache._heads(v, "v", tokens, heads)
+    shape = (tokens, heads, cache.dim)
+    kp, k_ld = cache._heads(k, "k", shape)
+    vp, v_ld = cache._heads(v, "v", shape)
     qp = qo = cu_p = None
     q_ld = qo_ld = q_heads = rope_rows = 0
     if cu is not None:
@@ -222,11 +226,12 @@ def kv_append(cache: KVCache, k, v, lens, positions, *, q=None, cu=None, rope=No
     elif tokens != rows:
         raise ValueError(f"without cu there is one token for each of the {rows} rows, got {tokens}")
     if q is not None:
-        q_heads = cache._q_heads(q)
-        qp, q_ld = cache._heads(q, "q", tokens, q_heads)
+        shape = cache._queries(q, tokens)
+        q_heads = shape[1]
+        qp, q_ld = cache._heads(q, "q", shape)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        qo, qo_ld = cache._heads(q_out, "q_out", tokens, q_heads)
+            q_out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        qo, qo_ld = cache._heads(q_out, "q_out", shape)
     elif q_out is not None or q_norm is not None:
         raise ValueError("q_out and q_norm go with q")
     if rope is not None:
@@ -262,8 +267,9 @@ def kv_attend(cache: KVCache, q, lens, *, scale: float | None = None, out=None, 
     binding's buffer of this device and stream), or a uint8 tensor of at least
     ``cache.attend_workspace_bytes(...)`` bytes, as a captured graph should have."""
     index = cache._dev
-    q_heads = cache._q_heads(q)
-    qp, q_ld = cache._heads(q, "q", cache.rows, q_heads)
+    shape = cache._queries(q, cache.rows)
+    q_heads = shape[1]
+    qp, q_ld = cache._heads(q, "q", shape)
     if scale is None:
         scale = 0.0
     elif not 0.0 < abs(scale) < 3e38:
@@ -273,8 +279,8 @@ def kv_attend(cache: KVCache, q, lens, *, scale: float | None = None, out=None, 
     elif max_len < 1:
         raise ValueError("max_len must be at least 1")
     if out is None:
-        out = torch.empty(q.shape, dtype=_BF16, device=q.device)
-    op, out_ld = cache._heads(out, "out", cache.rows, q_heads)
+        out = torch.empty(shape, dtype=_BF16, device=q.device)
+    op, out_ld = cache._heads(out, "out", shape)
     acc_p = acc_o = None
     if acc is not None:
         acc_p = _is(acc, "acc", _F32, cache._track, index)
