@@ -23,7 +23,7 @@
 //    histogram over their upper 11 bits, two more over the next 11 and the last 10
 //    of those in the wanted bin, counts, lists.  Histograms meet in integer
 //    atomics, whose order does not matter.
-//  - Moves need the whole device: with more than a few a last launch makes them, 64
+//  - Moves need the whole device: with more than a few a last launch makes them, 16
 //    to a workgroup.  In the steady state of one token over the budget the ranking's
 //    workgroup makes its one move itself.
 //
@@ -42,7 +42,7 @@ constexpr int EVICT_BINS_LOG2 = 11, EVICT_BINS = 1 << EVICT_BINS_LOG2;
 constexpr uint32_t KEY_INF = 0xFF800000u, KEY_NEG_INF = 0x007FFFFFu;
 constexpr int EVICT_ROW = 16384;     // the longest row that one workgroup ranks
 constexpr int PART_THREADS = 256, PART_GROUPS = 4, PART = PART_THREADS * PART_GROUPS * 4;  // longer ones: slots of a workgroup
-constexpr int MOVES = 64;           // moves of a workgroup of the second launch
+constexpr int MOVES = 16;           // moves of a workgroup of the second launch
 constexpr int FUSED_MOVES = 16;     // up to so many the ranking's workgroup makes itself
 constexpr int FEW_OUT = 4;          // up to so many slots over the budget are found one by one
 
@@ -74,7 +74,7 @@ __device__ __forceinline__ uint32_t evict_key(float acc, int32_t pos, int32_t ne
 template <int ROW_BYTES, int THREADS, bool NT>
 __device__ __forceinline__ void make_moves(const KvCache &c, const KvEvict &a, int row, int head, const int32_t *to,
                                            const int32_t *of, int count) {
-    constexpr int VECS = ROW_BYTES / 16, AT_ONCE = 4;
+    constexpr int VECS = ROW_BYTES / 16, AT_ONCE = 2;
     const int64_t base = ((int64_t)row * c.heads + head) * c.cap;
     const int end = count * VECS;  // at most MOVES or FUSED_MOVES rows
     for (int i0 = threadIdx.x; i0 < end; i0 += THREADS * AT_ONCE) {
