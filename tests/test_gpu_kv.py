@@ -134,6 +134,9 @@ ATTEND = [
     # every (row, head) a workgroup's, with and without its totals; more rows than a wave has lanes, divided
     ([700, 20, 300] * 33, 8, 2, 16, 64, BF16), ([900] * 30, 20, 1, 64, 64, FP8), ([1500, 70] * 5, 2, 16, 64, 64, BF16),
     ([3000] + [10] * 69, 2, 3, 32, 64, BF16), ([2000, 0, 900], 1, 40, 128, 64, BF16),
+    # shares that run from one (row, head) into the next; more rows than a workgroup has threads
+    ([3000, 17, 900, 1400, 0, 2222, 128, 640] * 5, 16, 2, 64, 64, BF16), ([2900, 400, 1100] * 15, 12, 3, 16, 64, FP8),
+    ([2500, 300] * 20, 16, 9, 32, 64, BF16), ([1200, 0] + [5] * 299, 1, 2, 16, 64, BF16),
 ]
 
 
@@ -172,6 +175,27 @@ def test_attend_in_place_totals_strided_queries_bound_and_repeats(nbw):
     s.lens_l = [min(n, 100) for n in s.lens_l]
     cut = nbw.kv_attend(s.cache, q, s.lens, max_len=100)
     check_attend(s, q, cut, 128 ** -0.5)
+
+
+def test_totals_at_any_address(nbw):
+    """Totals that are not 16-byte aligned, in a workgroup's hands and in the second launch's."""
+    for lens, room in (([100, 70], 0), ([3000, 70], 0)):
+        s = Setup(nbw, lens, page=16, seed=2)
+        q = s.normal(2, 4, 128)
+        first = s.totals()
+        odd = torch.empty(first.numel() + 1, device="cuda")[1:].view(first.shape)
+        odd.copy_(first)
+        out = nbw.kv_attend(s.cache, q, s.lens, acc=odd, decay=0.5)
+        check_attend(s, q, out, 128 ** -0.5, first, odd, 0.5, before=first)
+    pos = torch.arange(s.cap, dtype=torch.int32, device="cuda").repeat(2, 2, 1)
+    want = [torch.zeros_like(first), torch.zeros_like(pos)]
+    nbw.kv_evict(s.cache, first, pos, s.lens, 900, recent=9, acc_out=want[0], pos_out=want[1])
+    odd.copy_(first)
+    odd_pos = torch.empty(pos.numel() + 3, dtype=torch.int32, device="cuda")[3:].view(pos.shape)
+    odd_pos.copy_(pos)
+    got = [torch.zeros(first.numel() + 1, device="cuda")[1:].view(first.shape), torch.zeros_like(pos)]
+    nbw.kv_evict(s.cache, odd, odd_pos, s.lens, 900, recent=9, acc_out=got[0], pos_out=got[1])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_attend_lengths_outside_the_table_are_bounded(nbw):
