@@ -337,9 +337,8 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
 
         // Page numbers of a chunk's tile.  Pages of 16 slots and more: one for each
         // half, the same in all lanes; smaller ones: lane l has slot l % 32's.  Past the
-        // row's length they are whatever the table holds, and what is loaded by them
-        // (from a page of the pool in any case) is left out: the first tile's loads
-        // need not wait for the length.
+        // row's length they are whatever the table holds; in their place, and for pages
+        // that are not there, the pool's first page is loaded and left out.
         struct Pages { int32_t p[SMALL ? 1 : 2]; };
         auto pages_of = [&](int chunk) {
             Pages r;
@@ -363,7 +362,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
                 const int32_t safe = mine_ok ? own : -1;
                 auto place = [&](int s, bool &ok) -> int64_t {  // byte offset of slot s (0..31) of the tile
                     const int32_t p = __shfl(safe, s);
-                    ok = p >= 0;
+                    ok = p >= 0 && slot + s < len;
                     return ((((int64_t)(ok ? p : 0) * c.heads + head) << c.page_log2) + ((slot + s) & mask)) * ROW_BYTES;
                 };
 #pragma unroll
@@ -375,7 +374,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint8_t *q = c.v + place(16 * h + quad * 4 + i, ok) + col * T::VW * 4;
-                        t.there |= (uint32_t)(ok && slot + 16 * h + quad * 4 + i < len) << (4 * h + i);
+                        t.there |= (uint32_t)ok << (4 * h + i);
 #pragma unroll
                         for (int n = 0; n < T::NC; ++n) load_words<NT, T::VW>(t.v[h][i][n], q + n * (ROW_BYTES / T::NC));
                     }
@@ -384,7 +383,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int s = slot + 16 * h;
-                    const bool ok = (uint32_t)pg.p[h] < (uint32_t)c.pages;
+                    const bool ok = s < len && (uint32_t)pg.p[h] < (uint32_t)c.pages;
                     const int left = ok ? min(len - s, 16) - quad * 4 : 0;
                     t.there |= (left >= 4 ? 15u : left <= 0 ? 0u : (1u << left) - 1) << (4 * h);
                     const int64_t base = ((((int64_t)(ok ? pg.p[h] : 0) * c.heads + head) << c.page_log2) + (s & mask)) * ROW_BYTES;
@@ -845,8 +844,8 @@ static int64_t attend_plan(const KvCache &c, int q_heads, int max_len, bool weig
     // parts; and up to about eight for each time that the workgroups fill the device,
     // when the last ones to run are a small share of all.  (96 rows of up to 600 slots,
     // 8 heads: 30 us so, 49 us in equal shares.)  With totals the scores of a row have
-    // to stay in LDS.
-    pl->undivided = chunks <= 4 || (c.rows * vheads >= pl->wgs && chunks <= 8 * c.rows * vheads / pl->wgs);
+    // to stay in LDS, and the second launch, which then adds them up, is worth 12 steps.
+    pl->undivided = chunks <= (weights ? 12 : 4) || (c.rows * vheads >= pl->wgs && chunks <= 8 * c.rows * vheads / pl->wgs);
     if (weights && (pl->blocks > 1 || chunks > most_held(pl->block_heads))) pl->undivided = 0;
     if (pl->undivided) pl->wgs = (int)(c.rows * vheads);
     // Totals: eight units for each step of a workgroup, and a few workgroups for each CU.

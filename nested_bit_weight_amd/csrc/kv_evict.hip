@@ -40,10 +40,10 @@ typedef int32_t i32x4_ev __attribute__((ext_vector_type(4)));
 
 constexpr int EVICT_BINS_LOG2 = 11, EVICT_BINS = 1 << EVICT_BINS_LOG2;
 constexpr uint32_t KEY_INF = 0xFF800000u, KEY_NEG_INF = 0x007FFFFFu;
-constexpr int EVICT_ROW = 16384;     // the longest row that one workgroup ranks
+constexpr int EVICT_ROW = 16384;     // the longest row that one workgroup ranks (32 keys a thread spill: at 32768 both ways took 46-49 us)
 constexpr int PART_THREADS = 256, PART_GROUPS = 4, PART = PART_THREADS * PART_GROUPS * 4;  // longer ones: slots of a workgroup
 constexpr int MOVES = 16;           // moves of a workgroup of the second launch
-constexpr int FUSED_MOVES = 16;     // up to so many the ranking's workgroup makes itself
+constexpr int FUSED_MOVES = 64;     // up to so many the ranking's workgroup makes itself
 constexpr int FEW_OUT = 4;          // up to so many slots over the budget are found one by one
 
 // The workspace: the lists of each (row, head) and their lengths; for long rows,
