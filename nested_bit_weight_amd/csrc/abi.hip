@@ -549,8 +549,6 @@ nbw_status nbw_kv_evict(const nbw_kvcache *cache, const nbw_kv_evict_args *args,
     const int64_t need = nbw::kv_evict_workspace_bytes(c, (int)g.budget, a.max_len);
     if (need < 0) return NBW_EINVAL;  // more workgroups than an int counts
     if (need > 0 && (!g.workspace || g.workspace_bytes < need)) return NBW_ESCRATCH;
-    int cus = 0;
-    if ((st = cu_count(&cus)) != NBW_OK) return st;
     a.acc = g.acc;
     a.pos = g.pos;
     a.lens = g.lens;
@@ -561,7 +559,7 @@ nbw_status nbw_kv_evict(const nbw_kvcache *cache, const nbw_kv_evict_args *args,
     a.pos_out = g.pos_out;
     a.lens_out = g.lens_out;
     a.ws = (uint8_t *)g.workspace;
-    const hipError_t e = nbw::launch_kv_evict(c, a, cus, (hipStream_t)stream);
+    const hipError_t e = nbw::launch_kv_evict(c, a, (hipStream_t)stream);
     return e == hipSuccess ? NBW_OK : hip_failed(e);
 }
 

@@ -64,7 +64,7 @@ hipError_t launch_kv_append(const KvCache &c, const KvAppend &a, hipStream_t str
 int64_t kv_attend_workspace_bytes(const KvCache &c, int q_heads, int max_len, bool weights, int cu_count);
 hipError_t launch_kv_attend(const KvCache &c, const KvAttend &a, int cu_count, hipStream_t stream);
 int64_t kv_evict_workspace_bytes(const KvCache &c, int budget, int max_len);
-hipError_t launch_kv_evict(const KvCache &c, const KvEvict &a, int cu_count, hipStream_t stream);
+hipError_t launch_kv_evict(const KvCache &c, const KvEvict &a, hipStream_t stream);
 
 typedef uint32_t u32x2_kv __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_kv __attribute__((ext_vector_type(4)));

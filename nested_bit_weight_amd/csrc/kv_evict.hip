@@ -7,7 +7,7 @@
 // moves copy 4 * dim elements a moved row, so the two are separate problems:
 //
 //  - Ranking.  Up to 16384 slots one workgroup takes a (row, head), with its keys
-//    in registers, 16 a thread.  The budget-th largest key is found by counting: a
+//    in registers, up to 16 a thread.  The budget-th largest key is found by counting: a
 //    histogram of 2048 bins over the 11 bits below the leading bits that all
 //    candidates share, the bin that holds the wanted key, and again inside it,
 //    until a bin is wanted whole or holds one value.  On attention totals the first
@@ -706,20 +706,17 @@ static void launch_moves(const KvCache &c, const KvEvict &a, const EvictPlan &pl
         hipLaunchKernelGGL((kv_move_kernel<ROW_BYTES, false>), moves, threads, 0, stream, c, a, pl, (int)each);
 }
 
-hipError_t launch_kv_evict(const KvCache &c, const KvEvict &a, int cu_count, hipStream_t stream) {
+hipError_t launch_kv_evict(const KvCache &c, const KvEvict &a, hipStream_t stream) {
     EvictPlan pl;
     evict_plan(c, a.budget, a.max_len, a.ws, &pl);
     pl.vec = c.cap % 4 == 0 && (((uintptr_t)a.acc | (uintptr_t)a.pos | (uintptr_t)a.acc_out | (uintptr_t)a.pos_out) & 15) == 0;
     const dim3 grid((unsigned)c.rows * c.heads);
-    // Up to 4096 slots: with a CU for each (row, head), many waves with few keys each;
-    // with more of them than CUs, few waves with many keys each, whose barriers cost
-    // less.  (256 rows x heads of 2049 slots: 13.1 us and 15.7; 768 of 1025: 26 and 20.)
+    // The smallest workgroup that holds the longest row's keys, 4, 8 or 16 a thread.
+    // (Rows of 2049 slots as 256 threads with 16 keys: 17.6 us, and 14 so.)
     if (a.max_len <= 1024) {
         hipLaunchKernelGGL((kv_evict_kernel<256, 1>), grid, dim3(256), 0, stream, c, a, pl);
-    } else if (a.max_len <= 4096 && (int)grid.x <= cu_count) {
-        hipLaunchKernelGGL((kv_evict_kernel<512, 2>), grid, dim3(512), 0, stream, c, a, pl);
     } else if (a.max_len <= 4096) {
-        hipLaunchKernelGGL((kv_evict_kernel<256, 4>), grid, dim3(256), 0, stream, c, a, pl);
+        hipLaunchKernelGGL((kv_evict_kernel<512, 2>), grid, dim3(512), 0, stream, c, a, pl);
     } else if (!pl.parts) {
         hipLaunchKernelGGL((kv_evict_kernel<1024, 4>), grid, dim3(1024), 0, stream, c, a, pl);
     } else {
