@@ -192,11 +192,19 @@ def test_bad_attend_arguments_are_refused(lib, change, status):
     (dict(budget=0), EINVAL), (dict(budget=81), EINVAL), (dict(sink=-1), EINVAL), (dict(recent=-1), EINVAL),
     (dict(sink=33), EINVAL), (dict(recent=1 << 62), EINVAL), (dict(max_len=-5), EINVAL),
     (dict(acc=FAKE + 2), EALIGN), (dict(pos_out=FAKE + 2), EALIGN), (dict(workspace=FAKE + 4), EALIGN),
-    (dict(workspace_bytes=-1), EINVAL), (dict(workspace=None), ESCRATCH),
-    (dict(workspace=FAKE, workspace_bytes=8), ESCRATCH),
+    (dict(workspace_bytes=-1), EINVAL),
 ])
 def test_bad_evict_arguments_are_refused(lib, change, status):
     assert call(lib, "nbw_kv_evict", cache(), evict_args(**change)) == status
+
+
+def test_a_missing_or_small_workspace_is_refused(lib):
+    # 320 slots brought down to 100: more moves than the ranking's workgroup makes itself
+    big = cache(width=20)
+    assert call(lib, "nbw_kv_evict", big, evict_args(budget=100)) == ESCRATCH
+    assert call(lib, "nbw_kv_evict", big, evict_args(budget=100, workspace=FAKE, workspace_bytes=8)) == ESCRATCH
+    need = lib.nbw_kv_evict_workspace_bytes(ctypes.byref(big), 100, 0)
+    assert call(lib, "nbw_kv_evict", big, evict_args(budget=100, workspace=FAKE, workspace_bytes=need - 1)) == ESCRATCH
 
 
 def test_empty_batches_queue_nothing(lib):
@@ -215,7 +223,7 @@ def test_workspace_sizes_refuse_bad_arguments(lib):
     assert lib.nbw_kv_evict_workspace_bytes(ctypes.byref(c), 0, 0) == -1
     assert lib.nbw_kv_evict_workspace_bytes(ctypes.byref(c), 81, 0) == -1
     assert lib.nbw_kv_evict_workspace_bytes(ctypes.byref(c), 40, 40) == 0
-    assert lib.nbw_kv_evict_workspace_bytes(ctypes.byref(c), 40, 0) > 0
+    assert lib.nbw_kv_evict_workspace_bytes(ctypes.byref(cache(width=20)), 100, 0) > 0
 
 
 def test_binding_refuses_cpu_tensors():
