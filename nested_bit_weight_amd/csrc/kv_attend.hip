@@ -67,6 +67,13 @@ __device__ __forceinline__ int32_t uniform_word(const int32_t *p) {
     return *reinterpret_cast<const __attribute__((address_space(4))) int32_t *>(reinterpret_cast<uintptr_t>(p));
 }
 
+// The wave's accesses to LDS before this are over, in all lanes, before those after it.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // The launch's division of work and its scratch, the same for both kernels.
 struct AttendPlan {
     int wgs;             // workgroups of the first launch
@@ -422,11 +429,11 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
         auto put_scores = [&](int chunk) {  // up to this chunk's
             const int each = TILE / 4 * pl.block_heads;  // 16-byte pieces of a tile
             float *dst = pl.scores + ((seg0 + chunk - held + 1) * ATTEND_WAVES + wave) * each * 4;
-            __builtin_amdgcn_wave_barrier();
+            wave_fence();
             for (int i = lane; i < held * each; i += 64)
                 *reinterpret_cast<f32x4_kv *>(dst + ((int64_t)(i / each) * ATTEND_WAVES * each + i % each) * 4) =
                     *reinterpret_cast<const f32x4_kv *>(scores + i * 4);
-            __builtin_amdgcn_wave_barrier();
+            wave_fence();
             held = 0;
         };
         auto use = [&](T &t, int chunk) {
