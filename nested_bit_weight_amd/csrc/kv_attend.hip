@@ -118,7 +118,7 @@ __device__ __forceinline__ Parts parts_of(const KvCache &c, const AttendPlan &pl
 
 // Scores that a wave holds back (what leaves two workgroups room on a CU), and
 // their tiles: 12 of eight heads, 5 of sixteen.
-__host__ __device__ constexpr int held_scores(bool pack) { return pack ? 3072 : 2560; }
+__host__ __device__ constexpr int held_scores(bool pack) { return pack ? 12 * TILE * 8 : 5 * TILE * 16; }
 __host__ __device__ constexpr int most_held(int block_heads) { return held_scores(block_heads <= 8) / (TILE * block_heads); }
 
 // One wave's tile: keys and values as loaded, and which slots count.
