@@ -29,10 +29,12 @@
 //  - V is loaded row by row, lane l the dims 8 (l % 16) .. + 7 of the eight
 //    slots of its quarter, and one v_perm for each pair of slots makes the B
 //    operand of column t: dim 8 (l % 16) + t.
-// The weights enter the second product as two bf16 parts, p = hi + lo, so they
-// keep 15 bits or more; with up to 8 heads the parts share one product, hi in its rows
-// 0..7 and lo in rows 8..15, whose scores are computed twice instead of rows
-// standing empty.  Sums of p are taken in fp32 before that.
+// The weights enter the second product as three bf16 parts, which hold all 24 bits of
+// them; sums of p are taken in fp32 before that.  With up to 8 heads the two upper parts
+// share one product, in its rows 0..7 and 8..15, whose scores are computed twice instead
+// of rows standing empty, and half of the lowest part is in each half of another.  (With two
+// parts, 16 bits, everything takes as long within 1%: 64 rows 201 us, 24 rows with 12
+// heads 49, one row of 333 slots 7.6 and 7.8 so.)
 //
 // Measured (128 dims, 8 heads): 64 rows of up to 8192 slots, 1.2 GB: 199 us, 6.0 TB/s
 // (a plain read of as much: 175 us), with totals 249; one row of 131071 slots, 537 MB,
@@ -493,15 +495,19 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
                 p[i] = __builtin_amdgcn_exp2f(x[i] - ref);
                 sum += p[i];
             }
-            u32x4_kv hi, lo;
+            // The weights' 24 bits as three bf16 parts: each but the last is cut off, not
+            // rounded, so that none is negative, and none is 0, so an infinite value stays
+            // one (0 * inf and inf - inf would be NaN).
+            u32x4_kv hi, mid, lo;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                // hi is cut off, not rounded, so lo is not negative; neither is 0, so an
-                // infinite value stays one (0 * inf and inf - inf would be NaN).
                 const float a0 = fmaxf(p[2 * i], TINY), a1 = fmaxf(p[2 * i + 1], TINY);
                 hi[i] = __builtin_amdgcn_perm(__float_as_uint(a1), __float_as_uint(a0), 0x07060302u);
-                lo[i] = pack_bf16(fmaxf(a0 - bf16_lo(hi[i]), TINY), fmaxf(a1 - bf16_hi(hi[i]), TINY));
-                if (PACK) hi[i] = col < 8 ? hi[i] : lo[i];
+                const float b0 = fmaxf(a0 - bf16_lo(hi[i]), TINY), b1 = fmaxf(a1 - bf16_hi(hi[i]), TINY);
+                mid[i] = __builtin_amdgcn_perm(__float_as_uint(b1), __float_as_uint(b0), 0x07060302u);
+                constexpr float each = PACK ? 0.5f : 1.f;  // of the lowest part, in how many rows it is
+                lo[i] = pack_bf16(fmaxf((b0 - bf16_lo(mid[i])) * each, TINY), fmaxf((b1 - bf16_hi(mid[i])) * each, TINY));
+                if (PACK) hi[i] = col < 8 ? hi[i] : mid[i];
             }
 #pragma unroll
             for (int n = 0; n < T::NC; ++n) {
@@ -530,8 +536,10 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
                     o[n][e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_kv, hi),
                                                                       __builtin_bit_cast(bf16x8_kv, vf), o[n][e], 0, 0, 0);
                     if (!PACK)
-                        o[n][e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_kv, lo),
+                        o[n][e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_kv, mid),
                                                                           __builtin_bit_cast(bf16x8_kv, vf), o[n][e], 0, 0, 0);
+                    o[n][e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_kv, lo),
+                                                                      __builtin_bit_cast(bf16x8_kv, vf), o[n][e], 0, 0, 0);
                 }
             }
         };
