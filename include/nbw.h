@@ -464,9 +464,10 @@ typedef struct nbw_kv_attend_args {
  * and, with acc, for j < len (other entries are left as they are):
  *     acc_out_j = decay * acc_j + sum over g of p_j.
  * Products, softmax and sums are in fp32; out is rounded once.  A row of
- * length 0 gives zeros, as does a head whose scores are all -infinity; a NaN
- * among a row's scores or values gives NaN; what lies in slots past the length
- * has no part.  Deterministic: the same inputs give the same bits.
+ * length 0 gives zeros, as does a head whose scores are all -infinity, whatever
+ * its values; else a NaN among a row's scores or values gives NaN.  What lies in
+ * slots past the length has no part.  Deterministic: the same inputs give the
+ * same bits.
  * Errors: NBW_EINVAL, NBW_EALIGN, NBW_EUNSUPPORTED, NBW_ESCRATCH (workspace
  * missing or too small), NBW_EHIP. */
 nbw_status nbw_kv_attend(const nbw_kvcache *cache, const nbw_kv_attend_args *args, void *stream);

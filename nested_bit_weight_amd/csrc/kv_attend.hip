@@ -658,6 +658,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
                 for (int w = 0; w < ATTEND_WAVES; ++w) x += *reinterpret_cast<const f32x4_kv *>(wave_o(w, h, d)) * fade[w];
                 if (whole) {
                     const float inv = total == 0.f ? 0.f : v_by / total;
+                    if (total == 0.f) x = f32x4_kv{0.f, 0.f, 0.f, 0.f};  // nothing to attend to, whatever the values are
                     uint16_t *dst = a.out + (int64_t)row * a.out_ld + ((int64_t)head * pl.group + g0 + h) * DIM + n * COLS + d;
                     *reinterpret_cast<u32x2_kv *>(dst) = u32x2_kv{pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv)};
                 } else {
@@ -753,6 +754,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void kv_join_kernel(KvCache c, KvAtte
                 x += *reinterpret_cast<f32x4_kv *>(&slice_o[s][d]);
             }
             const float inv = total == 0.f ? 0.f : (c.fp8 ? c.v_scale[head] : 1.f) / total;
+            if (total == 0.f) x = f32x4_kv{0.f, 0.f, 0.f, 0.f};
             uint16_t *dst = a.out + (int64_t)row * a.out_ld + (int64_t)qh * DIM + d;
             *reinterpret_cast<u32x2_kv *>(dst) = u32x2_kv{pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv)};
         }

@@ -48,3 +48,37 @@ def test_attend_weights_keep_their_24_bits(nbw, group, dim, page):  # noqa: F811
     want = ((p - c1 - c2) / (2 + p)).repeat(group, axis=1)[..., None]
     assert np.abs(want).max() > 2.0**-19.5  # what two parts would lose is there to be seen
     assert np.all(np.abs(out - want) <= 2.0**-8 * 1.01 * np.abs(want) + 2.0**-21), float(np.abs(out - want).max() * 2.0**21)
+
+
+def rows_cache(nbw, lens, heads, dim, page, seed, width=None):  # noqa: F811
+    """A bf16 cache of rows on pages of their own: (cache, lens tensor, table as numpy)."""
+    rng = np.random.default_rng(seed)
+    need = [-(-n // page) for n in lens]
+    table = np.full((len(lens), width or max(need)), -1, dtype=np.int32)
+    at = 0
+    for r, m in enumerate(need):
+        table[r, :m] = np.arange(at, at + m)
+        at += m
+    pools = [torch.from_numpy(rng.standard_normal((at, heads, page, dim)).astype(np.float32)).to(BF16).cuda() for _ in "kv"]
+    cache = nbw.KVCache(*pools, torch.from_numpy(table).cuda())
+    return cache, torch.tensor(lens, dtype=torch.int32, device="cuda"), table
+
+
+@pytest.mark.parametrize("lens", [[60, 60], [500, 40], [3000, 2600]])
+@pytest.mark.parametrize("group,dim,page", [(2, 128, 16), (12, 64, 4), (4, 256, 32)])
+def test_attend_heads_without_a_score_give_zeros_whatever_their_values(nbw, lens, group, dim, page):  # noqa: F811
+    """Row 0's scores are all -infinity: zeros and unchanged totals, also where its values are infinite or NaN."""
+    cache, n, table = rows_cache(nbw, lens, 2, dim, page, 7)
+    mine = torch.from_numpy(table[0][table[0] >= 0]).long().cuda()
+    cache.k[mine, :, :, 0] = -math.inf
+    cache.v[mine[0], :, :, 3] = math.inf
+    cache.v[mine[-1], :, :, 5] = -math.inf
+    cache.v[mine[-1], :, 0, 7] = math.nan
+    q = torch.rand((2, 2 * group, dim), device="cuda").add_(0.01).to(BF16)
+    print(f"no scores {lens} group {group} dim {dim} page {page}", flush=True)
+    out = nbw.kv_attend(cache, q, n)
+    assert bool((out[0] == 0).all()) and bool(out[1].isfinite().all())
+    acc = torch.rand((2, 2, cache.capacity), device="cuda")
+    acc_out = torch.zeros_like(acc)
+    assert torch.equal(nbw.kv_attend(cache, q, n, acc=acc, acc_out=acc_out), out)
+    assert torch.equal(acc_out[0, :, :lens[0]], acc[0, :, :lens[0]])
