@@ -496,17 +496,18 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
                 sum += p[i];
             }
             // The weights' 24 bits as three bf16 parts: each but the last is cut off, not
-            // rounded, so that none is negative, and none is 0, so an infinite value stays
-            // one (0 * inf and inf - inf would be NaN).
+            // rounded, so that none is negative, and none of a weight's is 0 unless it is, so
+            // an infinite value stays one (0 * inf and inf - inf would be NaN).  A weight
+            // of 0 adds nothing, however large its value.
             u32x4_kv hi, mid, lo;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float a0 = fmaxf(p[2 * i], TINY), a1 = fmaxf(p[2 * i + 1], TINY);
+                const float a0 = p[2 * i], a1 = p[2 * i + 1], t0 = fminf(a0, TINY), t1 = fminf(a1, TINY);
                 hi[i] = __builtin_amdgcn_perm(__float_as_uint(a1), __float_as_uint(a0), 0x07060302u);
-                const float b0 = fmaxf(a0 - bf16_lo(hi[i]), TINY), b1 = fmaxf(a1 - bf16_hi(hi[i]), TINY);
+                const float b0 = fmaxf(a0 - bf16_lo(hi[i]), t0), b1 = fmaxf(a1 - bf16_hi(hi[i]), t1);
                 mid[i] = __builtin_amdgcn_perm(__float_as_uint(b1), __float_as_uint(b0), 0x07060302u);
                 constexpr float each = PACK ? 0.5f : 1.f;  // of the lowest part, in how many rows it is
-                lo[i] = pack_bf16(fmaxf((b0 - bf16_lo(mid[i])) * each, TINY), fmaxf((b1 - bf16_hi(mid[i])) * each, TINY));
+                lo[i] = pack_bf16(fmaxf((b0 - bf16_lo(mid[i])) * each, t0), fmaxf((b1 - bf16_hi(mid[i])) * each, t1));
                 if (PACK) hi[i] = col < 8 ? hi[i] : mid[i];
             }
 #pragma unroll

@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_kv import BF16, f64, nbw  # noqa: F401  (the fixture)
+from test_gpu_kv import BF16, FP8, Setup, check_attend, f64, nbw  # noqa: F401  (nbw: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +82,18 @@ def test_attend_heads_without_a_score_give_zeros_whatever_their_values(nbw, lens
     acc_out = torch.zeros_like(acc)
     assert torch.equal(nbw.kv_attend(cache, q, n, acc=acc, acc_out=acc_out), out)
     assert torch.equal(acc_out[0, :, :lens[0]], acc[0, :, :lens[0]])
+
+
+@pytest.mark.parametrize("lens", [[200, 64], [3000, 900]])
+@pytest.mark.parametrize("group", [2, 12])
+def test_attend_weights_of_zero_add_nothing_however_large_the_value(nbw, lens, group):  # noqa: F811
+    """Values of 3e38 in slots whose weight is below any number (scores 300 below the others) or 0 (scores of -infinity)."""
+    s = Setup(nbw, lens, heads=2, page=16, seed=group)
+    q = s.normal(2, 2 * group, 128).abs() + 0.25
+    for r, j, key in ((0, 3, -30.0), (0, lens[0] - 1, -math.inf), (1, 40, -30.0), (1, 41, -30.0)):
+        at = s.table_np[r, j // 16], slice(None), j % 16
+        s.k[at] = key
+        s.v[at] = 3e38
+    out = nbw.kv_attend(s.cache, q, s.lens)
+    assert bool((out.abs() < 8).all())
+    check_attend(s, q, out, 128 ** -0.5)
