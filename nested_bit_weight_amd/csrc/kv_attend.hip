@@ -93,6 +93,12 @@ struct AttendPlan {
     int vec;             // totals may be read and written 16 bytes at a time
 };
 
+// Weights are up to 2^RAISE, and n of them meet the values.  Times this power of two they
+// sum to 1 at the most, and finite values cannot run over.
+__device__ __forceinline__ float weights_by(int n) {
+    return __uint_as_float((uint32_t)(127 - (int)RAISE - (n > 1 ? 32 - __builtin_clz(n - 1) : 0)) << 23);
+}
+
 // The workgroup whose share a unit is in.
 __device__ __forceinline__ int owner_of(int64_t unit, int64_t units, int shares) {
     return (int)(((unit + 1) * shares - 1) / units);
@@ -334,6 +340,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
         const int head = vh / pl.blocks, block = vh % pl.blocks;
         const int g0 = block * pl.block_heads, heads = min(pl.block_heads, pl.group - g0);
         const int32_t *table = c.table + (int64_t)row * c.table_ld;
+        const float down = weights_by(len);
         const float by = a.scale * 1.44269504088896340736f * (FP8 ? c.k_scale[head] : 1.f), v_by = FP8 ? c.v_scale[head] : 1.f;
 
         // Q as the first product's B operand: column `col`'s head, the dims that
@@ -492,7 +499,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
             float p[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                p[i] = __builtin_amdgcn_exp2f(x[i] - ref);
+                p[i] = __builtin_amdgcn_exp2f(x[i] - ref) * down;
                 sum += p[i];
             }
             // The weights' 24 bits as three bf16 parts: each but the last is cut off, not
@@ -636,7 +643,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
                     pl.part_ml[(part * 16 + tid) * 2 + 1] = total;
                 } else if (totals) {
                     head_ml[tid][0] = top == NEG_INF ? 0.f : top;
-                    head_ml[tid][1] = total == 0.f ? 0.f : 1.f / total;
+                    head_ml[tid][1] = total == 0.f ? 0.f : down / total;
                 } else {
                     float *w = pl.whole + (((int64_t)row * vheads + vh) * 16 + tid) * 2;
                     w[0] = top;
@@ -818,7 +825,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void kv_join_kernel(KvCache c, KvAtte
             }
             if (few || lane == 0) {
                 head_m[g] = top == NEG_INF ? 0.f : top;
-                head_inv[g] = l == 0.f ? 0.f : 1.f / l;
+                head_inv[g] = l == 0.f ? 0.f : weights_by(n) / l;
             }
         }
         __syncthreads();

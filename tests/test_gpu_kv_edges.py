@@ -97,3 +97,16 @@ def test_attend_weights_of_zero_add_nothing_however_large_the_value(nbw, lens, g
     out = nbw.kv_attend(s.cache, q, s.lens)
     assert bool((out.abs() < 8).all())
     check_attend(s, q, out, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("lens", [[200, 1], [3000, 900]])
+@pytest.mark.parametrize("group,dim", [(2, 128), (12, 64), (3, 256)])
+def test_attend_values_near_the_largest_finite_one(nbw, lens, group, dim):  # noqa: F811
+    """All values 3.3e38, and with either sign: their mean is finite, their sum is not."""
+    s = Setup(nbw, lens, heads=2, page=16, dim=dim, seed=group)
+    q = s.normal(2, 2 * group, dim)
+    s.v[~s.v.isnan()] = 3.3e38
+    out = nbw.kv_attend(s.cache, q, s.lens)
+    check_attend(s, q, out, dim ** -0.5)
+    s.v[..., ::2] *= -1
+    check_attend(s, q, nbw.kv_attend(s.cache, q, s.lens), dim ** -0.5)
