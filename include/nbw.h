@@ -424,17 +424,18 @@ typedef struct nbw_kv_append_args {
 } nbw_kv_append_args;
 
 /* New tokens go into the cache: token i of row r (i = 0 for its first) takes
- * slot lens[r] + i.  A key's head x is, in fp32, divided by its root mean
- * square where k_norm is given, x * k_norm / sqrt(mean(x^2) + eps); then
- * rotated where rope is given, its halves (a, b) turning into
- * (a cos - b sin, b cos + a sin) at the token's position; then rounded once to
- * the cache's type (8 bits: of x / k_scale, limited to +-448, NaN kept).  A
- * value is stored as it is (or rounded to 8 bits likewise).  Queries take the
- * same two steps with q_norm and go to q_out.  pos of the new slots becomes
- * the token's position and acc 0; lens_out = lens + the row's new tokens.
- * Slots past the capacity, or on pages that are not there, are dropped.  A
- * position outside [0, rope_rows) turns keys and queries into NaN.  In place
- * (q_out = q) is fine; other overlaps of inputs and outputs are not.
+ * slot n + i, n = lens[r] within 0 and the capacity.  A key's head x is, in
+ * fp32, divided by its root mean square where k_norm is given,
+ * x * k_norm / sqrt(mean(x^2) + eps); then rotated where rope is given, its
+ * halves (a, b) turning into (a cos - b sin, b cos + a sin) at the token's
+ * position; then rounded once to the cache's type (8 bits: of x / k_scale,
+ * limited to +-448, NaN kept).  A value is stored as it is (or rounded to 8 bits
+ * likewise).  Queries take the same two steps with q_norm and go to q_out.  pos
+ * of the new slots becomes the token's position and acc 0; lens_out = n + the
+ * row's new tokens.  Slots past the capacity, or on pages that are not there,
+ * are dropped.  A position outside [0, rope_rows) turns keys and queries into
+ * NaN.  In place (q_out = q) is fine; other overlaps of inputs and outputs are
+ * not.
  * Errors: NBW_EINVAL, NBW_EALIGN, NBW_EUNSUPPORTED (dim, page or type), NBW_EHIP. */
 nbw_status nbw_kv_append(const nbw_kvcache *cache, const nbw_kv_append_args *args, void *stream);
 

@@ -27,7 +27,7 @@ __global__ __launch_bounds__(APPEND_THREADS) void kv_append_kernel(KvCache c, Kv
         const int row = (token - a.tokens) * APPEND_THREADS + tid;
         if (row < c.rows) {
             const int64_t added = a.cu ? (int64_t)a.cu[row + 1] - a.cu[row] : 1;
-            a.lens_out[row] = (int32_t)(a.lens[row] + added);
+            a.lens_out[row] = (int32_t)(kv_len(a.lens, row, c.cap) + added);
         }
         return;
     }
@@ -43,8 +43,8 @@ __global__ __launch_bounds__(APPEND_THREADS) void kv_append_kernel(KvCache c, Kv
         if (row >= c.rows) return;  // past the last row: cu does not reach the token
         first = a.cu[row];
     }
-    const int64_t slot64 = (int64_t)a.lens[row] + (token - first);
-    const bool fits = slot64 >= 0 && slot64 < c.cap && token >= first;
+    const int64_t slot64 = (int64_t)kv_len(a.lens, row, c.cap) + (token - first);
+    const bool fits = slot64 < c.cap && token >= first;
     const int slot = fits ? (int)slot64 : 0;
     const int32_t position = a.positions[token];
     const int lane = tid % L, unit = tid / L;

@@ -75,12 +75,13 @@ def append(k_pool, v_pool, table, lens, cu, positions, k, v, q=None, rope=None, 
     pages, _, page, _ = k_pool.shape
     cap = table.shape[1] * page
     q_out = None if q is None else np.zeros(q.shape)
+    lens = np.clip(np.asarray(lens), 0, cap)
     for r in range(len(lens)):
         for t in range(cu[r], cu[r + 1]):
             if q is not None:
                 q_out[t] = turned(q[t], positions[t], rope, q_norm, eps)
             slot = int(lens[r]) + t - cu[r]
-            if not 0 <= slot < cap:
+            if slot >= cap:
                 continue
             at = int(table[r][slot // page])
             if not 0 <= at < pages:
@@ -91,7 +92,7 @@ def append(k_pool, v_pool, table, lens, cu, positions, k, v, q=None, rope=None, 
                 pos[r, :, slot] = positions[t]
             if acc is not None:
                 acc[r, :, slot] = 0
-    return k_pool, v_pool, q_out, pos, acc, np.asarray(lens) + np.diff(cu)
+    return k_pool, v_pool, q_out, pos, acc, lens + np.diff(cu)
 
 
 def evict(k_pool, v_pool, table, lens, acc, pos, budget, sink, recent, acc_out, pos_out):

@@ -9,6 +9,8 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import kv as okv
+
 from test_gpu_kv import BF16, FP8, Setup, check_attend, f64, nbw  # noqa: F401  (nbw: the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -110,3 +112,37 @@ def test_attend_values_near_the_largest_finite_one(nbw, lens, group, dim):  # no
     check_attend(s, q, out, dim ** -0.5)
     s.v[..., ::2] *= -1
     check_attend(s, q, nbw.kv_attend(s.cache, q, s.lens), dim ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("many", [False, True])
+def test_append_bounds_the_lengths(nbw, dtype, many):  # noqa: F811
+    """A length below 0 counts as 0, one above the capacity as the capacity, in the slots and in the lengths that come back."""
+    s = Setup(nbw, [48, 48, 48, 20], page=16, dtype=dtype)
+    old = [-5, 1 << 30, -2**31, 20]
+    added = [7, 2, 1, 3] if many else [1] * 4
+    tokens = sum(added)
+    k, v = s.normal(tokens, 2, 128), s.normal(tokens, 2, 128)
+    positions = np.arange(100, 100 + tokens, dtype=np.int32)
+    cu = np.concatenate([[0], np.cumsum(added)]).astype(np.int32)
+    pos, acc = torch.full((4, 2, 48), -4, dtype=torch.int32, device="cuda"), torch.ones((4, 2, 48), device="cuda")
+    bits = torch.uint8 if dtype == FP8 else torch.int16
+    kept = [x.clone() for x in (s.k, s.v)]
+    _, lens = nbw.kv_append(s.cache, k, v, torch.tensor(old, dtype=torch.int32, device="cuda"), torch.from_numpy(positions).cuda(),
+                            cu=torch.from_numpy(cu).cuda() if many else None, pos=pos, acc=acc)
+    # the oracle moves numbers: which token is in a slot (0: what was there)
+    which = np.arange(1, tokens + 1)[:, None, None] * np.ones((tokens, 2, 128))
+    blank = np.zeros(s.k.shape)
+    at, _, _, wpos, wacc, wlens = okv.append(blank, blank, s.table_np, old, cu, positions, which, which, pos=f64(pos) * 0 - 4,
+                                             acc=f64(acc) * 0 + 1)
+    assert lens.tolist() == wlens.tolist() == [added[0], 48 + added[1], added[2], 20 + added[3]]
+    assert np.array_equal(f64(pos), wpos) and np.array_equal(f64(acc), wacc)
+    for new, pool, was, scale in ((k, s.k, kept[0], s.scales[0]), (v, s.v, kept[1], s.scales[1])):
+        x = new.float() if scale is None else (new.float() / scale[None, :, None]).clamp(-448, 448)
+        x = x.to(dtype)
+        want = was.clone()
+        for t in range(tokens):
+            page, place = np.argwhere(at[:, 0, :, 0] == t + 1).reshape(-1, 2).T
+            if len(page):
+                want[int(page[0]), :, int(place[0])] = x[t]
+        assert torch.equal(pool.view(bits), want.view(bits))

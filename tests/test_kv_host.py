@@ -88,6 +88,15 @@ def test_append_places_tokens_and_drops_what_does_not_fit():
     assert acc[:, 0].tolist() == [[1, 0, 0, 1], [0, 0, 1, 1]] and lens.tolist() == [3, 3]
 
 
+def test_append_bounds_the_lengths():
+    k0 = np.zeros((3, 1, 2, 4))
+    new = np.arange(1, 6)[:, None, None] * np.ones((5, 1, 4))
+    k, _, _, pos, _, lens = okv.append(k0, k0, np.array([[2], [1], [0]]), [-7, 9, 1], [0, 2, 3, 5], [11, 12, 13, 14, 15], new, new,
+                                       pos=np.zeros((3, 1, 2)))
+    assert k[:, 0, :, 0].tolist() == [[0, 4], [0, 0], [1, 2]]  # row 0 from slot 0 on, row 1 is full, row 2's second does not fit
+    assert pos[:, 0].tolist() == [[11, 12], [0, 0], [0, 14]] and lens.tolist() == [2, 3, 3]
+
+
 def test_evict_worked_example():
     acc = np.array([[[5.0, 1.0, 3.0, 3.0, np.nan, 9.0, 3.0, 0.0]]])
     pos = np.arange(8).reshape(1, 1, 8)
