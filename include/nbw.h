@@ -495,10 +495,10 @@ typedef struct nbw_kv_evict_args {
 
 /* Rows longer than `budget` keep, for each head, the budget slots of the
  * largest key, the lowest slot first among equals, where a slot's key is
- *     +infinity  if its position is below sink, or among the `recent` last
- *                (above the head's largest position - recent);
- *     -infinity  if its total is NaN;
- *     its total  otherwise.
+ *     above every total  if its position is below sink, or among the `recent`
+ *                        last (above the head's largest position - recent);
+ *     -infinity          if its total is NaN;
+ *     its total          otherwise.
  * The i-th slot at or past the budget that stays (ascending) takes the place
  * of the i-th slot below it that goes: key, value, total and position.  Every
  * other slot below the budget stays where it is, so no more rows move than

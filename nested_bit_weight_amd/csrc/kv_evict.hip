@@ -11,7 +11,7 @@
 //    histogram of 2048 bins over the 11 bits below the leading bits that all
 //    candidates share, the bin that holds the wanted key, and again inside it,
 //    until a bin is wanted whole or holds one value.  On attention totals the first
-//    two passes do.  Protected slots, which all share the key +infinity, are only
+//    two passes do.  Protected slots, which all share the largest key, are only
 //    counted.  (Bins over fixed leading bits put most totals, alike in sign and
 //    exponent, into a few bins, whose atomics then wait for each other.)
 //    A slot's place in the list of gaps (below the budget, not kept) or movers
@@ -45,7 +45,7 @@ typedef float f32x4_ev __attribute__((ext_vector_type(4)));
 typedef int32_t i32x4_ev __attribute__((ext_vector_type(4)));
 
 constexpr int EVICT_BINS_LOG2 = 11, EVICT_BINS = 1 << EVICT_BINS_LOG2;
-constexpr uint32_t KEY_INF = 0xFF800000u, KEY_NEG_INF = 0x007FFFFFu;
+constexpr uint32_t KEY_HELD = 0xFFFFFFFFu, KEY_NEG_INF = 0x007FFFFFu;  // protected: above +infinity's, 0xFF800000
 constexpr int EVICT_ROW = 16384;     // the longest row that one workgroup ranks (32 keys a thread spill: at 32768 both ways took 46-49 us)
 constexpr int PART_THREADS = 256, PART_GROUPS = 4, PART = PART_THREADS * PART_GROUPS * 4;  // longer ones: slots of a workgroup
 constexpr int MOVES = 16;           // moves of a workgroup of the second launch
@@ -69,7 +69,7 @@ struct EvictPlan {
 
 // Keys as unsigned numbers of the same order.  -0 and +0 are equal.
 __device__ __forceinline__ uint32_t evict_key(float acc, int32_t pos, int32_t newest, const KvEvict &a) {
-    if (pos < a.sink || (int64_t)pos > (int64_t)newest - a.recent) return KEY_INF;
+    if (pos < a.sink || (int64_t)pos > (int64_t)newest - a.recent) return KEY_HELD;
     if (acc != acc) return KEY_NEG_INF;
     const uint32_t u = __float_as_uint(acc == 0.f ? 0.f : acc);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
@@ -305,11 +305,11 @@ __global__ __launch_bounds__(THREADS) void kv_evict_kernel(KvCache c, KvEvict a,
         return;
     }
 
-    // The newest position, then the keys; how many are +infinity and the range of the rest.
+    // The newest position, then the keys; how many are protected and the range of the rest.
     uint32_t key[GROUPS][4];
     auto slot_of = [&](int g) { return (g * THREADS + tid) * 4; };
     int32_t newest = INT32_MIN;
-    int inf = 0;
+    int held = 0;
     uint32_t lo = 0xFFFFFFFFu, hi = 0;
     {
         Four<float> x[GROUPS];
@@ -337,8 +337,8 @@ __global__ __launch_bounds__(THREADS) void kv_evict_kernel(KvCache c, KvEvict a,
                 const bool there = slot_of(g) + e < n;
                 const uint32_t k = there ? evict_key(x[g].v[e], y[g].v[e], newest, a) : 0;  // 0: below every key
                 key[g][e] = k;
-                inf += k == KEY_INF;
-                if (there && k != KEY_INF) {
+                held += k == KEY_HELD;
+                if (there && k != KEY_HELD) {
                     lo = min(lo, k);
                     hi = max(hi, k);
                 }
@@ -404,26 +404,26 @@ __global__ __launch_bounds__(THREADS) void kv_evict_kernel(KvCache c, KvEvict a,
         }
     } else {
         __syncthreads();
-        inf = wave_sum(inf);
+        held = wave_sum(held);
         lo = wave_min_u(lo);
         hi = wave_max_u(hi);
         if (lane == 0) {
-            red[0][wave] = inf;
+            red[0][wave] = held;
             red[1][wave] = (int)lo;
             red[2][wave] = (int)hi;
         }
         __syncthreads();
-        inf = 0;
+        held = 0;
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
-            inf += red[0][w];
+            held += red[0][w];
             lo = min(lo, (uint32_t)red[1][w]);
             hi = max(hi, (uint32_t)red[2][w]);
         }
 
-        Limit lim = {KEY_INF, b, inf == b};
-        if (inf < b) {
-            lim.want = b - inf;
+        Limit lim = {KEY_HELD, b, held == b};
+        if (held < b) {
+            lim.want = b - held;
             while (lo != hi) {  // the want-th largest of the keys within [lo, hi]
                 const int bits = 32 - __builtin_clz(lo ^ hi);
                 const int shift = bits > EVICT_BINS_LOG2 ? bits - EVICT_BINS_LOG2 : 0;
@@ -583,22 +583,22 @@ __global__ __launch_bounds__(PART_THREADS) void kv_evict_part_kernel(KvCache c, 
         if (lim.all) return;
         for (int i = tid; i < EVICT_BINS; i += THREADS) hist[i] = 0;
         __syncthreads();
-        int inf = 0;
+        int held = 0;
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const uint32_t k = key[g][e];
-                if (STAGE == COUNT0) {  // +infinity, all protected slots' key, is counted apart
-                    if (k == KEY_INF) ++inf;
+                if (STAGE == COUNT0) {  // all protected slots' key is counted apart
+                    if (k == KEY_HELD) ++held;
                     else if (k) atomicAdd(&hist[k >> 21], 1);
                 } else if (k >> level_shift(LEVEL - 1) == lim.key >> level_shift(LEVEL - 1)) {
                     atomicAdd(&hist[(k >> level_shift(LEVEL)) & (STAGE == COUNT1 ? 2047 : 1023)], 1);
                 }
             }
         if (STAGE == COUNT0) {
-            inf = wave_sum(inf);
-            if (lane == 0 && inf) atomicAdd(&hist[KEY_INF >> 21], inf);
+            held = wave_sum(held);
+            if (lane == 0 && held) atomicAdd(&hist[KEY_HELD >> 21], held);
         }
         __syncthreads();
         for (int i = tid; i < EVICT_BINS; i += THREADS)

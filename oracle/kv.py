@@ -106,9 +106,10 @@ def evict(k_pool, v_pool, table, lens, acc, pos, budget, sink, recent, acc_out, 
             a, p = np.array(acc[r, h, :n]), np.array(pos[r, h, :n])
             if n > budget:
                 newest = p.max()
-                key = [np.inf if (x < sink or x > newest - recent) else -np.inf if np.isnan(y) else y
+                # protected slots first, whatever their totals
+                key = [(0, 0) if (x < sink or x > newest - recent) else (1, np.inf if np.isnan(y) else -y)
                        for x, y in zip(p.tolist(), a.tolist())]
-                kept = sorted(sorted(range(n), key=lambda j: (-key[j], j))[:budget])
+                kept = sorted(sorted(range(n), key=lambda j: (key[j], j))[:budget])
                 kept_set = set(kept)
                 gaps = [j for j in range(budget) if j not in kept_set]
                 for to, of in zip(gaps, [j for j in kept if j >= budget]):

@@ -146,3 +146,29 @@ def test_append_bounds_the_lengths(nbw, dtype, many):  # noqa: F811
             if len(page):
                 want[int(page[0]), :, int(place[0])] = x[t]
         assert torch.equal(pool.view(bits), want.view(bits))
+
+
+@pytest.mark.parametrize("lens,budget,sink,recent", [
+    ([70, 66], 64, 3, 5), ([66, 64], 64, 2, 62), ([700, 300], 200, 4, 100), ([3000, 900], 800, 0, 800), ([20000, 30000], 9000, 16, 3000),
+    ([18000], 12000, 0, 12000),
+])
+def test_evict_protected_slots_stay_beside_infinite_totals(nbw, lens, budget, sink, recent):  # noqa: F811
+    """More totals of +infinity than the budget has room for, in lower slots than the protected ones."""
+    s = Setup(nbw, lens, heads=2, page=32, dim=64, seed=budget)
+    shape = (len(lens), 2, s.cap)
+    acc = s.rng.uniform(0, 1, shape).astype(np.float32)
+    acc[s.rng.random(shape) < 0.9] = np.inf
+    pos = np.stack([[s.rng.permutation(n) if h else np.arange(n) for h in range(2)] for n in [s.cap] * len(lens)]).astype(np.int32)
+    for r, n in enumerate(lens):  # head 0: the newest lie last and have nothing
+        acc[r, 0, n - recent:n] = -np.inf
+    acc_t, pos_t = torch.from_numpy(acc).cuda(), torch.from_numpy(pos).cuda()
+    acc_out, pos_out = torch.zeros_like(acc_t), torch.full_like(pos_t, -7)
+    k0, v0 = (x.view(torch.int16).cpu().numpy() for x in (s.k, s.v))
+    want = okv.evict(k0, v0, s.table_np, lens, acc, pos, budget, sink, recent, acc_out.cpu().numpy(), pos_out.cpu().numpy())
+    nbw.kv_evict(s.cache, acc_t, pos_t, s.lens, budget, sink=sink, recent=recent, acc_out=acc_out, pos_out=pos_out)
+    for r, n in enumerate(lens):
+        if n > budget:
+            held = set(range(sink)) | set(range(n - recent, n))
+            assert held <= set(pos_out[r, 0, :budget].tolist())
+    assert np.array_equal(pos_out.cpu().numpy(), want[3]) and np.array_equal(acc_out.cpu().numpy(), want[2].astype(np.float32))
+    assert np.array_equal(s.k.view(torch.int16).cpu().numpy(), want[0]) and np.array_equal(s.v.view(torch.int16).cpu().numpy(), want[1])

@@ -116,6 +116,16 @@ def test_evict_worked_example():
     assert np.array_equal(k2, k) and lens.tolist() == [8] and p2[0, 0].tolist() == list(range(8))
 
 
+def test_evict_protected_slots_come_before_infinite_totals():
+    inf = np.inf
+    k = np.arange(6.0).reshape(3, 1, 2, 1)
+    blank = np.full((1, 1, 6), -1.0), np.full((1, 1, 6), -1)
+    k2, _, a2, p2, _ = okv.evict(k, -k, np.array([[0, 1, 2]]), [6], np.array([[[inf, inf, inf, 1.0, -inf, 0.0]]]),
+                                 np.array([[[4, 3, 1, 2, 0, 5]]]), 3, 1, 1, *blank)
+    assert k2.ravel()[:3].tolist() == [0, 4, 5] and p2[0, 0].tolist() == [4, 0, 5, -1, -1, -1]
+    assert a2[0, 0].tolist() == [inf, -inf, 0, -1, -1, -1]
+
+
 # ---------------------------------------------------------------------------
 # refusals
 
