@@ -376,6 +376,8 @@ nbw_status nbw_file_parse(const void *header, int64_t file_bytes, nbw_file_info 
  *    above max_len where a call takes one, as that bound.
  *  - Rows may share pages that are only read; nbw_kv_append and nbw_kv_evict
  *    write pages, which must then belong to one row.
+ *  - More (row, head) pairs, or units of work, than one launch takes (about 2^24)
+ *    are refused with NBW_EINVAL before anything is queued.
  * Running totals of the attention weights (fp32) and token positions (int32)
  * are kept apart from the pools, dense: [rows][heads][width * page].
  *
@@ -407,7 +409,7 @@ typedef struct nbw_kv_append_args {
     void *q_out;              /* with q: bf16 [tokens][q_heads][dim], may be q */
     int64_t k_ld, v_ld, q_ld, q_out_ld; /* elements from one token to the next: 0 (dense), or
                                  at least heads * dim (q_heads * dim) and a multiple of 8 */
-    int64_t tokens;           /* >= 0; below 2^31 */
+    int64_t tokens;           /* 0..2^24 - 2^13 */
     int32_t q_heads;
     float eps;                /* of the norms, >= 0 */
     const int32_t *cu;        /* NULL: one token for each row (tokens = rows).  Else [rows + 1],

@@ -423,7 +423,7 @@ nbw_status nbw_kv_append(const nbw_kvcache *cache, const nbw_kv_append_args *arg
     if (st != NBW_OK) return st;
     if (!args) return NBW_EINVAL;
     const nbw_kv_append_args &g = *args;
-    if (g.tokens < 0 || g.tokens > INT_MAX - (1 << 20)) return NBW_EINVAL;
+    if (g.tokens < 0 || g.tokens > nbw::APPEND_TOKENS) return NBW_EINVAL;
     if (!g.cu && g.tokens != c.rows) return NBW_EINVAL;
     if (c.rows == 0) return g.tokens == 0 ? NBW_OK : NBW_EINVAL;
     if (!g.lens || g.lens_out == g.lens) return NBW_EINVAL;
@@ -506,7 +506,7 @@ nbw_status nbw_kv_attend(const nbw_kvcache *cache, const nbw_kv_attend_args *arg
     int cus = 0;
     if ((st = cu_count(&cus)) != NBW_OK) return st;
     const int64_t need = nbw::kv_attend_workspace_bytes(c, g.q_heads, a.max_len, g.acc != nullptr, cus);
-    if (need < 0) return NBW_EINVAL;  // more units than an int counts
+    if (need < 0) return NBW_EINVAL;  // more than a launch takes
     if (need > 0 && (!g.workspace || g.workspace_bytes < need)) return NBW_ESCRATCH;
     a.q = (const uint16_t *)g.q;
     a.out = (uint16_t *)g.out;
@@ -547,7 +547,7 @@ nbw_status nbw_kv_evict(const nbw_kvcache *cache, const nbw_kv_evict_args *args,
         !aligned(g.pos_out, 4) || !aligned(g.lens_out, 4) || !aligned(g.workspace, 256))
         return NBW_EALIGN;
     const int64_t need = nbw::kv_evict_workspace_bytes(c, (int)g.budget, a.max_len);
-    if (need < 0) return NBW_EINVAL;  // more workgroups than an int counts
+    if (need < 0) return NBW_EINVAL;  // more than a launch takes
     if (need > 0 && (!g.workspace || g.workspace_bytes < need)) return NBW_ESCRATCH;
     a.acc = g.acc;
     a.pos = g.pos;

@@ -60,6 +60,11 @@ struct KvEvict {
     uint8_t *ws;
 };
 
+// Work-items that a launch takes in a dimension.
+constexpr int64_t MOST_ITEMS = ((int64_t)1 << 32) - 1;
+constexpr bool fits_launch(int64_t groups, int threads) { return groups <= MOST_ITEMS / threads; }
+constexpr int64_t APPEND_TOKENS = ((int64_t)1 << 24) - (1 << 13);  // 256 work-items each, and one for each row's length
+
 hipError_t launch_kv_append(const KvCache &c, const KvAppend &a, hipStream_t stream);
 int64_t kv_attend_workspace_bytes(const KvCache &c, int q_heads, int max_len, bool weights, int cu_count);
 hipError_t launch_kv_attend(const KvCache &c, const KvAttend &a, int cu_count, hipStream_t stream);

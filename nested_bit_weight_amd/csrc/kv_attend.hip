@@ -710,7 +710,7 @@ __global__ __launch_bounds__(ATTEND_THREADS, DIM > 128 ? 1 : 2) void kv_attend_k
     }
 }
 
-constexpr int JOIN_THREADS = 256;
+constexpr int JOIN_THREADS = ATTEND_THREADS;
 constexpr int FEW_PARTS = 6;
 
 // The second launch.  The first `sharers` workgroups add the weights to the
@@ -858,7 +858,8 @@ __global__ __launch_bounds__(JOIN_THREADS) void kv_join_kernel(KvCache c, KvAtte
     }
 }
 
-// The plan, its scratch laid out from `base`; returns the bytes (-1: too many units).
+// The plan, its scratch laid out from `base`; returns the bytes (-1: more units than an int
+// counts, or more workgroups than a launch takes).
 static int64_t attend_plan(const KvCache &c, int q_heads, int max_len, bool weights, int cu_count, uint8_t *base,
                            AttendPlan *pl) {
     pl->group = q_heads / c.heads;
@@ -880,6 +881,7 @@ static int64_t attend_plan(const KvCache &c, int q_heads, int max_len, bool weig
     if (pl->undivided) pl->wgs = (int)(c.rows * vheads);
     // Totals: eight units for each step of a workgroup, and a few workgroups for each CU.
     pl->sharers = weights ? (int)std::max<int64_t>(1, std::min<int64_t>((most + 7) / 8, (int64_t)cu_count * 4)) : 0;
+    if (!fits_launch(pl->undivided ? c.rows * vheads : (int64_t)c.rows * q_heads + pl->sharers, ATTEND_THREADS)) return -1;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         uint8_t *p = base ? base + at : nullptr;

@@ -658,15 +658,18 @@ __global__ __launch_bounds__(PART_THREADS) void kv_evict_part_kernel(KvCache c, 
 
 template <int ROW_BYTES, bool NT>
 __global__ __launch_bounds__(256) void kv_move_kernel(KvCache c, KvEvict a, EvictPlan pl, int parts) {
-    const int which = blockIdx.x / parts, first = blockIdx.x % parts * MOVES;
-    const int count = pl.counts[which];
-    if (first >= count) return;
+    const int which = blockIdx.x / parts, count = pl.counts[which];
     const int32_t *to = pl.lists + (int64_t)which * 2 * pl.most;
-    make_moves<ROW_BYTES, 256, NT>(c, a, which / c.heads, which % c.heads, to + first, to + pl.most + first,
-                               min(MOVES, count - first));
+    for (int64_t first = (int64_t)(blockIdx.x % parts) * MOVES; first < count; first += (int64_t)parts * MOVES)
+        make_moves<ROW_BYTES, 256, NT>(c, a, which / c.heads, which % c.heads, to + first, to + pl.most + first,
+                                       (int)min((int64_t)MOVES, count - first));
 }
 
-static int64_t evict_plan(const KvCache &c, int budget, int max_len, uint8_t *base, EvictPlan *pl) {  // -1: too many workgroups
+// Threads of the workgroup that ranks one (row, head): the smallest that holds the longest
+// row's keys, 4, 8 or 16 a thread.  (Rows of 2049 slots as 256 threads with 16 keys: 17.6 us, and 14 so.)
+static int ranking_threads(int max_len) { return max_len <= 1024 ? 256 : max_len <= 4096 ? 512 : 1024; }
+
+static int64_t evict_plan(const KvCache &c, int budget, int max_len, uint8_t *base, EvictPlan *pl) {  // -1: more than a launch takes
     const int64_t lists = (int64_t)c.rows * c.heads;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -677,7 +680,7 @@ static int64_t evict_plan(const KvCache &c, int budget, int max_len, uint8_t *ba
     *pl = EvictPlan{};
     pl->most = std::max(0, std::min(budget, max_len - budget));
     if (max_len > EVICT_ROW) pl->parts = (max_len + PART - 1) / PART;
-    if (lists * std::max(pl->parts, (pl->most + MOVES - 1) / MOVES) > INT32_MAX) return -1;
+    if (!(pl->parts ? fits_launch(lists * pl->parts, PART_THREADS) : fits_launch(lists, ranking_threads(max_len)))) return -1;
     if (pl->most) {
         if (pl->parts || pl->most > FUSED_MOVES) {
             pl->lists = (int32_t *)take(lists * 2 * pl->most * 4);
@@ -701,7 +704,9 @@ int64_t kv_evict_workspace_bytes(const KvCache &c, int budget, int max_len) {
 
 template <int ROW_BYTES>
 static void launch_moves(const KvCache &c, const KvEvict &a, const EvictPlan &pl, hipStream_t stream) {
-    const int64_t lists = (int64_t)c.rows * c.heads, each = (pl.most + MOVES - 1) / MOVES;
+    // A workgroup for each 16 moves, or for several times 16 where a launch does not take as many.
+    const int64_t lists = (int64_t)c.rows * c.heads;
+    const int64_t each = std::min<int64_t>((pl.most + MOVES - 1) / MOVES, MOST_ITEMS / 256 / lists);
     const dim3 moves((unsigned)(lists * each)), threads(256);
     // The rows are read for the last time.  Saying so pays where they are many, and
     // costs where the caches still hold them: with up to 201 MB of them 77 us so and
@@ -717,14 +722,11 @@ hipError_t launch_kv_evict(const KvCache &c, const KvEvict &a, hipStream_t strea
     evict_plan(c, a.budget, a.max_len, a.ws, &pl);
     pl.vec = c.cap % 4 == 0 && (((uintptr_t)a.acc | (uintptr_t)a.pos | (uintptr_t)a.acc_out | (uintptr_t)a.pos_out) & 15) == 0;
     const dim3 grid((unsigned)c.rows * c.heads);
-    // The smallest workgroup that holds the longest row's keys, 4, 8 or 16 a thread.
-    // (Rows of 2049 slots as 256 threads with 16 keys: 17.6 us, and 14 so.)
-    if (a.max_len <= 1024) {
-        hipLaunchKernelGGL((kv_evict_kernel<256, 1>), grid, dim3(256), 0, stream, c, a, pl);
-    } else if (a.max_len <= 4096) {
-        hipLaunchKernelGGL((kv_evict_kernel<512, 2>), grid, dim3(512), 0, stream, c, a, pl);
-    } else if (!pl.parts) {
-        hipLaunchKernelGGL((kv_evict_kernel<1024, 4>), grid, dim3(1024), 0, stream, c, a, pl);
+    if (!pl.parts) {
+        const int n = ranking_threads(a.max_len);
+        if (n == 256) hipLaunchKernelGGL((kv_evict_kernel<256, 1>), grid, dim3(n), 0, stream, c, a, pl);
+        else if (n == 512) hipLaunchKernelGGL((kv_evict_kernel<512, 2>), grid, dim3(n), 0, stream, c, a, pl);
+        else hipLaunchKernelGGL((kv_evict_kernel<1024, 4>), grid, dim3(n), 0, stream, c, a, pl);
     } else {
         const dim3 parts((unsigned)((int64_t)grid.x * pl.parts)), threads(PART_THREADS);
         if (pl.most) {

@@ -172,3 +172,68 @@ def test_evict_protected_slots_stay_beside_infinite_totals(nbw, lens, budget, si
             assert held <= set(pos_out[r, 0, :budget].tolist())
     assert np.array_equal(pos_out.cpu().numpy(), want[3]) and np.array_equal(acc_out.cpu().numpy(), want[2].astype(np.float32))
     assert np.array_equal(s.k.view(torch.int16).cpu().numpy(), want[0]) and np.array_equal(s.v.view(torch.int16).cpu().numpy(), want[1])
+
+
+def test_attend_refuses_more_than_a_launch_takes(nbw):  # noqa: F811
+    import ctypes
+
+    from nested_bit_weight_amd import kv
+    # one workgroup for each (row, head); then divided, the second launch with one for each query head
+    for rows, heads, width, q_heads, totals, fits in ((1 << 19, 16, 1, 16, 0, True), (1 << 19, 32, 1, 32, 0, False),
+                                                      (1 << 15, 8, 512, 256, 1, True), (1 << 15, 8, 512, 512, 1, False)):
+        view = kv.KVView(1 << 20, 1 << 20, 10, heads, 16, 64, 0, None, None, 1 << 20, rows, width, 0)
+        need = nbw.library().nbw_kv_attend_workspace_bytes(ctypes.byref(view), q_heads, 0, totals)
+        assert (need >= 0) == fits, (rows, heads, width, q_heads, need)
+
+
+def moves(acc, pos, n, budget, sink, recent):
+    """The places below the budget that go and the slots past it that stay, of one head's first n slots (numpy, no NaN)."""
+    a, p = acc[:n].astype(np.float64), pos[:n].astype(np.int64)
+    held = (p < sink) | (p > p.max() - recent)
+    first = np.lexsort((np.arange(n), -a, ~held))[:budget]
+    stays = np.zeros(n, dtype=bool)
+    stays[first] = True
+    return np.flatnonzero(~stays[:budget]), budget + np.flatnonzero(stays[budget:])
+
+
+def check_evict(nbw, cache, lens, table, acc, pos, budget, sink, recent, **kw):  # noqa: F811
+    """One eviction on the GPU against `moves`, bit for bit."""
+    rows, heads = acc.shape[:2]
+    acc_out, pos_out = torch.full_like(acc, -7.0), torch.full_like(pos, -7)
+    bits = [x.view(torch.uint8 if x.element_size() == 1 else torch.int16) for x in (cache.k, cache.v)]
+    was = [x.clone() for x in bits]
+    lens_out = nbw.kv_evict(cache, acc, pos, lens, budget, sink=sink, recent=recent, acc_out=acc_out, pos_out=pos_out, **kw)
+    assert lens_out.tolist() == [min(n, budget) for n in lens.tolist()]
+    total = 0
+    for r, n in enumerate(lens.tolist()):
+        for h in range(heads if n else 0):
+            m = min(n, budget)
+            a, p = acc[r, h, :n].cpu().numpy(), pos[r, h, :n].cpu().numpy()
+            a2, p2 = a.copy(), p.copy()
+            if n > budget:
+                to, of = moves(a, p, n, budget, sink, recent)
+                a2[to], p2[to] = a[of], p[of]
+                total += len(to)
+                at = [(torch.from_numpy(table[r, j // cache.page].astype(np.int64)).cuda(), torch.from_numpy(j % cache.page).cuda())
+                      for j in (to, of)]
+                for x in was:
+                    x[at[0][0], h, at[0][1]] = x[at[1][0], h, at[1][1]]
+            assert np.array_equal(acc_out[r, h, :m].cpu().numpy(), a2[:m]) and np.array_equal(pos_out[r, h, :m].cpu().numpy(), p2[:m])
+            assert bool((acc_out[r, h, m:] == -7).all()) and bool((pos_out[r, h, m:] == -7).all())
+    assert torch.equal(bits[0], was[0]) and torch.equal(bits[1], was[1])
+    return total
+
+
+def test_evict_more_moves_than_a_launch_has_workgroups(nbw):  # noqa: F811
+    """512 rows of 8 heads in a table of 131072 slots, one of them full, brought down to half: 2^24 times 16 places for moves."""
+    lens = [131072] + [0] * 511
+    cache, n, table = rows_cache(nbw, lens, 8, 64, 256, 3)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    acc = torch.empty((512, 8, cache.capacity), device="cuda")
+    pos = torch.empty((512, 8, cache.capacity), dtype=torch.int32, device="cuda")
+    # the upper half has the larger totals in three slots of four: 49152 moves; all of them for the last head
+    acc[0] = torch.rand((8, cache.capacity), generator=g, device="cuda")
+    acc[0, :, 65536:] += (torch.arange(65536, device="cuda") % 4 > 0).float()
+    acc[0, 7, 65536:] += 2.0
+    pos[0] = torch.arange(cache.capacity, dtype=torch.int32, device="cuda")
+    assert check_evict(nbw, cache, n, table, acc, pos, 65536, 0, 100) > 7 * 45000 + 65535

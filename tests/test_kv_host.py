@@ -245,6 +245,22 @@ def test_workspace_sizes_refuse_bad_arguments(lib):
     assert lib.nbw_kv_evict_workspace_bytes(ctypes.byref(cache(width=20)), 100, 0) > 0
 
 
+def test_more_than_a_launch_takes_is_refused_before_anything_is_queued(lib):
+    size = lib.nbw_kv_evict_workspace_bytes
+    many = dict(rows=1 << 20, width=1, page=16)
+    assert size(ctypes.byref(cache(**many, heads=15)), 8, 0) == 0
+    assert size(ctypes.byref(cache(**many, heads=16)), 8, 0) == -1    # 2^24 workgroups of 256 threads
+    assert size(ctypes.byref(cache(rows=1 << 20, width=256, page=16, heads=8)), 8, 0) == -1   # 2^23 of 512
+    assert size(ctypes.byref(cache(rows=1 << 20, width=512, page=16, heads=4)), 8, 0) == -1   # 2^22 of 1024
+    assert size(ctypes.byref(cache(rows=1 << 14, width=4096, page=1024, heads=1)), 8, 0) == -1  # 1024 parts each
+    assert call(lib, "nbw_kv_evict", cache(**many, heads=16), evict_args(budget=8, sink=0)) == EINVAL
+    # a move launch is never more than one takes: 64 x 8 rows of 2^20 slots brought down to half
+    assert size(ctypes.byref(cache(rows=64, heads=8, width=4096, page=256)), 1 << 19, 0) > 0
+    for tokens in ((1 << 24) - (1 << 13) + 1, 1 << 24, (1 << 31) - (1 << 20)):
+        assert call(lib, "nbw_kv_append", cache(), append_args(cu=FAKE, tokens=tokens, k=FAKE + 2)) == EINVAL
+    assert call(lib, "nbw_kv_append", cache(), append_args(cu=FAKE, tokens=(1 << 24) - (1 << 13), k=FAKE + 2)) == EALIGN
+
+
 def test_binding_refuses_cpu_tensors():
     pool = torch.zeros((2, 1, 16, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError):
