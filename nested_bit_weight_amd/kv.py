@@ -272,8 +272,10 @@ def kv_attend(cache: KVCache, q, lens, *, scale: float | None = None, out=None, 
     qp, q_ld = cache._heads(q, "q", shape)
     if scale is None:
         scale = 0.0
-    elif not 0.0 < abs(scale) < 3e38:
-        raise ValueError("scale must be finite and not 0")
+    else:
+        scale = _f32(scale).value  # a number too small for fp32 would be 0, which stands for the default
+        if not 0.0 < abs(scale) < 3e38:
+            raise ValueError("scale must be finite and not 0 in fp32")
     if max_len is None:
         max_len = 0
     elif max_len < 1:

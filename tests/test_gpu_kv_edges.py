@@ -237,3 +237,13 @@ def test_evict_more_moves_than_a_launch_has_workgroups(nbw):  # noqa: F811
     acc[0, 7, 65536:] += 2.0
     pos[0] = torch.arange(cache.capacity, dtype=torch.int32, device="cuda")
     assert check_evict(nbw, cache, n, table, acc, pos, 65536, 0, 100) > 7 * 45000 + 65535
+
+
+def test_attend_scales_that_fp32_does_not_hold_are_refused(nbw):  # noqa: F811
+    s = Setup(nbw, [40, 7], page=16)
+    q = s.normal(2, 4, 128)
+    for scale in (1e-46, -1e-46, 0.0, 1e39, -1e300, math.inf, math.nan):
+        with pytest.raises(ValueError):
+            nbw.kv_attend(s.cache, q, s.lens, scale=scale)
+    for scale in (1e-30, -0.25, 1e-40):  # what it holds, subnormal numbers among it
+        check_attend(s, q, nbw.kv_attend(s.cache, q, s.lens, scale=scale), float(np.float32(scale)))
