@@ -48,6 +48,7 @@ class EvictArgs(ctypes.Structure):
                 ("workspace_bytes", _i64)]
 
 
+SIZES_KEPT = 64
 KV_DTYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
 
 
@@ -185,7 +186,10 @@ class KVCache:
                 raise ValueError("workspace must be 'auto', a tensor or None")
             nbytes = self._sizes.get(sizes)
             if nbytes is None:
-                nbytes = self._sizes[sizes] = _bytes(query(self._ref, *sizes))
+                nbytes = _bytes(query(self._ref, *sizes))
+                if len(self._sizes) >= SIZES_KEPT:  # a bound that grows with every token passes by here once
+                    self._sizes.clear()
+                self._sizes[sizes] = nbytes
             if nbytes == 0:
                 return None, 0
             workspace = _workspace(self._dev, stream, nbytes)

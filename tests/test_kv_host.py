@@ -261,6 +261,24 @@ def test_more_than_a_launch_takes_is_refused_before_anything_is_queued(lib):
     assert call(lib, "nbw_kv_append", cache(), append_args(cu=FAKE, tokens=(1 << 24) - (1 << 13), k=FAKE + 2)) == EALIGN
 
 
+def test_workspace_sizes_that_a_cache_remembers_are_few():
+    c = nbw.KVCache.__new__(nbw.KVCache)
+    c._sizes, c._ref, c._dev = {}, None, 0
+    asked = []
+
+    def query(ref, *sizes):
+        asked.append(sizes)
+        return 0
+
+    for step in range(1, 2000):  # a bound of the lengths that grows with every token
+        assert c._scratch("auto", query, (32, step, True), 0) == (None, 0)
+        assert len(c._sizes) <= kv.SIZES_KEPT
+    last = len(asked)
+    for _ in range(3):
+        c._scratch("auto", query, (32, 1999, True), 0)
+    assert last == 1999 and len(asked) == last
+
+
 def test_binding_refuses_cpu_tensors():
     pool = torch.zeros((2, 1, 16, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError):
