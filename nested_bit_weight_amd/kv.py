@@ -10,7 +10,7 @@ a table of page numbers for each sequence; see ``include/nbw.h`` for every detai
     lens2 = kv_evict(cache, acc, pos, lens1, budget, recent=64, acc_out=acc2, pos_out=pos2)
 
 As everywhere in this package the calls only marshal arguments, queue the work on the
-current stream of the tensors' GPU and raise if the library is not built.
+current stream of the tensors' GPU, whichever GPU is the current one, and raise if the library is not built.
 """
 from __future__ import annotations
 
@@ -64,6 +64,8 @@ def declare(lib) -> None:
     lib.nbw_kv_evict_workspace_bytes.restype = _i64
 
 
+# The GPU that kernels go to (the bare getter: the tensors are there, so the runtime is up).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _BF16, _F32, _INT32 = torch.bfloat16, torch.float32, torch.int32
 
 
@@ -170,7 +172,8 @@ class KVCache:
 
     def attend_workspace_bytes(self, q_heads: int, max_len: int = 0, weights: bool = False) -> int:
         """Bytes of scratch kv_attend needs."""
-        return _bytes(_lib().nbw_kv_attend_workspace_bytes(self._ref, q_heads, max_len, int(weights)))
+        with torch.cuda.device(self._dev):  # they depend on its number of compute units
+            return _bytes(_lib().nbw_kv_attend_workspace_bytes(self._ref, q_heads, max_len, int(weights)))
 
     def evict_workspace_bytes(self, budget: int, max_len: int = 0) -> int:
         """Bytes of scratch kv_evict needs."""
@@ -217,6 +220,10 @@ def kv_append(cache: KVCache, k, v, lens, positions, *, q=None, cu=None, rope=No
     [tokens][q_heads][dim], normalised and rotated alongside into ``q_out`` (which may be q).
     ``pos`` and ``acc`` ([rows][heads][capacity], int32 and fp32) get the tokens' positions
     and zeros.  Returns (q_out or None, lens + new tokens)."""
+    if _current_device() != cache._dev:
+        with torch.cuda.device(cache._dev):
+            return kv_append(cache, k, v, lens, positions, q=q, cu=cu, rope=rope, q_norm=q_norm, k_norm=k_norm, eps=eps,
+                             q_out=q_out, pos=pos, acc=acc, lens_out=lens_out)
     if not isinstance(k, torch.Tensor):
         raise TypeError("k must be a torch.Tensor")
     tokens, rows, heads, index = k.size(0) if k.dim() else 0, cache.rows, cache.heads, cache._dev
@@ -271,6 +278,10 @@ def kv_attend(cache: KVCache, q, lens, *, scale: float | None = None, out=None, 
     binding's buffer of this device and stream), or a uint8 tensor of at least
     ``cache.attend_workspace_bytes(...)`` bytes, as a captured graph should have."""
     index = cache._dev
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return kv_attend(cache, q, lens, scale=scale, out=out, acc=acc, acc_out=acc_out, decay=decay, max_len=max_len,
+                             workspace=workspace)
     shape = cache._queries(q, cache.rows)
     q_heads = shape[1]
     qp, q_ld = cache._heads(q, "q", shape)
@@ -313,6 +324,10 @@ def kv_evict(cache: KVCache, acc, pos, lens, budget: int, *, sink: int = 0, rece
     of their own, of the same shapes).  Returns min(lens, budget) in ``lens_out``.
     ``max_len`` and ``workspace`` as for :func:`kv_attend`."""
     index, track = cache._dev, cache._track
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return kv_evict(cache, acc, pos, lens, budget, sink=sink, recent=recent, acc_out=acc_out, pos_out=pos_out,
+                            lens_out=lens_out, max_len=max_len, workspace=workspace)
     if max_len is None:
         max_len = 0
     elif max_len < 1:

@@ -247,3 +247,42 @@ def test_attend_scales_that_fp32_does_not_hold_are_refused(nbw):  # noqa: F811
             nbw.kv_attend(s.cache, q, s.lens, scale=scale)
     for scale in (1e-30, -0.25, 1e-40):  # what it holds, subnormal numbers among it
         check_attend(s, q, nbw.kv_attend(s.cache, q, s.lens, scale=scale), float(np.float32(scale)))
+
+
+def test_calls_go_to_the_tensors_gpu(nbw, monkeypatch):  # noqa: F811
+    """With another GPU the current one (as far as the binding can tell), every call makes the tensors' its own for as long
+    as it takes, and its results are the same."""
+    from nested_bit_weight_amd import kv
+    s = Setup(nbw, [3000, 40], page=16, room=2)
+    q, k = s.normal(2, 4, 128), s.normal(2, 2, 128)
+    acc, pos = s.totals(), torch.arange(s.cap, dtype=torch.int32, device="cuda").repeat(2, 2, 1)
+    positions = torch.tensor([3000, 40], dtype=torch.int32, device="cuda")
+    start = s.k.clone(), s.v.clone()
+
+    def step():
+        s.k.copy_(start[0]), s.v.copy_(start[1])
+        _, lens = nbw.kv_append(s.cache, k, k, s.lens, positions)
+        total, acc2, pos2 = acc.clone(), torch.zeros_like(acc), torch.zeros_like(pos)
+        out = nbw.kv_attend(s.cache, q, lens, acc=total)
+        left = nbw.kv_evict(s.cache, total, pos, lens, 1000, acc_out=acc2, pos_out=pos2)
+        return [x.clone() for x in (lens, out, total, acc2, pos2, left, s.k.view(torch.int16), s.v.view(torch.int16))]
+
+    want = step()
+    current, entered = [1], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            entered.append(self.index)
+            self.was, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.was
+
+    monkeypatch.setattr(kv, "_current_device", lambda: current[0])
+    monkeypatch.setattr(kv.torch.cuda, "device", Device)
+    got = step()
+    assert entered == [0, 0, 0] and current == [1]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
