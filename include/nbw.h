@@ -396,7 +396,7 @@ typedef struct nbw_kvcache {
     int32_t dtype;         /* nbw_kvdtype */
     const float *k_scale;  /* NBW_KV_FP8: [heads], positive; else NULL */
     const float *v_scale;
-    const int32_t *table;  /* [rows][table_ld] */
+    const int32_t *table;  /* [rows][table_ld]; may be NULL if rows is 0 */
     int64_t rows;          /* sequences, >= 0 */
     int64_t width;         /* pages of a row, >= 1; width * page <= 2^30 */
     int64_t table_ld;      /* elements from one table row to the next: 0 (= width) or >= width */

@@ -119,7 +119,7 @@ nbw_status check_ld(int64_t ld, int64_t cols, int64_t *out) {
 
 // A cache's own fields, and the form its kernels take.  Rows of 0 are fine.
 nbw_status check_cache(const nbw_kvcache *c, nbw::KvCache *out) {
-    if (!c || !c->k || !c->v || !c->table) return NBW_EINVAL;
+    if (!c || !c->k || !c->v || (!c->table && c->rows != 0)) return NBW_EINVAL;  // an empty tensor has no address
     if (c->dim != 64 && c->dim != 128 && c->dim != 256) return NBW_EUNSUPPORTED;
     if (c->dtype != NBW_KV_BF16 && c->dtype != NBW_KV_FP8) return NBW_EUNSUPPORTED;
     if (c->page < 1 || c->page > 4096 || (c->page & (c->page - 1))) return NBW_EUNSUPPORTED;

@@ -286,3 +286,21 @@ def test_calls_go_to_the_tensors_gpu(nbw, monkeypatch):  # noqa: F811
     got = step()
     assert entered == [0, 0, 0] and current == [1]
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_batch_without_rows(nbw):  # noqa: F811
+    """Every sequence has ended: the calls take empty tensors and give empty ones."""
+    pool = torch.zeros((4, 2, 16, 128), dtype=BF16, device="cuda")
+    ints = lambda *shape: torch.zeros(shape, dtype=torch.int32, device="cuda")  # noqa: E731
+    heads = lambda h: torch.zeros((0, h, 128), dtype=BF16, device="cuda")  # noqa: E731
+    cache = nbw.KVCache(pool, pool.clone(), ints(0, 3))
+    acc, pos = torch.zeros((0, 2, 48), device="cuda"), ints(0, 2, 48)
+    assert cache.attend_workspace_bytes(8, weights=True) == 0 and cache.evict_workspace_bytes(10) == 0
+    q_out, lens = nbw.kv_append(cache, heads(2), heads(2), ints(0), ints(0), q=heads(8), pos=pos, acc=acc)
+    assert q_out.shape == (0, 8, 128) and lens.shape == (0,)
+    assert nbw.kv_attend(cache, heads(8), ints(0), acc=acc).shape == (0, 8, 128)
+    assert nbw.kv_evict(cache, acc, pos, ints(0), 10, acc_out=acc.clone(), pos_out=pos.clone()).shape == (0,)
+    # rows without a new token, and with none at all
+    s = Setup(nbw, [5, 0], page=16, room=2)
+    _, lens = nbw.kv_append(s.cache, heads(2), heads(2), s.lens, ints(0), cu=ints(3))
+    assert lens.tolist() == [5, 0]

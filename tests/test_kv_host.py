@@ -234,6 +234,15 @@ def test_empty_batches_queue_nothing(lib):
     assert call(lib, "nbw_kv_evict", none, evict_args(acc=None)) == OK
 
 
+def test_a_batch_without_rows_needs_no_table(lib):
+    none = cache(rows=0, table=None)
+    assert call(lib, "nbw_kv_append", none, append_args(tokens=0)) == OK
+    assert call(lib, "nbw_kv_attend", none, attend_args(q=None, out=None, lens=None)) == OK
+    assert call(lib, "nbw_kv_evict", none, evict_args(acc=None)) == OK
+    assert lib.nbw_kv_evict_workspace_bytes(ctypes.byref(none), 40, 0) == 0
+    assert call(lib, "nbw_kv_attend", cache(rows=-1, table=None), attend_args()) == EINVAL
+
+
 def test_workspace_sizes_refuse_bad_arguments(lib):
     c = cache()
     assert lib.nbw_kv_attend_workspace_bytes(ctypes.byref(c), 5, 0, 0) == -1
