@@ -666,7 +666,10 @@ __global__ __launch_bounds__(256) void kv_move_kernel(KvCache c, KvEvict a, Evic
 }
 
 // Threads of the workgroup that ranks one (row, head): the smallest that holds the longest
-// row's keys, 4, 8 or 16 a thread.  (Rows of 2049 slots as 256 threads with 16 keys: 17.6 us, and 14 so.)
+// row's keys, 4, 8 or 16 a thread.  The same for every batch: calls in a graph, one token over
+// the budget, 256 threads with 16 keys against 512 with 8: 64 (row, head) of 2049 slots 5.8 and
+// 5.0 us, 256 of them 6.2 and 5.5, 768 of them 9.0 and 8.7, 512 of 1025 slots 6.4 and 5.9, 768 of
+// those 7.0 and 7.2; 768 of 2049 brought down to half 59 both.
 static int ranking_threads(int max_len) { return max_len <= 1024 ? 256 : max_len <= 4096 ? 512 : 1024; }
 
 static int64_t evict_plan(const KvCache &c, int budget, int max_len, uint8_t *base, EvictPlan *pl) {  // -1: more than a launch takes
