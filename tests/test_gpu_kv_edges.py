@@ -304,3 +304,154 @@ def test_a_batch_without_rows(nbw):  # noqa: F811
     s = Setup(nbw, [5, 0], page=16, room=2)
     _, lens = nbw.kv_append(s.cache, heads(2), heads(2), s.lens, ints(0), cu=ints(3))
     assert lens.tolist() == [5, 0]
+
+
+# ---------------------------------------------------------------------------
+# tables wider than their rows: the launches, and whether loads stream, go by the capacity
+
+def widen(nbw, s, width):  # noqa: F811
+    """The cache of a Setup with a table of `width` pages a row, junk past each row's."""
+    table = s.rng.choice([-1, 10**9, 0, s.cache.pages - 1], size=(len(s.lens_l), width)).astype(np.int32)
+    table[:, :s.table_np.shape[1]] = s.table_np
+    return nbw.KVCache(s.k, s.v, torch.from_numpy(table).cuda(), *s.scales)
+
+
+@pytest.mark.parametrize("group", [4, 11])
+@pytest.mark.parametrize("page", [8, 16])
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_attend_in_a_wide_table(nbw, dim, dtype, page, group):  # noqa: F811
+    """Rows of a few hundred slots that may become so long that their keys and values are 256 MB and more."""
+    lens = [700, 0, 333, 64, 1]
+    s = Setup(nbw, lens, heads=2, page=page, dim=dim, dtype=dtype, seed=dim + group)
+    slots = (256 << 20) // (len(lens) * 2 * dim * (2 if dtype == FP8 else 4)) + page
+    cache = widen(nbw, s, -(-slots // page))
+    print(f"wide attend dim {dim} {dtype} page {page} group {group} capacity {cache.capacity}", flush=True)
+    assert len(lens) * 2 * cache.capacity * dim * (2 if dtype == FP8 else 4) > 256 << 20
+    q = s.normal(len(lens), 2 * group, dim, by=1.5)
+    check_attend(s, q, nbw.kv_attend(cache, q, s.lens), dim ** -0.5)
+    acc = torch.rand((len(lens), 2, cache.capacity), device="cuda")
+    acc_out = torch.full_like(acc, -3.0)
+    out = nbw.kv_attend(cache, q, s.lens, acc=acc, acc_out=acc_out, decay=0.75)
+    check_attend(s, q, out, dim ** -0.5, acc, acc_out, 0.75, before=torch.full_like(acc, -3.0))
+
+
+@pytest.mark.parametrize("lens,budget,width", [([2049, 2048, 0, 2050], 2048, 4096), ([1500, 900, 3000], 700, 2048), ([30, 64], 64, 3000)])
+def test_evict_in_a_wide_table(nbw, lens, budget, width):  # noqa: F811
+    """Short rows whose table is longer than one workgroup ranks."""
+    cache, n, table = rows_cache(nbw, lens, 3, 64, 16, 5, width=width)
+    assert cache.capacity > 16384
+    g = torch.Generator(device="cuda").manual_seed(6)
+    acc = torch.randn((len(lens), 3, cache.capacity), generator=g, device="cuda").exp()
+    pos = torch.rand((len(lens), 3, cache.capacity), generator=g, device="cuda").argsort(dim=2).int()
+    total = check_evict(nbw, cache, n, table, acc, pos, budget, 4, budget // 8)
+    assert (total > 0) == (max(lens) > budget)
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, FP8), (64, BF16), (128, BF16), (256, BF16)])
+def test_evict_with_streaming_moves(nbw, dim, dtype):  # noqa: F811
+    """Moves that may come to more than 64 MB, 64, 128, 256 and 512 bytes a row."""
+    row = dim * (1 if dtype == FP8 else 2)
+    budget = (64 << 20) // (4 * 2 * row) + 100
+    lens = [budget + 700, budget + 3]
+    cache, n, table = rows_cache(nbw, lens, 2, dim, 64, dim, width=-(-2 * budget // 64))
+    if dtype == FP8:
+        scale = torch.ones(2, device="cuda")
+        cache = nbw.KVCache(cache.k.to(FP8), cache.v.to(FP8), cache.table, scale, scale)
+    print(f"streaming moves of {row} bytes, budget {budget}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    acc = torch.rand((2, 2, cache.capacity), generator=g, device="cuda")
+    acc[:, :, budget:] += 0.5
+    pos = torch.arange(cache.capacity, dtype=torch.int32, device="cuda").repeat(2, 2, 1)
+    assert check_evict(nbw, cache, n, table, acc, pos, budget, 4, 300) > 600
+
+
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("lens,heads,budget,streams", [
+    ([3000, 0, 700, 129], 2, 300, False),    # divided attention with totals and its join; lists of moves in the workspace
+    ([20000, 17000, 0, 40], 2, 9000, True),  # rows that several workgroups rank
+    ([2600, 40] * 35, 4, 1000, False),       # more rows than a wave has lanes
+])
+def test_other_streams_and_replays_of_calls_with_a_workspace(nbw, lens, heads, budget, streams):  # noqa: F811
+    """A step of append, attend and evict on another stream, and captured in a graph and replayed with longer and shorter rows
+    than it was captured with, against the same step run eagerly on the same inputs."""
+    rows = len(lens)
+    s = Setup(nbw, lens, heads=heads, page=16, room=40, seed=8)
+    if streams:
+        s.cache = widen(nbw, s, s.table_np.shape[1] + 700)
+    cap = s.cache.capacity
+    q, k, v = s.normal(rows, heads * 4, 128), s.normal(rows, heads, 128), s.normal(rows, heads, 128)
+    positions = s.lens.clone()
+    sizes = s.cache.attend_workspace_bytes(heads * 4, weights=True), s.cache.evict_workspace_bytes(budget)
+    assert min(sizes) > 0
+    ws = torch.empty(max(sizes), dtype=torch.uint8, device="cuda")
+    acc0 = torch.rand((rows, heads, cap), device="cuda")
+    pos0 = torch.arange(cap, dtype=torch.int32, device="cuda").repeat(rows, heads, 1)
+    b = dict(lens=s.lens.clone(), acc=acc0.clone(), pos=pos0.clone(), out=torch.empty_like(q), lens1=torch.empty_like(s.lens),
+             lens2=torch.empty_like(s.lens), acc2=torch.zeros_like(acc0), pos2=torch.zeros_like(pos0))
+    k0, v0 = s.k.clone(), s.v.clone()
+
+    def step():
+        nbw.kv_append(s.cache, k, v, b["lens"], positions, pos=b["pos"], acc=b["acc"], lens_out=b["lens1"])
+        nbw.kv_attend(s.cache, q, b["lens1"], out=b["out"], acc=b["acc"], decay=0.5, workspace=ws)
+        nbw.kv_evict(s.cache, b["acc"], b["pos"], b["lens1"], budget, recent=10, acc_out=b["acc2"], pos_out=b["pos2"],
+                     lens_out=b["lens2"], workspace=ws)
+
+    def reset(extra):
+        b["lens"].copy_(torch.clamp(s.lens + extra, min=0))
+        b["acc"].copy_(acc0), b["pos"].copy_(pos0), s.k.copy_(k0), s.v.copy_(v0)
+        for n in ("out", "lens1", "lens2", "acc2", "pos2"):
+            b[n].zero_()
+        ws.fill_(0xA5)
+
+    def results():
+        torch.cuda.synchronize()
+        return [x.clone().view(torch.uint8) for x in (b["out"], b["acc"], b["pos"], b["lens1"], b["lens2"], b["acc2"], b["pos2"], s.k, s.v)]
+
+    # pages past a row's length hold NaN, which longer rows would read: give them numbers
+    k0.nan_to_num_(0.25), v0.nan_to_num_(0.5)
+    want = {}
+    for extra in (0, 17, -350, 35):
+        reset(extra)
+        step()
+        want[extra] = results()
+    reset(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(results(), want[0]))
+    g = torch.cuda.CUDAGraph()
+    reset(0)
+    with torch.cuda.graph(g):
+        step()
+    for extra in (0, 17, 35, -350, 0, 17):
+        reset(extra)
+        nbw.kv_attend(s.cache, q, s.lens, acc=acc0.clone())  # other eager work between the replays
+        torch.cuda.synchronize()
+        g.replay()
+        assert all(torch.equal(x, y) for x, y in zip(results(), want[extra])), extra
+
+
+def test_append_limits_keys_and_values_to_the_largest_8_bit_number(nbw):  # noqa: F811
+    s = Setup(nbw, [0, 0], heads=1, dim=64, dtype=FP8, room=4)
+    x = s.normal(2, 1, 64)
+    special = torch.tensor([1e4, -1e4, math.inf, -math.inf, math.nan, 0.0], dtype=BF16)
+    x[0, 0, :6] = special
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    nbw.kv_append(s.cache, x, x, s.lens, zero)
+    for pool, scale in ((s.k, s.scales[0]), (s.v, s.scales[1])):
+        got = pool[s.table_np[0, 0], 0, 0].float().cpu()
+        assert got[:4].tolist() == [448, -448, 448, -448] and bool(got[4].isnan()) and got[5].item() == 0
+        plain = (x[1, 0].float() / scale).clamp(-448, 448).to(FP8)
+        assert torch.equal(pool[s.table_np[1, 0], 0, 0].view(torch.uint8), plain.view(torch.uint8))
+    # a pair within the limit whose rotation by 45 degrees is past it: 5 and 5 at a factor of 0.0125 are 400 each, and 566 together
+    s.scales[0].fill_(0.0125)
+    y = torch.zeros((2, 1, 64), dtype=BF16, device="cuda")
+    y[:, 0, 7], y[:, 0, 32 + 7] = 5.0, 5.0
+    rope = torch.full((1, 64), math.sqrt(0.5), device="cuda")
+    nbw.kv_append(s.cache, y, y, zero, zero, rope=rope)
+    got = s.k[s.table_np[0, 0], 0, 0].float().cpu()
+    assert got[7].item() == 0 and got[32 + 7].item() == 448 and got.abs().sum().item() == 448
