@@ -76,6 +76,23 @@ def log(msg):
     print(msg, file=sys.stderr, flush=True)
 
 
+def without_tables(x, path="", tables=None):
+    """The result without its lists of entries by product, which stderr has in words and --tables writes, and those
+    lists by their place in it: the line on stdout stays below 8 KB, so that a reader that keeps only the end of the
+    output has all of it."""
+    tables = {} if tables is None else tables
+    kept = {}
+    for key, v in x.items():
+        at = f"{path}.{key}" if path else key
+        if isinstance(v, dict):
+            kept[key] = without_tables(v, at, tables)[0]
+        elif isinstance(v, list) and v and isinstance(v[0], dict):
+            tables[at] = v
+        else:
+            kept[key] = v
+    return kept, tables
+
+
 def parse():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -83,6 +100,7 @@ def parse():
     ap.add_argument("--warmup", type=int, default=20)
     ap.add_argument("--only", default="", help="comma list of sections (default: all): " + ",".join(SECTIONS))
     ap.add_argument("--no-cpu-baseline", action="store_true", help="leave out the cpu section")
+    ap.add_argument("--tables", metavar="FILE", help="write the lists of entries by product (JSON) there")
     ap.add_argument("--b1-kernel", default="auto", help="kernel for the batch-1 step (auto, gemv, smallb)")
     ap.add_argument("--pmc-probe", metavar="KIND",
                     help="run only a counter probe (a plain device copy of known size, then a fixed set of "
@@ -922,7 +940,11 @@ def main():
     if "cpu" in only:
         result["cpu_baseline"] = cpu_baseline(synth, one_core)
 
-    print(json.dumps(result), flush=True)
+    line, tables = without_tables(result)
+    if args.tables:
+        with open(args.tables, "w") as f:
+            json.dump(tables, f, indent=1)
+    print(json.dumps(line, separators=(",", ":")), flush=True)
 
 
 if __name__ == "__main__":

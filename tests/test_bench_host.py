@@ -36,6 +36,23 @@ def test_unknown_section_is_refused():
     assert res.returncode != 0 and "nonsense" in res.stderr
 
 
+def test_the_line_is_short_and_the_tables_are_not_lost():
+    import json
+
+    import bench
+    entry = {"linear": "gate_up", "r": 4, "us": 12.78, "kernel": "nbw::gemv_kernel<4, 1, false, 1, false>"}
+    contract = {"metric": bench.METRIC, "value": 3014.5, "unit": "GB/s", "n_gpus": 1, "steps": 20, "warmup": 5, "ms_per_step": 0.08,
+                "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+                "config": {"batch": 1, "r": [4, 3, 2]}}
+    full = dict(contract, per_shape=[entry] * 12, large_b1=[entry] * 6, sections=["b1"],
+                qwen3_8b={"r": [6, 4], "batches": {"batch1": {"ms_per_step": 0.1, "kernels": ["a", "b"]}}, "b1_products": [entry] * 99})
+    line, tables = bench.without_tables(full)
+    assert {k: line[k] for k in contract} == contract and line["sections"] == ["b1"]
+    assert line["qwen3_8b"] == {"r": [6, 4], "batches": full["qwen3_8b"]["batches"]}
+    assert tables == {"per_shape": [entry] * 12, "large_b1": [entry] * 6, "qwen3_8b.b1_products": [entry] * 99}
+    assert len(json.dumps(line)) < 8000
+
+
 def test_rotation_rule():
     import bench
     # >= 600 MB of other bytes between two uses: ceil(600 MB / bytes) + 1 copies
