@@ -135,14 +135,4 @@ __device__ __forceinline__ uint32_t to_fp8x4(float a, float b, float c, float d)
     return (uint32_t)w;
 }
 
-// Byte `i` (0..3) of a word of 8-bit values, as fp32 (exact).
-__device__ __forceinline__ float fp8_at(uint32_t w, int i) {
-    switch (i) {
-    case 0: return __builtin_amdgcn_cvt_f32_fp8(w, 0);
-    case 1: return __builtin_amdgcn_cvt_f32_fp8(w, 1);
-    case 2: return __builtin_amdgcn_cvt_f32_fp8(w, 2);
-    default: return __builtin_amdgcn_cvt_f32_fp8(w, 3);
-    }
-}
-
 }  // namespace nbw
