@@ -468,9 +468,9 @@ typedef struct nbw_kv_attend_args {
  *     acc_out_j = decay * acc_j + sum over g of p_j.
  * Products, softmax and sums are in fp32; out is rounded once.  A row of
  * length 0 gives zeros, as does a head whose scores are all -infinity, whatever
- * its values; else a NaN among a row's scores or values gives NaN.  What lies in
- * slots past the length has no part.  Deterministic: the same inputs give the
- * same bits.
+ * its values; else a NaN among a row's scores or values gives NaN, and so does an
+ * infinite value whose weight is 0.  What lies in slots past the length has no
+ * part.  Deterministic: the same inputs give the same bits.
  * Errors: NBW_EINVAL, NBW_EALIGN, NBW_EUNSUPPORTED, NBW_ESCRATCH (workspace
  * missing or too small), NBW_EHIP. */
 nbw_status nbw_kv_attend(const nbw_kvcache *cache, const nbw_kv_attend_args *args, void *stream);
@@ -490,7 +490,9 @@ typedef struct nbw_kv_evict_args {
     float *acc_out;         /* acc's shape, not acc */
     int32_t *pos_out;       /* pos's shape, not pos */
     int32_t *lens_out;      /* [rows], not lens */
-    int64_t max_len;        /* 0 (the capacity), or a bound of the lengths */
+    int64_t max_len;        /* 0 (the capacity), or a bound of the lengths, which sizes launches
+                               and workspace: worth passing where a table is much wider than its
+                               rows (above 16384 slots the ranking takes six launches) */
     void *workspace;        /* as for nbw_kv_attend; nbw_kv_evict_workspace_bytes bytes */
     int64_t workspace_bytes;
 } nbw_kv_evict_args;
@@ -508,7 +510,8 @@ typedef struct nbw_kv_evict_args {
  * row (the others are left as they are), lens_out min(len, budget); pages
  * past that length may be given to other rows when the call has completed.
  * Exact: no arithmetic but comparisons.  Slots on pages that are not there
- * take part in the ranking, and what would move to or from them is not moved.
+ * take part in the ranking; their totals and positions move like any other, a
+ * key and value that would move to or from them stay.
  * Errors: as nbw_kv_attend. */
 nbw_status nbw_kv_evict(const nbw_kvcache *cache, const nbw_kv_evict_args *args, void *stream);
 

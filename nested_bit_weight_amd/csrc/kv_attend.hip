@@ -36,9 +36,9 @@
 // parts, 16 bits, everything takes as long within 1%: 64 rows 201 us, 24 rows with 12
 // heads 49, one row of 333 slots 7.6 and 7.8 so.)
 //
-// Measured (128 dims, 8 heads): 64 rows of up to 8192 slots, 1.2 GB: 199 us, 6.0 TB/s
-// (a plain read of as much: 175 us), with totals 249; one row of 131071 slots, 537 MB,
-// 64 query heads: 87 us, 6.2 TB/s; 16 rows of up to 2048 slots: 15 us, half of it the
+// Measured (128 dims, 8 heads): 64 rows of up to 8192 slots, 1.2 GB: 200 us, 6.0 TB/s
+// (a plain read of as much: 175 us), with totals 248; one row of 131071 slots, 537 MB,
+// 64 query heads: 88 us, 6.1 TB/s; 16 rows of up to 2048 slots: 15 us, half of it the
 // chain of loads before the first key and the join; one row of 333 slots: 7 us.
 //
 // The running maximum m of a head is only raised, and o and the sum rescaled,

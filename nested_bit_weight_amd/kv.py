@@ -205,7 +205,7 @@ class KVCache:
 def _bytes(n: int) -> int:
     if n < 0:
         raise ValueError("bad arguments: query heads must be a multiple of the cache's heads, a budget within the "
-                         "capacity, a bound of the lengths not negative")
+                         "capacity, a bound of the lengths not negative, the work no more than one launch takes")
     return n
 
 
@@ -319,7 +319,7 @@ def kv_evict(cache: KVCache, acc, pos, lens, budget: int, *, sink: int = 0, rece
     """Rows longer than ``budget`` keep, for each head, the budget slots with the largest
     totals ``acc`` (fp32 [rows][heads][capacity]; the lowest slot first among equals); the
     ones whose position ``pos`` (int32, same shape) is below ``sink`` or among the ``recent``
-    last are kept in any case (sink + recent <= budget).  Slots that stay past the budget move
+    last are kept in any case, whatever their totals (sink + recent <= budget).  Slots that stay past the budget move
     into the ones below it that go, in the pools, in ``acc_out`` and in ``pos_out`` (buffers
     of their own, of the same shapes).  Returns min(lens, budget) in ``lens_out``.
     ``max_len`` and ``workspace`` as for :func:`kv_attend`."""
