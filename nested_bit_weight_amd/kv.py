@@ -135,7 +135,8 @@ class KVCache:
         if _lib().nbw_kv_evict_workspace_bytes(self._ref, 1, 1) < 0:
             raise ValueError(f"a cache of {pages} pages of {page} slots, {heads} heads of {dim} and a table of "
                              f"{rows} x {width} is outside what the library takes (dim 64, 128 or 256; pages of a "
-                             f"power of two up to 4096 slots, 16-byte aligned; a row of at most 2^30 slots)")
+                             f"power of two up to 4096 slots, 16-byte aligned; a row of at most 2^30 slots; "
+                             f"rows x heads below 2^24)")
 
     def _heads(self, t, name: str, shape):
         """Address of a bf16 tensor of shape [n][heads][dim] and its stride from one token
