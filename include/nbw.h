@@ -518,6 +518,151 @@ nbw_status nbw_kv_evict(const nbw_kvcache *cache, const nbw_kv_evict_args *args,
 /* Bytes of workspace nbw_kv_evict needs, or -1 on bad arguments.  Host only. */
 int64_t nbw_kv_evict_workspace_bytes(const nbw_kvcache *cache, int64_t budget, int64_t max_len);
 
+/* ---------------------------------------------------------------------------
+ * A step with drafted tokens: a narrow child of the nested weights drafts a few
+ * tokens for each sequence, a wider one takes them all in one step.  Pages and
+ * slots for them (nbw_kv_reserve), the attention of several new tokens of a
+ * row, over a past that rows may share (nbw_kv_attend_shared), and which of
+ * the drafts stand (nbw_verify_drafts). */
+
+/* Arguments of nbw_kv_reserve. */
+typedef struct nbw_kv_reserve_args {
+    int32_t *table;           /* the cache's table, which is written */
+    const int32_t *lens;      /* [rows] slots in use */
+    const int32_t *want;      /* [rows] new tokens asked for */
+    const int32_t *held;      /* [rows] pages that the row's table entries 0..held-1 name */
+    const int32_t *shared;    /* NULL, or [rows]: of these the first that are not the row's to
+                                 give back (a prefix that other rows have too) */
+    const int32_t *seen;      /* NULL (lens), or [rows]: position of the row's first new token */
+    int32_t *free;            /* [free_size] numbers of the free pages, a stack: the last is taken first */
+    int64_t free_size;        /* 1..2^31 - 1: pages that can be free at once */
+    const int32_t *count;     /* [1] free pages */
+    int64_t max_tokens;       /* 0..2^24 - 2^13: places for tokens */
+    int32_t *cu;              /* [rows + 1] */
+    int32_t *positions;       /* [max_tokens] */
+    int64_t *slots;           /* [max_tokens], 8-byte aligned */
+    int32_t *granted;         /* [rows] */
+    int32_t *held_out;        /* [rows], not held */
+    int32_t *count_out;       /* [1], not count */
+} nbw_kv_reserve_args;
+
+/* Pages for the rows' next tokens, and each token's place.  With n = lens[r]
+ * (within 0 and the capacity) and t = want[r] (0 if negative, or if n + t is
+ * more than the capacity) a row needs ceil((n + t) / page) pages:
+ *  - a row that holds more gives those past the need back, but for its first
+ *    `shared`; the i-th page given back (rows ascending, then entries) lies on
+ *    the stack above all later ones, so it is the i-th to be taken again;
+ *  - a row that holds fewer takes the missing ones, rows and entries ascending;
+ *  - rows are served in their order.  The first whose pages or tokens no longer
+ *    fit, and all after it, are granted no token and take no page.
+ * granted is t or 0, cu its running sum from 0 on, held_out and count_out the
+ * pages then held and free.  Token i of row r, number cu[r] + i, has
+ *     positions = seen[r] + i,
+ *     slots = table[r][j / page] * page + j % page,  j = n + i
+ * (-1 where that page is not in the pool); entries from cu[rows] on are 0 and
+ * -1.  Table entries are written only where a page is taken, free only above
+ * count and below count_out: the call can be repeated on the same inputs, and
+ * a reservation that is given back leaves stack and pages as they were.
+ * cu, positions and the cache are what nbw_kv_append takes.
+ * held is bounded by 0 and the width, count by 0 and free_size.  Exact: whole
+ * numbers only.  Other overlaps of inputs and outputs are not allowed.
+ * Errors: NBW_EINVAL, NBW_EALIGN, NBW_EUNSUPPORTED, NBW_EHIP. */
+nbw_status nbw_kv_reserve(const nbw_kvcache *cache, const nbw_kv_reserve_args *args, void *stream);
+
+/* Arguments of nbw_kv_attend_shared. */
+typedef struct nbw_kv_attend_shared_args {
+    const void *q;            /* bf16 [tokens][q_heads][dim], rotated */
+    void *out;                /* bf16 [tokens][q_heads][dim] */
+    int64_t q_ld, out_ld;     /* elements from one token to the next: 0 (dense), or at least
+                                 q_heads * dim and a multiple of 8 */
+    int64_t tokens;           /* 0..2^24 - 2^13 */
+    int32_t q_heads;          /* a multiple of the cache's heads */
+    float scale;              /* of the scores; 0: 1 / sqrt(dim) */
+    const int32_t *cu;        /* NULL: one token for each row (tokens = rows).  Else [rows + 1],
+                                 ascending from 0: row r has tokens cu[r]..cu[r+1]-1 */
+    const int32_t *lens;      /* [rows] slots in use, the new tokens' (the last of them) among them */
+    const int32_t *group_rows; /* NULL: nothing is shared.  Else [groups + 1], ascending from 0 to
+                                 rows: group g has the rows group_rows[g]..group_rows[g+1]-1 */
+    const int32_t *prefix;    /* with group_rows: [groups] leading slots that a group's rows share */
+    int64_t groups;           /* 0..2^20 */
+    int64_t max_len;          /* as for nbw_kv_attend */
+    void *workspace;          /* as for nbw_kv_attend; nbw_kv_attend_shared_workspace_bytes bytes */
+    int64_t workspace_bytes;
+} nbw_kv_attend_shared_args;
+
+/* Attention of each row's new tokens over its cached slots.  Token j of the n of
+ * a row of length L sees the slots below L - n + 1 + j, that is the row's past
+ * and the new tokens up to itself:
+ *     s_i = scale * q_g . k_i,  p = softmax over what the token sees,  out_g = sum_i p_i v_i
+ * with query heads as in nbw_kv_attend.  The first prefix[g] slots of group g's
+ * rows are read once for all of the group's tokens, through the table of the
+ * group's first row: the other rows must hold the same there.  (A row shorter
+ * than the prefix has as much of it as it is long.)
+ * Scores, softmax and sums are in fp32; the weights are rounded to bf16 for the
+ * product with the values, and so divided by the sum of what they were rounded
+ * to: an average of equal values is exact.  out is rounded once.  A token that
+ * sees no slot gives zeros, as does a head whose scores are all -infinity; else
+ * a NaN among the scores or values that a token sees gives NaN, and so does an
+ * infinite value whose weight is 0.  What a token does not see has no part in
+ * its result.  Tokens from cu[rows] on are left as they are.  Deterministic.
+ * Errors: as nbw_kv_attend. */
+nbw_status nbw_kv_attend_shared(const nbw_kvcache *cache, const nbw_kv_attend_shared_args *args, void *stream);
+
+/* Bytes of workspace nbw_kv_attend_shared needs, or -1 on bad arguments.  Host
+ * only; queries the device's compute-unit count. */
+int64_t nbw_kv_attend_shared_workspace_bytes(const nbw_kvcache *cache, int32_t q_heads, int64_t tokens,
+                                             int64_t groups, int64_t max_len);
+
+/* Element types of probabilities. */
+typedef enum nbw_probtype {
+    NBW_PROB_F32 = 0,
+    NBW_PROB_BF16 = 1
+} nbw_probtype;
+
+/* Arguments of nbw_verify_drafts. */
+typedef struct nbw_verify_args {
+    const void *target;       /* [tokens][vocab]: the target's probabilities after each token */
+    const void *draft;        /* NULL, or [tokens][vocab]: those that the next token was drafted from
+                                 (a row's last line is not read) */
+    int64_t target_ld, draft_ld; /* elements from one line to the next: 0 (= vocab) or >= vocab */
+    int64_t tokens;           /* 0..2^24 - 2^13 */
+    int64_t vocab;            /* 1..2^30 */
+    int64_t rows;             /* 0..2^20 */
+    int32_t dtype;            /* nbw_probtype, of both */
+    const int32_t *cu;        /* NULL: one token for each row (tokens = rows).  Else [rows + 1], ascending
+                                 from 0 to tokens: row r has tokens cu[r]..cu[r+1]-1, the last one that
+                                 is certain, then the drafts */
+    const int32_t *ids;       /* [tokens] the tokens; only the drafts are read (NULL without cu) */
+    const float *u;           /* [tokens] random numbers within [0, 1): for each draft the one in the
+                                 place before its own, and in the row's last place that for the next token */
+    int32_t *accepted;        /* [rows] */
+    int32_t *next;            /* [rows] */
+    void *workspace;          /* as for nbw_kv_attend; nbw_verify_drafts_workspace_bytes bytes */
+    int64_t workspace_bytes;
+} nbw_verify_args;
+
+/* Which drafts stand, and the token after them.  With p and q the lines of
+ * target and draft in the place before a draft x's own, and u the number there,
+ * x stands if all before it do and
+ *     u * q[x] < p[x]           (q[x] = 1 without draft);
+ * accepted is how many do.  The next token follows from weights w over the
+ * vocabulary: p of the row's last line if all drafts stand; else, with p and q of
+ * the line that refused, max(p - q, 0) (without draft: p, but 0 for x), or p again
+ * if none of those is above 0.  It is the first i with
+ *     w_0 + .. + w_i > u * (w_0 + .. + w_(vocab-1)),  u from the row's last place,
+ * so that the tokens are distributed as the target's own.  (Fast inference from
+ * transformers via speculative decoding, Leviathan et al., algorithm 1.)
+ * Comparisons are exact; differences and sums are in fp64.  A weight that is not
+ * a positive finite number counts as 0; with none above 0, or for a row without
+ * tokens, next is -1.  u is bounded by 0 and 1 (NaN: 0) for the next token.  A draft
+ * outside the vocabulary is refused.  Deterministic.
+ * Alignment: 4 bytes, bf16 lines 2 bytes, workspace 256.
+ * Errors: NBW_EINVAL, NBW_EALIGN, NBW_EUNSUPPORTED (dtype), NBW_ESCRATCH, NBW_EHIP. */
+nbw_status nbw_verify_drafts(const nbw_verify_args *args, void *stream);
+
+/* Bytes of workspace nbw_verify_drafts needs, or -1 on bad arguments.  Host only. */
+int64_t nbw_verify_drafts_workspace_bytes(int64_t rows, int64_t vocab);
+
 /* Name of the kernel template instance nbw_qgemm_kernel would launch for
  * this problem on the current device (for example "nbw::gemv_kernel<4, 1, 2>",
  * as profilers print it without the parameter list), or "" on bad input.  The

@@ -77,7 +77,8 @@ EXPORTS = ("nbw_plane_bytes", "nbw_packed_bytes", "nbw_pack_bitplanes", "nbw_mak
            "nbw_mfma_rate_sink_floats", "nbw_mfma_rate",
            "nbw_file_prefix_bytes", "nbw_file_header", "nbw_file_parse",
            "nbw_kv_append", "nbw_kv_attend", "nbw_kv_attend_workspace_bytes", "nbw_kv_evict",
-           "nbw_kv_evict_workspace_bytes",
+           "nbw_kv_evict_workspace_bytes", "nbw_kv_reserve", "nbw_kv_attend_shared",
+           "nbw_kv_attend_shared_workspace_bytes", "nbw_verify_drafts", "nbw_verify_drafts_workspace_bytes",
            "nbw_kernel_name", "nbw_status_str", "nbw_last_hip_error", "nbw_version")
 
 
@@ -139,6 +140,7 @@ def _lib():
         lib.nbw_file_parse.argtypes = [vp, i64, ctypes.POINTER(FileInfo)]
         lib.nbw_file_parse.restype = ctypes.c_int
         kv.declare(lib)
+        drafts.declare(lib)
         _LIB = lib
     return _LIB
 
@@ -583,9 +585,11 @@ def version() -> str:
 
 
 from . import kv  # noqa: E402  (uses the helpers above)
-from .kv import KVCache, kv_append, kv_attend, kv_evict  # noqa: E402
+from .kv import KVCache, Reserved, kv_append, kv_attend, kv_attend_shared, kv_evict, kv_reserve  # noqa: E402
+from . import drafts  # noqa: E402
+from .drafts import verify_drafts  # noqa: E402
 
-__all__ = ["KVCache", "kv_append", "kv_attend", "kv_evict", "pack_bitplanes", "slice_view", "save_parent", "load_child", "file_info",
+__all__ = ["KVCache", "Reserved", "kv_append", "kv_attend", "kv_attend_shared", "kv_evict", "kv_reserve", "verify_drafts", "pack_bitplanes", "slice_view", "save_parent", "load_child", "file_info",
            "file_prefix_bytes", "qgemm", "QgemmCall", "qgemm_grouped", "workspace_bytes", "choose_codes", "unpack_codes", "stream_read", "stream_sink", "mfma_rate", "mfma_rate_sink", "mfma_rate_flops", "plane_bytes",
            "packed_bytes", "PackedWeight", "NBWError", "KERNELS", "library", "kernel_name",
            "version"]

@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnbw.so")
 SOURCES = ["abi.hip", "pack.hip", "gemv.hip", "smallb.hip", "gemm.hip", "gemm_wide.hip", "choose.hip",
-           "stream.hip", "file.hip", "kv_append.hip", "kv_attend.hip", "kv_evict.hip"]
+           "stream.hip", "file.hip", "kv_append.hip", "kv_attend.hip", "kv_evict.hip",
+           "kv_reserve.hip", "kv_shared.hip", "verify.hip"]
 ARCH = "gfx950"
 
 

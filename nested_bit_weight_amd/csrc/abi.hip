@@ -160,6 +160,13 @@ nbw_status check_q_heads(int32_t q_heads, const nbw::KvCache &c) {
     return (int64_t)q_heads * (c.rows ? c.rows : 1) <= (1 << 30) ? NBW_OK : NBW_EINVAL;
 }
 
+// Tokens of a call, and the query heads' work with them, as one launch takes it.
+bool tokens_ok(int64_t tokens, int32_t q_heads) {
+    return tokens >= 0 && tokens <= nbw::APPEND_TOKENS && tokens * q_heads <= (1 << 30);
+}
+
+bool groups_ok(int64_t groups) { return groups >= 0 && groups <= (1 << 20); }
+
 }  // namespace
 
 extern "C" {
@@ -560,6 +567,139 @@ nbw_status nbw_kv_evict(const nbw_kvcache *cache, const nbw_kv_evict_args *args,
     a.lens_out = g.lens_out;
     a.ws = (uint8_t *)g.workspace;
     const hipError_t e = nbw::launch_kv_evict(c, a, (hipStream_t)stream);
+    return e == hipSuccess ? NBW_OK : hip_failed(e);
+}
+
+nbw_status nbw_kv_reserve(const nbw_kvcache *cache, const nbw_kv_reserve_args *args, void *stream) {
+    nbw::KvCache c;
+    nbw_status st = check_cache(cache, &c);
+    if (st != NBW_OK) return st;
+    if (!args) return NBW_EINVAL;
+    const nbw_kv_reserve_args &g = *args;
+    if (g.max_tokens < 0 || g.max_tokens > nbw::APPEND_TOKENS) return NBW_EINVAL;
+    if (g.free_size < 1 || g.free_size > (1 << 30)) return NBW_EINVAL;
+    if (g.table != c.table) return NBW_EINVAL;
+    if (c.rows && (!g.lens || !g.want || !g.held || !g.granted || !g.held_out)) return NBW_EINVAL;
+    if (!g.free || !g.count || !g.cu || !g.count_out || (g.max_tokens && (!g.positions || !g.slots))) return NBW_EINVAL;
+    if ((c.rows && g.held == g.held_out) || g.count == g.count_out) return NBW_EINVAL;
+    if (!aligned(g.lens, 4) || !aligned(g.want, 4) || !aligned(g.held, 4) || !aligned(g.shared, 4) || !aligned(g.seen, 4) ||
+        !aligned(g.free, 4) || !aligned(g.count, 4) || !aligned(g.cu, 4) || !aligned(g.positions, 4) || !aligned(g.slots, 8) ||
+        !aligned(g.granted, 4) || !aligned(g.held_out, 4) || !aligned(g.count_out, 4))
+        return NBW_EALIGN;
+    int cus = 0;
+    if ((st = cu_count(&cus)) != NBW_OK) return st;
+    nbw::KvReserve a = {};
+    a.table = g.table;
+    a.lens = g.lens;
+    a.want = g.want;
+    a.held = g.held;
+    a.shared = g.shared;
+    a.seen = g.seen;
+    a.free = g.free;
+    a.free_size = (int)g.free_size;
+    a.count = g.count;
+    a.max_tokens = (int)g.max_tokens;
+    a.cu = g.cu;
+    a.positions = g.positions;
+    a.slots = g.slots;
+    a.granted = g.granted;
+    a.held_out = g.held_out;
+    a.count_out = g.count_out;
+    const hipError_t e = nbw::launch_kv_reserve(c, a, cus, (hipStream_t)stream);
+    return e == hipSuccess ? NBW_OK : hip_failed(e);
+}
+
+int64_t nbw_kv_attend_shared_workspace_bytes(const nbw_kvcache *cache, int32_t q_heads, int64_t tokens,
+                                             int64_t groups, int64_t max_len) {
+    nbw::KvCache c;
+    int most = 0, cus = 0;
+    if (check_cache(cache, &c) != NBW_OK || check_q_heads(q_heads, c) != NBW_OK ||
+        check_max_len(max_len, c, &most) != NBW_OK || !tokens_ok(tokens, q_heads) || !groups_ok(groups))
+        return -1;
+    if (c.rows == 0 || tokens == 0) return 0;
+    if (cu_count(&cus) != NBW_OK) return -1;
+    return nbw::kv_attend_shared_workspace_bytes(c, q_heads, (int)tokens, (int)groups, most, cus);
+}
+
+nbw_status nbw_kv_attend_shared(const nbw_kvcache *cache, const nbw_kv_attend_shared_args *args, void *stream) {
+    nbw::KvCache c;
+    nbw_status st = check_cache(cache, &c);
+    if (st != NBW_OK) return st;
+    if (!args) return NBW_EINVAL;
+    const nbw_kv_attend_shared_args &g = *args;
+    nbw::KvAttendShared a = {};
+    if ((st = check_q_heads(g.q_heads, c)) != NBW_OK) return st;
+    if ((st = check_max_len(g.max_len, c, &a.max_len)) != NBW_OK) return st;
+    const int64_t cols = (int64_t)g.q_heads * c.dim;
+    if ((st = check_ld(g.q_ld, cols, &a.q_ld)) != NBW_OK) return st;
+    if ((st = check_ld(g.out_ld, cols, &a.out_ld)) != NBW_OK) return st;
+    if (!(g.scale >= -3.4e38f && g.scale <= 3.4e38f)) return NBW_EINVAL;  // NaN too
+    if (!tokens_ok(g.tokens, g.q_heads) || (!g.cu && g.tokens != c.rows)) return NBW_EINVAL;
+    if (!groups_ok(g.groups) || (g.groups && (!g.group_rows || !g.prefix))) return NBW_EINVAL;
+    if (g.workspace_bytes < 0) return NBW_EINVAL;
+    if (c.rows == 0 || g.tokens == 0) return NBW_OK;
+    if (!g.q || !g.out || !g.lens) return NBW_EINVAL;
+    if (!aligned(g.q, 16) || !aligned(g.out, 16) || !aligned(g.lens, 4) || !aligned(g.cu, 4) ||
+        !aligned(g.group_rows, 4) || !aligned(g.prefix, 4) || !aligned(g.workspace, 256))
+        return NBW_EALIGN;
+    int cus = 0;
+    if ((st = cu_count(&cus)) != NBW_OK) return st;
+    const int64_t need = nbw::kv_attend_shared_workspace_bytes(c, g.q_heads, (int)g.tokens, (int)g.groups, a.max_len, cus);
+    if (need < 0) return NBW_EINVAL;  // more than a launch takes
+    if (need > 0 && (!g.workspace || g.workspace_bytes < need)) return NBW_ESCRATCH;
+    a.q = (const uint16_t *)g.q;
+    a.out = (uint16_t *)g.out;
+    a.tokens = (int)g.tokens;
+    a.q_heads = g.q_heads;
+    a.scale = g.scale != 0.f ? g.scale : c.dim == 64 ? 0.125f : c.dim == 256 ? 0.0625f : 0.08838834764831845f;
+    a.cu = g.cu;
+    a.lens = g.lens;
+    a.group_rows = g.groups ? g.group_rows : nullptr;
+    a.prefix = g.prefix;
+    a.groups = (int)g.groups;
+    a.ws = (uint8_t *)g.workspace;
+    const hipError_t e = nbw::launch_kv_attend_shared(c, a, cus, (hipStream_t)stream);
+    return e == hipSuccess ? NBW_OK : hip_failed(e);
+}
+
+int64_t nbw_verify_drafts_workspace_bytes(int64_t rows, int64_t vocab) {
+    if (rows < 0 || rows > (1 << 20) || vocab < 1 || vocab > (1 << 30)) return -1;
+    return nbw::verify_drafts_workspace_bytes((int)rows, (int)vocab);
+}
+
+nbw_status nbw_verify_drafts(const nbw_verify_args *args, void *stream) {
+    if (!args) return NBW_EINVAL;
+    const nbw_verify_args &g = *args;
+    if (g.dtype != NBW_PROB_F32 && g.dtype != NBW_PROB_BF16) return NBW_EUNSUPPORTED;
+    const int64_t need = nbw_verify_drafts_workspace_bytes(g.rows, g.vocab);
+    if (need < 0 || g.workspace_bytes < 0) return NBW_EINVAL;
+    if (g.tokens < 0 || g.tokens > nbw::APPEND_TOKENS || (!g.cu && g.tokens != g.rows)) return NBW_EINVAL;
+    if ((g.target_ld && g.target_ld < g.vocab) || (g.draft_ld && g.draft_ld < g.vocab)) return NBW_EINVAL;
+    if (g.target_ld > ((int64_t)1 << 32) || g.draft_ld > ((int64_t)1 << 32)) return NBW_EINVAL;  // offsets stay below 2^63
+    if (g.rows == 0) return g.tokens == 0 ? NBW_OK : NBW_EINVAL;
+    if (!g.accepted || !g.next || g.accepted == g.next) return NBW_EINVAL;
+    if (g.tokens && (!g.target || !g.u || (g.cu && !g.ids))) return NBW_EINVAL;
+    const uintptr_t size = g.dtype == NBW_PROB_F32 ? 4 : 2;
+    if (!aligned(g.target, size) || !aligned(g.draft, size) || !aligned(g.cu, 4) || !aligned(g.ids, 4) || !aligned(g.u, 4) ||
+        !aligned(g.accepted, 4) || !aligned(g.next, 4) || !aligned(g.workspace, 256))
+        return NBW_EALIGN;
+    if (!g.workspace || g.workspace_bytes < need) return NBW_ESCRATCH;
+    nbw::VerifyDrafts a = {};
+    a.target = g.target;
+    a.draft = g.draft;
+    a.target_ld = g.target_ld ? g.target_ld : g.vocab;
+    a.draft_ld = g.draft_ld ? g.draft_ld : g.vocab;
+    a.tokens = (int)g.tokens;
+    a.vocab = (int)g.vocab;
+    a.rows = (int)g.rows;
+    a.bf16 = g.dtype == NBW_PROB_BF16;
+    a.cu = g.cu;
+    a.ids = g.ids;
+    a.u = g.u;
+    a.accepted = g.accepted;
+    a.next = g.next;
+    a.ws = (uint8_t *)g.workspace;
+    const hipError_t e = nbw::launch_verify_drafts(a, (hipStream_t)stream);
     return e == hipSuccess ? NBW_OK : hip_failed(e);
 }
 

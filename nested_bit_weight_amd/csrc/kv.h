@@ -60,6 +60,40 @@ struct KvEvict {
     uint8_t *ws;
 };
 
+struct KvReserve {
+    int32_t *table;
+    const int32_t *lens, *want, *held, *shared, *seen;
+    int32_t *free;
+    int free_size;
+    const int32_t *count;
+    int max_tokens;
+    int32_t *cu, *positions;
+    int64_t *slots;
+    int32_t *granted, *held_out, *count_out;
+};
+
+struct KvAttendShared {
+    const uint16_t *q;
+    uint16_t *out;
+    int64_t q_ld, out_ld;
+    int tokens, q_heads;
+    float scale;
+    const int32_t *cu, *lens, *group_rows, *prefix;
+    int groups;
+    int max_len;
+    uint8_t *ws;
+};
+
+struct VerifyDrafts {
+    const void *target, *draft;
+    int64_t target_ld, draft_ld;
+    int tokens, vocab, rows, bf16;
+    const int32_t *cu, *ids;
+    const float *u;
+    int32_t *accepted, *next;
+    uint8_t *ws;
+};
+
 // Work-items that a launch takes in a dimension.
 constexpr int64_t MOST_ITEMS = ((int64_t)1 << 32) - 1;
 constexpr bool fits_launch(int64_t groups, int threads) { return groups <= MOST_ITEMS / threads; }
@@ -70,6 +104,12 @@ int64_t kv_attend_workspace_bytes(const KvCache &c, int q_heads, int max_len, bo
 hipError_t launch_kv_attend(const KvCache &c, const KvAttend &a, int cu_count, hipStream_t stream);
 int64_t kv_evict_workspace_bytes(const KvCache &c, int budget, int max_len);
 hipError_t launch_kv_evict(const KvCache &c, const KvEvict &a, hipStream_t stream);
+
+hipError_t launch_kv_reserve(const KvCache &c, const KvReserve &a, int cu_count, hipStream_t stream);
+int64_t kv_attend_shared_workspace_bytes(const KvCache &c, int q_heads, int tokens, int groups, int max_len, int cu_count);
+hipError_t launch_kv_attend_shared(const KvCache &c, const KvAttendShared &a, int cu_count, hipStream_t stream);
+int64_t verify_drafts_workspace_bytes(int rows, int vocab);
+hipError_t launch_verify_drafts(const VerifyDrafts &a, hipStream_t stream);
 
 typedef uint32_t u32x2_kv __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_kv __attribute__((ext_vector_type(4)));

@@ -1,4 +1,4 @@
-"""The key-value cache of a decode step: append, attend, evict.
+"""The key-value cache of a decode step: reserve, append, attend, evict.
 
 What runs between a layer's qkv product and its o product, over one paged cache
 (pools [pages][heads][page][dim] of bf16, or of 8 bits with a factor for each head, and
@@ -9,12 +9,19 @@ a table of page numbers for each sequence; see ``include/nbw.h`` for every detai
     out = kv_attend(cache, q_out, lens1, acc=acc)       # acc: running totals of the weights
     lens2 = kv_evict(cache, acc, pos, lens1, budget, recent=64, acc_out=acc2, pos_out=pos2)
 
+Several new tokens of a row, as drafts are, and pasts that rows share:
+
+    got = kv_reserve(cache, lens, want, held, free, count, max_tokens)     # pages for them
+    q_out, lens1 = kv_append(cache, k, v, lens, got.positions, q=q, cu=got.cu, rope=rope)
+    out = kv_attend_shared(cache, q_out, lens1, cu=got.cu, groups=groups, prefix=prefix)
+
 As everywhere in this package the calls only marshal arguments, queue the work on the
 current stream of the tensors' GPU, whichever GPU is the current one, and raise if the library is not built.
 """
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple
 
 import torch
 
@@ -48,6 +55,18 @@ class EvictArgs(ctypes.Structure):
                 ("workspace_bytes", _i64)]
 
 
+class ReserveArgs(ctypes.Structure):
+    _fields_ = [("table", _vp), ("lens", _vp), ("want", _vp), ("held", _vp), ("shared", _vp), ("seen", _vp),
+                ("free", _vp), ("free_size", _i64), ("count", _vp), ("max_tokens", _i64), ("cu", _vp),
+                ("positions", _vp), ("slots", _vp), ("granted", _vp), ("held_out", _vp), ("count_out", _vp)]
+
+
+class AttendSharedArgs(ctypes.Structure):
+    _fields_ = [("q", _vp), ("out", _vp), ("q_ld", _i64), ("out_ld", _i64), ("tokens", _i64), ("q_heads", _i32),
+                ("scale", _f32), ("cu", _vp), ("lens", _vp), ("group_rows", _vp), ("prefix", _vp), ("groups", _i64),
+                ("max_len", _i64), ("workspace", _vp), ("workspace_bytes", _i64)]
+
+
 SIZES_KEPT = 64
 KV_DTYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
 
@@ -55,18 +74,21 @@ KV_DTYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
 def declare(lib) -> None:
     """The C signatures of the cache's entry points."""
     pc = ctypes.POINTER(KVView)
-    for name, args in (("nbw_kv_append", AppendArgs), ("nbw_kv_attend", AttendArgs), ("nbw_kv_evict", EvictArgs)):
+    for name, args in (("nbw_kv_append", AppendArgs), ("nbw_kv_attend", AttendArgs), ("nbw_kv_evict", EvictArgs),
+                       ("nbw_kv_reserve", ReserveArgs), ("nbw_kv_attend_shared", AttendSharedArgs)):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = [pc, ctypes.POINTER(args), _vp], ctypes.c_int
     lib.nbw_kv_attend_workspace_bytes.argtypes = [pc, _i32, _i64, _i32]
     lib.nbw_kv_attend_workspace_bytes.restype = _i64
     lib.nbw_kv_evict_workspace_bytes.argtypes = [pc, _i64, _i64]
     lib.nbw_kv_evict_workspace_bytes.restype = _i64
+    lib.nbw_kv_attend_shared_workspace_bytes.argtypes = [pc, _i32, _i64, _i64, _i64]
+    lib.nbw_kv_attend_shared_workspace_bytes.restype = _i64
 
 
 # The GPU that kernels go to (the bare getter: the tensors are there, so the runtime is up).
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_BF16, _F32, _INT32 = torch.bfloat16, torch.float32, torch.int32
+_BF16, _F32, _INT32, _INT64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 
 
 def _is(t, name: str, dtype, shape, index: int) -> int:
@@ -179,6 +201,11 @@ class KVCache:
     def evict_workspace_bytes(self, budget: int, max_len: int = 0) -> int:
         """Bytes of scratch kv_evict needs."""
         return _bytes(_lib().nbw_kv_evict_workspace_bytes(self._ref, budget, max_len))
+
+    def attend_shared_workspace_bytes(self, q_heads: int, tokens: int, groups: int = 0, max_len: int = 0) -> int:
+        """Bytes of scratch kv_attend_shared needs."""
+        with torch.cuda.device(self._dev):  # they depend on its number of compute units
+            return _bytes(_lib().nbw_kv_attend_shared_workspace_bytes(self._ref, q_heads, tokens, groups, max_len))
 
     def _scratch(self, workspace, query, sizes, stream: int):
         """Address and size of a call's workspace; "auto": the binding's buffer, of the
@@ -349,3 +376,109 @@ def kv_evict(cache: KVCache, acc, pos, lens, budget: int, *, sink: int = 0, rece
     if st:
         _check(st, "nbw_kv_evict")
     return lens_out
+
+
+class Reserved(NamedTuple):
+    """What :func:`kv_reserve` gives: ``cu`` [rows + 1], ``positions`` and ``slots`` [max_tokens],
+    ``granted`` and ``held`` [rows], ``count`` [1]."""
+    cu: torch.Tensor
+    positions: torch.Tensor
+    slots: torch.Tensor
+    granted: torch.Tensor
+    held: torch.Tensor
+    count: torch.Tensor
+
+
+def kv_reserve(cache: KVCache, lens, want, held, free, count, max_tokens: int, *, shared=None, seen=None, cu=None,
+               positions=None, slots=None, granted=None, held_out=None, count_out=None) -> Reserved:
+    """Pages for the rows' next tokens, ``want`` of them each (int32 [rows], as ``lens``, the
+    slots in use, and ``held``, the pages that the row's table entries name), and each token's
+    place.  ``free`` (int32, any length) is the stack of free pages, the first ``count`` (int32 [1])
+    of it; the cache's table and ``free`` are written.
+
+    A row that holds more pages than it needs gives them back, but for its first ``shared``
+    (int32 [rows]); one that holds fewer takes them.  Rows are served in order while pages, and
+    ``max_tokens`` places for tokens, last; the others are granted 0.  A token's position counts
+    from ``seen`` (int32 [rows], ``lens`` if None); its slot is page * page size + place, or -1.
+    ``positions`` (int32) and ``slots`` (int64) have 0 and -1 from token cu[rows] on.  The call
+    can be repeated on the same inputs; ``held_out`` and ``count_out`` are tensors of their own."""
+    index = cache._dev
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return kv_reserve(cache, lens, want, held, free, count, max_tokens, shared=shared, seen=seen, cu=cu,
+                              positions=positions, slots=slots, granted=granted, held_out=held_out, count_out=count_out)
+    if max_tokens < 0:
+        raise ValueError("max_tokens must not be negative")
+    rows, one, places, device = cache._row, (1,), (max_tokens,), cache.device
+    if not isinstance(free, torch.Tensor) or free.dim() != 1 or not free.numel():
+        raise ValueError("free must be an int32 tensor of one dimension, of at least one element")
+    got = Reserved(torch.empty(cache.rows + 1, dtype=_INT32, device=device) if cu is None else cu,
+                   torch.empty(places, dtype=_INT32, device=device) if positions is None else positions,
+                   torch.empty(places, dtype=_INT64, device=device) if slots is None else slots,
+                   torch.empty(rows, dtype=_INT32, device=device) if granted is None else granted,
+                   torch.empty(rows, dtype=_INT32, device=device) if held_out is None else held_out,
+                   torch.empty(one, dtype=_INT32, device=device) if count_out is None else count_out)
+    args = ReserveArgs(
+        cache.view.table, _is(lens, "lens", _INT32, rows, index), _is(want, "want", _INT32, rows, index),
+        _is(held, "held", _INT32, rows, index), None if shared is None else _is(shared, "shared", _INT32, rows, index),
+        None if seen is None else _is(seen, "seen", _INT32, rows, index), _is(free, "free", _INT32, free.shape, index),
+        free.size(0), _is(count, "count", _INT32, one, index), max_tokens, _is(got.cu, "cu", _INT32, (cache.rows + 1,), index),
+        _is(got.positions, "positions", _INT32, places, index), _is(got.slots, "slots", _INT64, places, index),
+        _is(got.granted, "granted", _INT32, rows, index), _is(got.held, "held_out", _INT32, rows, index),
+        _is(got.count, "count_out", _INT32, one, index))
+    st = _lib().nbw_kv_reserve(cache._ref, ctypes.byref(args), _raw_stream(index))
+    if st:
+        _check(st, "nbw_kv_reserve")
+    return got
+
+
+def kv_attend_shared(cache: KVCache, q, lens, *, cu=None, groups=None, prefix=None, scale: float | None = None, out=None,
+                     max_len: int | None = None, workspace="auto") -> torch.Tensor:
+    """Attention of each row's new tokens, ``q`` bf16 [tokens][q_heads][dim], over the row's first
+    ``lens`` slots (int32 [rows], the new tokens' the last among them): bf16
+    [tokens][q_heads][dim].  One token for each row, or with ``cu`` (int32 [rows + 1]) tokens
+    cu[r]..cu[r+1]-1 for row r, of which each sees the ones up to itself.
+
+    ``groups`` (int32 [n + 1], ascending from 0 to rows) and ``prefix`` (int32 [n]): the first
+    prefix[g] slots are the same for rows groups[g]..groups[g+1]-1, and are read once for all of
+    them, through the table of the first.  ``scale``, ``max_len`` and ``workspace`` as for
+    :func:`kv_attend` (``cache.attend_shared_workspace_bytes(...)``)."""
+    index = cache._dev
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return kv_attend_shared(cache, q, lens, cu=cu, groups=groups, prefix=prefix, scale=scale, out=out, max_len=max_len,
+                                    workspace=workspace)
+    tokens = q.size(0) if isinstance(q, torch.Tensor) and q.dim() else 0
+    if cu is None and tokens != cache.rows:
+        raise ValueError(f"without cu there is one token for each of the {cache.rows} rows, got {tokens}")
+    shape = cache._queries(q, tokens)
+    q_heads = shape[1]
+    qp, q_ld = cache._heads(q, "q", shape)
+    if scale is None:
+        scale = 0.0
+    else:
+        scale = _f32(scale).value  # a number too small for fp32 would be 0, which stands for the default
+        if not 0.0 < abs(scale) < 3e38:
+            raise ValueError("scale must be finite and not 0 in fp32")
+    if max_len is None:
+        max_len = 0
+    elif max_len < 1:
+        raise ValueError("max_len must be at least 1")
+    if (groups is None) != (prefix is None):
+        raise ValueError("groups and prefix go together")
+    n, gp, pp = 0, None, None
+    if groups is not None:
+        n = prefix.size(0) if isinstance(prefix, torch.Tensor) and prefix.dim() == 1 else 0
+        gp, pp = _is(groups, "groups", _INT32, (n + 1,), index), _is(prefix, "prefix", _INT32, (n,), index)
+    if out is None:
+        out = torch.empty(shape, dtype=_BF16, device=q.device)
+    op, out_ld = cache._heads(out, "out", shape)
+    lib, stream = _lib(), _raw_stream(index)
+    ws, ws_bytes = cache._scratch(workspace, lib.nbw_kv_attend_shared_workspace_bytes, (q_heads, tokens, n, max_len), stream)
+    args = AttendSharedArgs(qp, op, q_ld, out_ld, tokens, q_heads, scale,
+                            None if cu is None else _is(cu, "cu", _INT32, (cache.rows + 1,), index),
+                            _is(lens, "lens", _INT32, cache._row, index), gp, pp, n, max_len, ws, ws_bytes)
+    st = lib.nbw_kv_attend_shared(cache._ref, ctypes.byref(args), stream)
+    if st:
+        _check(st, "nbw_kv_attend_shared")
+    return out

@@ -120,3 +120,53 @@ def evict(k_pool, v_pool, table, lens, acc, pos, budget, sink, recent, acc_out, 
             m = min(n, budget)
             acc_out[r, h, :m], pos_out[r, h, :m] = a[:m], p[:m]
     return k_pool, v_pool, acc_out, pos_out, np.minimum(lens, budget)
+
+
+def reserve(table, page, pages, lens, want, held, free, count, max_tokens, shared=None, seen=None):
+    """One row after the other: (table, free, cu, positions, slots, granted, held, count), inputs left alone."""
+    table, free = np.array(table), np.array(free)
+    rows, width = table.shape
+    cap = width * page
+    stack = list(free[:min(max(int(count), 0), len(free))])
+    bottom = len(stack)
+    lens = [min(max(int(n), 0), cap) for n in lens]
+    held = [min(max(int(h), 0), width) for h in held]
+    ask, need, given = [], [], []
+    for r in range(rows):
+        t = max(int(want[r]), 0)
+        ask.append(t if lens[r] + t <= cap else 0)
+        need.append(-(-(lens[r] + ask[r]) // page))
+        if shared is not None:
+            need[r] = max(need[r], min(int(shared[r]), held[r]))
+        given += list(table[r, need[r]:held[r]])
+        held[r] = min(held[r], max(need[r], 0)) if held[r] > need[r] else held[r]
+    stack += given[::-1]  # the first one given back on top
+    granted, open_ = [0] * rows, True
+    for r in range(rows):
+        open_ = open_ and need[r] - held[r] <= len(stack) and sum(granted) + ask[r] <= max_tokens
+        if open_:
+            granted[r] = ask[r]
+            while held[r] < need[r]:
+                table[r, held[r]] = stack.pop()
+                held[r] += 1
+    end = min(len(stack), len(free))
+    free[bottom:end] = stack[bottom:end]
+    cu = np.concatenate([[0], np.cumsum(granted)]).astype(np.int64)
+    positions, slots = np.zeros(max_tokens, dtype=np.int64), np.full(max_tokens, -1, dtype=np.int64)
+    for r in range(rows):
+        for i in range(granted[r]):
+            j = lens[r] + i
+            at = int(table[r, j // page])
+            positions[cu[r] + i] = (lens[r] if seen is None else int(seen[r])) + i
+            slots[cu[r] + i] = at * page + j % page if 0 <= at < pages else -1
+    return table, free, cu, positions, slots, granted, held, end
+
+
+def attend_tokens(q, k, v, table, lens, cu, scale):
+    """q [tokens][q_heads][dim], token j of the n of a row of length L over its first L - n + 1 + j slots."""
+    out = np.zeros(q.shape)
+    for r in range(len(lens)):
+        for t in range(cu[r], cu[r + 1]):
+            n = int(lens[r]) - int(cu[r + 1]) + 1 + t
+            out[t] = attend(q[t:t + 1], k, v, table[r:r + 1], [n], scale)[0][0]
+    return out
