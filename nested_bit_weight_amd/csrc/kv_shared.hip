@@ -58,8 +58,8 @@ struct Segment {
     int row;             // whose table holds its slots
     int token, tokens;   // its lines' tokens
     int start, end;      // its slots
-    int chunks, blocks;  // units of a head: of a block of lines, and blocks
-    int pad;
+    int chunks, blocks;  // units of a block of lines of a head, and blocks
+    int ranges;          // pieces that those units are cut into
 };
 
 // The call's division of work and its scratch.
@@ -69,14 +69,25 @@ struct SharedPlan {
     int2 *tokens;                // [tokens] the token's row, or -1, and that row's group, or -1
     int32_t *sees;               // [tokens] slots that it sees
     int32_t *shares;             // [2] of the workgroups, those of each side
+    int32_t *reach;              // [2] units of a piece at most
     struct Side {                // 0: the groups' prefixes, 1: the rows' own slots
         int lines, segments;     // lines of a block
+        int64_t places;          // that there are
         Segment *segment;        // [segments]
-        int64_t *units;          // [segments + 1] units before each segment
-        float *first_ml, *first_o;  // [tokens][q_heads][2], [..][dim]: a line's part from its segment's first slot on
-        float *more_ml, *more_o;    // [wgs][lines][2], [..][dim]: the part that a workgroup begins elsewhere
+        int64_t *cost;           // [segments + 1] of the segments before each
+        int64_t *parts;          // [segments] places of parts before each segment's
+        float *ml, *o;           // [place][2] and [place][dim]: a line's part, its m and sum, and o.  First the
+                                 // [wgs][lines] that a workgroup begins within a piece, then a place for
+                                 // each piece's beginning: by segment, head, range and line
     } side[2];
 };
+
+// A piece costs as much as its units and START more, for the loads that depend on each other at its
+// start and the result at its end (few lines: 7 us beside 3 for a unit; many: 8 beside 5).
+constexpr int START = 2;
+__device__ __forceinline__ int64_t head_cost(const Segment &s) {
+    return (int64_t)s.blocks * (s.chunks + START * s.ranges);
+}
 
 __device__ __forceinline__ int bounded(int x, int low, int high) { return min(max(x, low), high); }
 __device__ __forceinline__ int first_token(const KvAttendShared &a, int row) {
@@ -99,11 +110,31 @@ __device__ __forceinline__ int group_of(const KvAttendShared &a, int row) {
     return g < a.groups && a.group_rows[g] <= row ? g : -1;
 }
 
-// The last workgroup of the launch counts the segments' units, the others find each token's row.
+// The sum of x over the workgroup's threads up to this one, and over all.
+template <int THREADS>
+__device__ __forceinline__ int64_t upto_mine(int64_t x, int64_t *s_wave, int64_t *all) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t y = __shfl_up(x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 63) s_wave[wave] = x;
+    __syncthreads();
+    *all = 0;
+    for (int w = 0; w < THREADS / 64; ++w) {
+        if (w < wave) x += s_wave[w];
+        *all += s_wave[w];
+    }
+    __syncthreads();
+    return x;
+}
+
+// The last workgroup of the launch divides the work, the others find each token's row.
 constexpr int PLAN_THREADS = 256;
 __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c, KvAttendShared a, SharedPlan pl) {
-    __shared__ int64_t s_wave[PLAN_THREADS / 64], s_all[2];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    __shared__ int64_t s_wave[PLAN_THREADS / 64];
+    const int tid = threadIdx.x;
     if (blockIdx.x + 1 < gridDim.x) {
         const int token = blockIdx.x * PLAN_THREADS + tid;
         if (token >= a.tokens) return;
@@ -117,13 +148,14 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
         pl.sees[token] = row < 0 ? 0 : max(kv_len(a.lens, row, a.max_len) - behind, 0);
         return;
     }
-    // Running sums of the segments' units, a strip of segments for each thread.
+    // The segments, a strip of them for each thread, and their units.
+    int64_t units[2], blocks[2];
+#pragma unroll
     for (int which = 0; which < 2; ++which) {
         const auto &side = pl.side[which];
-        const int n = side.segments;
-        const int strip = (n + PLAN_THREADS - 1) / PLAN_THREADS, s0 = min(tid * strip, n), s1 = min(s0 + strip, n);
-        int64_t mine = 0;
-        for (int s = s0; s < s1; ++s) {
+        const int n = side.segments, strip = (n + PLAN_THREADS - 1) / PLAN_THREADS;
+        int64_t u = 0, b = 0;
+        for (int s = min(tid * strip, n); s < min((tid + 1) * strip, n); ++s) {
             Segment x = {s, 0, 0, 0, 0, 0, 0, 0};
             if (which) {
                 const int g = group_of(a, s), t1 = first_token(a, s + 1);
@@ -139,44 +171,65 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
                 x.end = bounded(a.prefix[s], 0, a.max_len);
             }
             x.chunks = x.tokens > 0 && x.end > x.start ? (x.end - x.start + UNIT - 1) / UNIT : 0;
-            x.blocks = (int)(((int64_t)x.tokens * pl.group + side.lines - 1) / side.lines);
+            x.blocks = x.chunks ? (int)(((int64_t)x.tokens * pl.group + side.lines - 1) / side.lines) : 0;
             side.segment[s] = x;
-            mine += (int64_t)c.heads * x.blocks * x.chunks;
+            u += (int64_t)x.blocks * x.chunks;
+            b += x.blocks;
         }
-        int64_t upto = mine;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int64_t x = __shfl_up(upto, d);
-            if (lane >= d) upto += x;
-        }
-        if (lane == 63) s_wave[wave] = upto;
-        __syncthreads();
-        for (int w = 0; w < wave; ++w) upto += s_wave[w];
-        int64_t at = upto - mine;
-        for (int s = s0; s < s1; ++s) {
-            side.units[s] = at;
-            at += (int64_t)c.heads * side.segment[s].blocks * side.segment[s].chunks;
-        }
-        if (tid == PLAN_THREADS - 1) side.units[n] = s_all[which] = upto;
-        __syncthreads();
+        upto_mine<PLAN_THREADS>(u * c.heads, s_wave, &units[which]);
+        upto_mine<PLAN_THREADS>(b * c.heads, s_wave, &blocks[which]);
     }
-    if (tid == 0) {
-        // Workgroups by the sides' units, one for each unit at the most and one for a side that has any.
-        const int64_t u0 = s_all[0], u1 = s_all[1];
-        int64_t n0 = u0, n1 = u1;
-        if (u0 + u1 > pl.wgs) {
-            n0 = (pl.wgs * u0 + (u0 + u1) / 2) / (u0 + u1);
-            n0 = min(max(n0, (int64_t)(u0 > 0)), (int64_t)pl.wgs - (u1 > 0));
-            n1 = min(pl.wgs - n0, u1);
+    // Workgroups by the sides' cost, a unit of many lines taking 5/3 of the time of one of few; one for each
+    // unit at the most, and one for a side that has any.
+    int64_t n0 = units[0], n1 = units[1];
+    if (n0 + n1 > pl.wgs) {
+        const int64_t w0 = (units[0] + START * blocks[0]) * (pl.side[0].lines > 32 ? 5 : 3);
+        const int64_t w1 = (units[1] + START * blocks[1]) * (pl.side[1].lines > 32 ? 5 : 3);
+        n0 = (pl.wgs * w0 + (w0 + w1) / 2) / (w0 + w1);
+        n0 = min(max(n0, (int64_t)(w0 > 0)), (int64_t)pl.wgs - (w1 > 0));
+        n0 = min(n0, units[0]);
+        n1 = min(pl.wgs - n0, units[1]);
+    }
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        // A piece has no more units than an equal share: the blocks of a range of slots then go to
+        // neighbouring workgroups, which meet its keys and values at about the same time.
+        const auto &side = pl.side[which];
+        const int64_t shares = which ? n1 : n0;
+        const int reach = shares ? (int)((units[which] + shares - 1) / shares) : 1;
+        if (tid == 0) {
+            pl.shares[which] = (int)shares;
+            pl.reach[which] = reach;
         }
-        pl.shares[0] = (int)n0;
-        pl.shares[1] = (int)n1;
+        const int n = side.segments, strip = (n + PLAN_THREADS - 1) / PLAN_THREADS, s0 = min(tid * strip, n), s1 = min(s0 + strip, n);
+        auto places_of = [&](const Segment &x) { return (int64_t)((x.chunks + reach - 1) / reach) * x.tokens * pl.group * c.heads; };
+        int64_t cost = 0, parts = 0, all;
+        for (int s = s0; s < s1; ++s) parts += places_of(side.segment[s]);
+        int64_t place = upto_mine<PLAN_THREADS>(parts, s_wave, &all) - parts;
+        for (int s = s0; s < s1; ++s) {
+            Segment x = side.segment[s];
+            const int64_t n = places_of(x);
+            // Rows that say they have the same tokens would need more places than there are.
+            if (place + n + (int64_t)pl.wgs * side.lines > side.places) x.chunks = 0;
+            x.ranges = (x.chunks + reach - 1) / reach;
+            side.segment[s].chunks = x.chunks;
+            side.segment[s].ranges = x.ranges;
+            side.parts[s] = place;
+            place += n;
+            cost += head_cost(x) * c.heads;
+        }
+        int64_t at = upto_mine<PLAN_THREADS>(cost, s_wave, &all) - cost;
+        if (tid == 0) side.cost[n] = all;
+        for (int s = s0; s < s1; ++s) {
+            side.cost[s] = at;
+            at += head_cost(side.segment[s]) * c.heads;
+        }
     }
 }
 
-// The workgroup whose share a unit is in.
-__device__ __forceinline__ int owner_of(int64_t unit, int64_t units, int shares) {
-    return (int)(((unit + 1) * shares - 1) / units);
+// The share that a place among all costs is in.
+__device__ __forceinline__ int owner_of(int64_t at, int64_t all, int shares) {
+    return (int)(((at + 1) * shares - 1) / all);
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
@@ -215,6 +268,9 @@ __device__ __forceinline__ void meet() {  // the workgroup's waves, their LDS ac
     asm volatile("" ::: "memory");
 }
 
+// Nothing is moved across: what is written before it is asked for, or begun, before what follows.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
 // How a workgroup takes its lines.  Few: 32, and of each 128 slots a wave has 32, in LDS of its
 // own, so that no wave waits for another.  Many: 128, 32 to a wave, over tiles in two buffers
 // that the waves fill together.
@@ -236,15 +292,14 @@ struct Shape {
 
 // 16 bytes of each lane to LDS, side by side from `lds` on, which is the same for all of them.  Written out, as the
 // compiler puts a wait for all such loads before each transposing read, whatever that reads; what
-// has to have arrived is said by wait_loads.  No register is written.
+// has to have arrived is said by wait_loads.  No register is written but m0, which nothing else here uses.
 __device__ __forceinline__ void load_to_lds(const uint8_t *p, uint8_t *lds) {
     const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) void *)lds);
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(at) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(at) : "memory");
 }
 
 struct SharedLds {
     uint8_t *pool;
-    int (*bad)[SHARED_WAVES];   // by buffer and wave: a page of the tile is not there
     float (*m)[32], (*l)[32];   // by wave and line
 };
 
@@ -259,44 +314,59 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int half = lane >> 5, col = lane & 31;
     const auto &side = pl.side[which];
-    const int64_t units = side.units[side.segments];
-    int64_t u = units * share / shares;
-    const int64_t u1 = units * (share + 1) / shares;
+    const int64_t all_cost = side.cost[side.segments];
+    const int reach = pl.reach[which];
+    int64_t u = all_cost * share / shares;
+    const int64_t u1 = all_cost * (share + 1) / shares;
     int seg = 0;  // segments that end at or before u
     for (int at = 0; at < side.segments; at += 64) {
-        const int n = __popcll(__ballot(at + lane < side.segments && side.units[at + lane + 1] <= u));
+        const int n = __popcll(__ballot(at + lane < side.segments && side.cost[at + lane + 1] <= u));
         seg += n;
         if (n < 64) break;
     }
 
-    // A row of a tile has its pieces at places turned by the row's number s: by (s / R) % PIECES for
-    // keys, whose readers have 32 rows side by side; by 4 ((s / R) % (8 / R)) for values, whose readers
-    // have 8 rows and 4 pieces.  A lane fills place l % PIECES of rows ROWS i + l / PIECES, of which s / R is
-    // 2 i + l / 32 (from a multiple of 8 on), so the piece it loads for i differs from that for 0 by bits of i.
+    // A row of a tile has its pieces at places turned by the row's number s.  Keys, whose readers have 32 rows side by
+    // side, 16 bytes each: by (s / R) % PIECES.  Values, whose readers have 8 rows and 64 bytes of each: by 4 v_way(s),
+    // which puts rows 0..3, 4..7, the even and the odd ones each in banks of their own.  A lane fills place
+    // l % PIECES of rows ROWS i + l / PIECES (from a multiple of 8 on), of which s / R is 2 i + l / 32, and v_way that
+    // of l / PIECES turned by bits of i: so the piece it loads for i differs from that for 0 by bits of i.
+    auto v_way = [](int s) { return DIM == 64 ? (s >> 1 ^ s >> 2) & 1 : DIM == 128 ? (s & 3) ^ (s >> 2 & 1) : s & 7; };
     const int first_row = FEW ? 0 : wave * X::FILLED;  // that the wave fills
     const int fill_row = lane / PIECES;
-    const int k_fill = ((lane % PIECES) ^ ((first_row / R + half) & (PIECES - 1))) << 4, v_fill = ((lane % PIECES) ^ (half << 2)) << 4;
+    const int k_fill = ((lane % PIECES) ^ ((first_row / R + half) & (PIECES - 1))) << 4;
+    const int v_fill = ((lane % PIECES) ^ (v_way(fill_row) << 2)) << 4;
     const int k_read = col * ROW, k_turn = (half ^ ((col / R) & (PIECES - 1))) << 4;
     const int v_slot = 4 * half + (lane & 15) / 4;
-    const int v_turn = ((v_slot / R) & (8 / R - 1)) << 6;
+    const int v_turn = v_way(v_slot) << 6;
     const int v_read = v_slot * ROW + (2 * ((lane >> 4) & 1) + (lane & 3) / 2) * 16 + (lane & 1) * 8;
     uint8_t *const own = lds.pool + (FEW ? wave * X::OWN : 0);
 
-    for (;;) {  // a piece: chunks [c0, c1) of one block of a segment's lines
+    for (;;) {  // a piece, or a part of one: chunks [c0, c1) of one block of a segment's lines
         const Segment sg = side.segment[seg];
-        const int64_t in = u - side.units[seg];
-        const int per_head = sg.blocks * sg.chunks, head = (int)(in / per_head), rest = (int)(in % per_head);
-        const int block = rest / sg.chunks, c0 = rest % sg.chunks, c1 = (int)min((int64_t)sg.chunks, c0 + (u1 - u));
+        const int64_t in = u - side.cost[seg], per_head = head_cost(sg), per_range = (int64_t)sg.blocks * (reach + START);
+        const int head = (int)(in / per_head);
+        int64_t rest = in % per_head;
+        const int range = (int)min(rest / per_range, (int64_t)sg.ranges - 1);
+        rest -= range * per_range;
+        const int len = min(reach, sg.chunks - range * reach);
+        const int block = (int)(rest / (len + START)), off = (int)(rest % (len + START));
+        const int take = (int)min(u1 - u, (int64_t)(len + START - off));
+        const int c0 = range * reach + max(off - START, 0), c1 = range * reach + max(off + take - START, 0);
+        const bool begins = off <= START;
+        u += take;
+        if (c0 == c1) return;  // the share ends before the piece's first unit
         const int nlines = min(X::LINES, sg.tokens * pl.group - block * X::LINES);
         const int from = sg.start + c0 * UNIT + (FEW ? wave * TILE : 0);  // the wave's first slot
         const int32_t *table = c.table + (int64_t)sg.row * c.table_ld;
 
-        // The page of a slot of a tile that the wave fills: lane l has that of its row l % FILLED.
-        int32_t page;
-        auto ask_page = [&](int tile) {
-            page = table[min(from + tile * X::STEP + first_row + lane % X::FILLED, c.cap - 1) >> c.page_log2];
+        // 64 entries of the table from pages_at on, one in each lane.
+        int32_t pages;
+        int pages_at;
+        auto ask_pages = [&](int slot) {
+            pages_at = min(slot, c.cap - 1) >> c.page_log2;
+            pages = table[min(pages_at + lane, c.width - 1)];
         };
-        ask_page(0);
+        ask_pages(from);
 
         const int line = FEW ? col : wave * 32 + col;
         const bool valid = line < nlines;
@@ -325,29 +395,35 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
         const int n = sg.end - sg.start;
         const float room = RAISE + (n > 1 ? 32 - __builtin_clz(n - 1) : 0);
 
-        // A tile's rows of a pool, by numbers: a table of one word for each of the wave's rows, in its lanes.
-        uint32_t rows = 0;
-        auto find = [&](int tile) {  // the page asked for last is the tile's
-            const int slot = from + tile * X::STEP + first_row + lane % X::FILLED;
+        // Where a tile's slots are: the numbers of the pools' rows that this lane loads a piece of.  Tells
+        // whether a slot's page is not there (in its place the pool's first page is read, and its slots left out).
+        uint32_t rows[LOADS];
+        auto find = [&](int tile) {
+            const int slot0 = from + tile * X::STEP, slot = min(slot0 + lane % TILE, c.cap - 1);
+            if ((min(slot0 + TILE, c.cap) - 1 >> c.page_log2) - pages_at >= 64) ask_pages(slot0);
+            const int32_t page = __shfl(pages, (slot >> c.page_log2) - pages_at);
             const bool there = page >= 0 && page < c.pages;
-            rows = (((uint32_t)(there ? page : 0) * (uint32_t)c.heads + (uint32_t)head) << c.page_log2) +
-                   (uint32_t)(slot & ((1 << c.page_log2) - 1));
-            return __any(!there);
+            const uint32_t mine = (((uint32_t)(there ? page : 0) * (uint32_t)c.heads + (uint32_t)head) << c.page_log2) +
+                                  (uint32_t)(slot & ((1 << c.page_log2) - 1));
+            int row = first_row + fill_row;
+            again(row);
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) rows[i] = __shfl(mine, row + i * X::ROWS);
+            return (bool)__any(!there);
         };
         // 8-bit values come through registers, to be widened.
         u32x2_kv raw[FP8 ? 2 : 1][LOADS];
         auto load = [&](bool values, uint8_t *to_lds) {
-            int fill = values ? v_fill : k_fill, row = fill_row;
-            again(fill, row);
+            int fill = values ? v_fill : k_fill;
+            again(fill);
             const uint8_t *pool = values ? c.v : c.k;
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) {
-                const uint32_t r = __shfl(rows, row + i * X::ROWS);
-                const int at = values ? fill ^ (((2 * i) & (8 / R - 1)) << 6) : fill ^ (2 * i << 4);
+                const int at = values ? fill ^ (v_way(i * X::ROWS) << 6) : fill ^ (2 * i << 4);
                 if constexpr (FP8) {
-                    raw[values][i] = *reinterpret_cast<const u32x2_kv *>(pool + (int64_t)r * DIM + (at >> 1));
+                    raw[values][i] = *reinterpret_cast<const u32x2_kv *>(pool + (int64_t)rows[i] * DIM + (at >> 1));
                 } else {
-                    load_to_lds(pool + (int64_t)r * ROW + at, to_lds + i * 1024);
+                    load_to_lds(pool + (int64_t)rows[i] * ROW + at, to_lds + i * 1024);
                 }
             }
         };
@@ -371,24 +447,40 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
         f32x16_sh s[SUBS];
         u32x4_kv p[SUBS][2];
 
-        // S^T of the tile whose keys are at kb.
+        // S^T of the tile whose keys are at kb; four operands are under way while four are used.
         auto scores = [&](const uint8_t *kb) {
             int row = k_read, way = k_turn;
             again(row, way);
+            constexpr int GROUPS = SUBS * QF / 4;
+            u32x4_kv kf[2][4];
+            auto ask = [&](int g) {
 #pragma unroll
-            for (int b = 0; b < SUBS; ++b) {
+                for (int i = 0; i < 4; ++i) {
+                    const int f = (g * 4 + i) % QF, b = (g * 4 + i) / QF;
+                    kf[g & 1][i] = *reinterpret_cast<const u32x4_kv *>(kb + b * 32 * ROW + row + (way ^ (f << 5)));
+                }
+            };
+            ask(0);
+#pragma unroll
+            for (int b = 0; b < SUBS; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
 #pragma unroll
-                for (int f = 0; f < QF; ++f) {
-                    const u32x4_kv kf = *reinterpret_cast<const u32x4_kv *>(kb + b * 32 * ROW + row + (way ^ (f << 5)));
-                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_sh, kf),
+            for (int g = 0; g < GROUPS; ++g) {
+                if (g + 1 < GROUPS) ask(g + 1);
+                in_order();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int f = (g * 4 + i) % QF, b = (g * 4 + i) / QF;
+                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_sh, kf[g & 1][i]),
                                                                    __builtin_bit_cast(bf16x8_sh, q[f]), s[b], 0, 0, 0);
                 }
+                in_order();
             }
         };
-        // The weights, in s and rounded in p; `first` is the tile's first slot, `all` says that every line sees the whole tile.
-        auto weigh = [&](int first, auto all, const uint32_t *there) {
+        // The running maximum, for the scores in s; gives what the weights are taken from.  `first` is the
+        // tile's first slot, `all` says that every line sees the whole tile.
+        auto raise = [&](int first, auto all, const uint32_t *there) {
             if constexpr (!decltype(all)::value) {
 #pragma unroll
                 for (int b = 0; b < SUBS; ++b) {
@@ -418,48 +510,56 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[d][i] *= fade;
             }
-            const float ref = m == NEG_INF ? 0.f : m;
-            float part = 0.f;  // of a long sum, so that few roundings follow each other
-#pragma unroll
-            for (int b = 0; b < SUBS; ++b)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    s[b][2 * i] = __builtin_amdgcn_exp2f(fmaf(s[b][2 * i], by, -ref));
-                    s[b][2 * i + 1] = __builtin_amdgcn_exp2f(fmaf(s[b][2 * i + 1], by, -ref));
-                    const bf16x2_sh two = {(__bf16)s[b][2 * i], (__bf16)s[b][2 * i + 1]};
-                    part = __builtin_amdgcn_fdot2_f32_bf16(two, bf16x2_sh{(__bf16)1.f, (__bf16)1.f}, part, false);
-                    p[b][i / 4][i % 4] = __builtin_bit_cast(uint32_t, two);
-                }
-            sum += part;
+            return m == NEG_INF ? 0.f : m;
         };
-        // O^T with the values at vb.
-        auto add = [&](const uint8_t *vb, auto finite) {
+        // Weights 8 b + i and the one after it, in s and rounded in p, and the sum of what they are rounded to in `part`.
+        auto weigh = [&](int b, int i, float ref, float &part) {
+            s[b][2 * i] = __builtin_amdgcn_exp2f(fmaf(s[b][2 * i], by, -ref));
+            s[b][2 * i + 1] = __builtin_amdgcn_exp2f(fmaf(s[b][2 * i + 1], by, -ref));
+            const bf16x2_sh two = {(__bf16)s[b][2 * i], (__bf16)s[b][2 * i + 1]};
+            part = __builtin_amdgcn_fdot2_f32_bf16(two, bf16x2_sh{(__bf16)1.f, (__bf16)1.f}, part, false);
+            p[b][i / 4][i % 4] = __builtin_bit_cast(uint32_t, two);
+        };
+        // O^T with the values at vb.  Step k is 16 slots: while its products run, the next step's values are
+        // under way and its weights are worked out.
+        auto add = [&](const uint8_t *vb, float ref) {
             int row = v_read, way = v_turn;
             again(row, way);
+            constexpr int STEPS = 2 * SUBS;
+            u32x4_kv vf[2][DB];
+            auto ask = [&](int k) {
 #pragma unroll
-            for (int b = 0; b < SUBS; ++b)
+                for (int d = 0; d < DB; ++d) {
+                    const uint8_t *src = vb + 16 * k * ROW + row + ((d << 6) ^ way);
+                    const u32x2_kv v0 = transposed(src), v1 = transposed(src + 8 * ROW);
+                    vf[k & 1][d] = u32x4_kv{v0[0], v0[1], v1[0], v1[1]};
+                }
+            };
+            float part = 0.f;  // of a long sum, so that few roundings follow each other
+            ask(0);
+            in_order();
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+            for (int i = 0; i < 4; ++i) weigh(0, i, ref, part);
 #pragma unroll
-                    for (int d = 0; d < DB; ++d) {
-                        const uint8_t *src = vb + (b * 32 + 16 * k) * ROW + row + ((d << 6) ^ way);
-                        const u32x2_kv v0 = transposed(src), v1 = transposed(src + 8 * ROW);
-                        u32x4_kv vf = {v0[0], v0[1], v1[0], v1[1]};
-                        if constexpr (decltype(finite)::value) {
+            for (int k = 0; k < STEPS; ++k) {
+                if (k + 1 < STEPS) ask(k + 1);
+                in_order();
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if ((vf[e] & 0x7F80u) == 0x7F80u) vf[e] &= 0xFFFF0000u;
-                                if ((vf[e] & 0x7F800000u) == 0x7F800000u) vf[e] &= 0x0000FFFFu;
-                            }
-                        }
-                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_sh, vf),
-                                                                       __builtin_bit_cast(bf16x8_sh, p[b][k]), o[d], 0, 0, 0);
-                    }
+                for (int d = 0; d < DB; ++d) {
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_sh, vf[k & 1][d]),
+                                                                   __builtin_bit_cast(bf16x8_sh, p[k / 2][k % 2]), o[d], 0, 0, 0);
+                    if (k + 1 < STEPS)
+#pragma unroll
+                        for (int i = d * 4 / DB; i < (d + 1) * 4 / DB; ++i) weigh((k + 1) / 2, (k + 1) % 2 * 4 + i, ref, part);
+                    in_order();
+                }
+            }
+            sum += part;
         };
         // The same where a slot may not count, for a line or for all: its weight is 0, but what
         // lies there may be NaN or infinite.  Such values are left out of the product and added to the
         // lines that do see them, one slot after the other.
-        auto add_with_care = [&](const uint8_t *vb, int first, const uint32_t *there) {
+        auto add_with_care = [&](const uint8_t *vb, int first, const uint32_t *there, float ref) {
             uint32_t odd[SUBS] = {};  // slots with such a value
             for (int i = 0; i < TILE / X::ROWS; ++i) {
                 const u32x4_kv x = *reinterpret_cast<const u32x4_kv *>(vb + i * 1024 + lane * 16);
@@ -480,10 +580,32 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
 #pragma unroll
             for (int b = 0; b < SUBS; ++b) any = any || odd[b];
             if (!any) {
-                add(vb, std::false_type());
+                add(vb, ref);
                 return;
             }
-            add(vb, std::true_type());
+            float part = 0.f;
+            int row = v_read, way = v_turn;
+            again(row, way);
+#pragma unroll
+            for (int k = 0; k < 2 * SUBS; ++k) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) weigh(k / 2, k % 2 * 4 + i, ref, part);
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    in_order();  // few loads at a time
+                    const uint8_t *src = vb + 16 * k * ROW + row + ((d << 6) ^ way);
+                    const u32x2_kv v0 = transposed(src), v1 = transposed(src + 8 * ROW);
+                    u32x4_kv vf = {v0[0], v0[1], v1[0], v1[1]};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if ((vf[e] & 0x7F80u) == 0x7F80u) vf[e] &= 0xFFFF0000u;
+                        if ((vf[e] & 0x7F800000u) == 0x7F800000u) vf[e] &= 0x0000FFFFu;
+                    }
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_sh, vf),
+                                                                   __builtin_bit_cast(bf16x8_sh, p[k / 2][k % 2]), o[d], 0, 0, 0);
+                }
+            }
+            sum += part;
             int dim0 = 4 * half;
             again(dim0);
 #pragma unroll
@@ -497,13 +619,13 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
                         if (8 * (i / 4) + i % 4 == (j & ~4)) w = s[b][i];
                     w = __shfl(w, col + 32 * (j >> 2 & 1));
                     const bool seen = first + b * 32 + j < sees;
-                    const int row = b * 32 + j, turn = ((row / R) & (8 / R - 1)) << 6;
+                    const int row = b * 32 + j, turn = v_way(row) << 6;
                     const uint8_t *src = vb + row * ROW + dim0 * 2;
 #pragma unroll
                     for (int d = 0; d < DB; ++d) {
-                        __builtin_amdgcn_sched_barrier(0);  // few loads at a time
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
+                            if (i % 4 == 0) in_order();  // few loads at a time
                             const uint32_t x = *reinterpret_cast<const uint16_t *>(src + (((d << 6) ^ turn) + 16 * (i / 4) + 2 * (i % 4)));
                             if ((x & 0x7F80u) == 0x7F80u && seen) o[d][i] += w * __uint_as_float(x << 16);
                         }
@@ -531,26 +653,24 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
                 missing = find(0);
                 load(false, kb);
                 load(true, vb);
-                ask_page(min(1, tiles - 1));
             }
             auto step = [&](int t, auto all) {
                 const int first = from + t * X::STEP;
                 if constexpr (FP8) widen(false, kb);
-                else wait_loads<LOADS + 1>();  // the values and a page number
+                else wait_loads<LOADS>();  // the values
                 scores(kb);
                 wait_lds();
-                if constexpr (!FP8) wait_loads<0>();
                 uint32_t there[SUBS];
                 if constexpr (!decltype(all)::value) present(first, missing, there);
                 missing = find(min(t + 1, tiles - 1));
                 if constexpr (FP8) widen(true, vb);
                 load(false, kb);
-                weigh(first, all, there);
-                if constexpr (decltype(all)::value) add(vb, std::false_type());
-                else add_with_care(vb, first, there);
+                const float ref = raise(first, all, there);
+                if constexpr (!FP8) wait_loads<LOADS>();  // the next keys
+                if constexpr (decltype(all)::value) add(vb, ref);
+                else add_with_care(vb, first, there, ref);
                 wait_lds();
                 load(true, vb);
-                ask_page(min(t + 2, tiles - 1));
             };
             int t = 0;
             for (; t < tiles && from + t * X::STEP + TILE <= least && !missing; ++t) step(t, std::true_type());
@@ -559,8 +679,6 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
         } else {
             auto buf = [&](int t) { return own + (t & 1) * 2 * TILE * ROW; };
             auto fill = [&](int t) {
-                const bool any = find(t);
-                if (lane == 0) lds.bad[t & 1][wave] = any;
                 load(false, buf(t) + first_row * ROW);
                 load(true, buf(t) + (TILE + first_row) * ROW);
             };
@@ -573,47 +691,45 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
                 }
                 meet();
             };
-            auto missing = [&](int t) {
-                bool any = false;
-#pragma unroll
-                for (int w = 0; w < SHARED_WAVES; ++w) any = any || lds.bad[t & 1][w];
-                return (bool)__builtin_amdgcn_readfirstlane(any);
-            };
+            bool missing = false, missing_next = false;
             if (tiles > 0) {
+                missing = find(0);
                 fill(0);
-                ask_page(min(1, tiles - 1));
+                missing_next = find(min(1, tiles - 1));
                 arrive(0);
             }
             // Each wave meets the others once a tile, whichever of the two loops it is in.
             auto step = [&](int t, auto all) {
-                if (t + 1 < tiles) {
-                    fill(t + 1);
-                    ask_page(min(t + 2, tiles - 1));
-                }
+                if (t + 1 < tiles) fill(t + 1);
                 const int first = from + t * X::STEP;
                 const uint8_t *kb = buf(t), *vb = kb + TILE * ROW;
                 if constexpr (decltype(all)::value) {
                     scores(kb);
-                    weigh(first, all, nullptr);
-                    add(vb, std::false_type());
+                    add(vb, raise(first, all, nullptr));
                 } else if (first < most) {
                     uint32_t there[SUBS];
-                    present(first, missing(t), there);
+                    present(first, missing, there);
                     scores(kb);
-                    weigh(first, all, there);
-                    add_with_care(vb, first, there);
+                    add_with_care(vb, first, there, raise(first, all, there));
                 }
-                if (t + 1 < tiles) arrive(t + 1);
+                if (t + 1 < tiles) {
+                    missing = missing_next;
+                    missing_next = find(min(t + 2, tiles - 1));
+                    arrive(t + 1);
+                }
             };
             int t = 0;
-            for (; t < tiles && from + t * X::STEP + TILE <= least && !missing(t); ++t) step(t, std::true_type());
+            for (; t < tiles && from + t * X::STEP + TILE <= least && !missing; ++t) step(t, std::true_type());
             for (; t < tiles; ++t) step(t, std::false_type());
         }
 
         // The piece's result.  One that has all that its lines see is the result; others wait for the join.
         sum += __shfl_xor(sum, 32);
-        const bool sole = which && sg.start == 0 && c0 == 0 && c1 == sg.chunks;
+        const bool sole = which && sg.start == 0 && c1 - c0 == sg.chunks;
         const float v_by = FP8 ? c.v_scale[head] : 1.f;
+        const int64_t part0 = begins ? (int64_t)pl.wgs * X::LINES + side.parts[seg] +
+                                           ((int64_t)head * sg.ranges + range) * sg.tokens * pl.group + block * X::LINES
+                                     : (int64_t)share * X::LINES;
         auto store = [&](int ln, int d, f32x4_sh x, float mm, float total) {  // dims d..d+3 of a line of the block
             const int sl = block * X::LINES + ln;
             const int64_t t = sg.token + sl / pl.group, qh = head * pl.group + sl % pl.group;
@@ -623,12 +739,11 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
                 *reinterpret_cast<u32x2_kv *>(a.out + t * a.out_ld + qh * DIM + d) =
                     u32x2_kv{bf16_pair(x[0] * inv, x[1] * inv), bf16_pair(x[2] * inv, x[3] * inv)};
             } else {
-                const int64_t at = c0 == 0 ? t * a.q_heads + qh : (int64_t)share * X::LINES + ln;
-                float *ml = c0 == 0 ? side.first_ml : side.more_ml, *po = c0 == 0 ? side.first_o : side.more_o;
-                *reinterpret_cast<f32x4_sh *>(po + at * DIM + d) = x;
+                const int64_t at = part0 + ln;
+                *reinterpret_cast<f32x4_sh *>(side.o + at * DIM + d) = x;
                 if (d == 0) {
-                    ml[2 * at] = mm;
-                    ml[2 * at + 1] = total;
+                    side.ml[2 * at] = mm;
+                    side.ml[2 * at + 1] = total;
                 }
             }
         };
@@ -666,19 +781,17 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
                 store(ln, d, x, top, total);
             }
         }
-        u += c1 - c0;
         if (u >= u1) return;
         meet();  // the pool and the sums are free
-        while (side.units[seg + 1] <= u) ++seg;
+        while (side.cost[seg + 1] <= u) ++seg;
     }
 }
 
 template <int DIM, bool FP8>
 __global__ __launch_bounds__(SHARED_THREADS, DIM > 128 ? 1 : 2) void kv_shared_kernel(KvCache c, KvAttendShared a, SharedPlan pl) {
     __shared__ __align__(16) uint8_t pool[std::max(Shape<DIM, true>::BYTES, Shape<DIM, false>::BYTES)];
-    __shared__ __align__(16) int s_bad[2][SHARED_WAVES];
     __shared__ float s_m[SHARED_WAVES][32], s_l[SHARED_WAVES][32];
-    const SharedLds lds = {pool, s_bad, s_m, s_l};
+    const SharedLds lds = {pool, s_m, s_l};
     const int n0 = pl.shares[0], n1 = pl.shares[1], b = (int)blockIdx.x;
     if (b >= n0 + n1) return;
     const int which = b >= n0;
@@ -691,6 +804,7 @@ __global__ __launch_bounds__(SHARED_THREADS, DIM > 128 ? 1 : 2) void kv_shared_k
 
 // The last launch: each line's parts, in a fixed order, by a wave.
 constexpr int JOIN_THREADS = 256;
+constexpr float PART_BY = 1.f / (1 << 20);  // each part's weights sum to 1 at the most, and there are fewer than 2^20 of them
 template <int DIM>
 __global__ __launch_bounds__(JOIN_THREADS) void kv_shared_join_kernel(KvCache c, KvAttendShared a, SharedPlan pl) {
     constexpr int LANES = DIM / 4, SLICES = 64 / LANES;  // lanes of a part, four dims each, and parts taken side by side
@@ -700,8 +814,13 @@ __global__ __launch_bounds__(JOIN_THREADS) void kv_shared_join_kernel(KvCache c,
     const int token = line / a.q_heads, qh = line % a.q_heads, head = qh / pl.group;
     const int2 of = pl.tokens[token];
     if (of.x < 0) return;
-    int first[2] = {0, 0}, n[2] = {0, 0}, in_block[2] = {0, 0};  // of each side: the first part's share, parts, line of its block
-    bool written = false;
+    // Where the line's parts are, RANGES ranges at a time: of each the part that begins it and those that
+    // workgroups begin within it, 3 at the most: a share is more than half of a piece.
+    constexpr int RANGES = 64, MOST_PARTS = 4;
+    __shared__ uint32_t s_place[JOIN_THREADS / 64][RANGES * MOST_PARTS];
+    uint32_t *const places = s_place[threadIdx.x >> 6];
+    float top = NEG_INF, total = 0.f;
+    f32x4_sh x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         const int seg = which ? of.x : of.y;
@@ -709,60 +828,65 @@ __global__ __launch_bounds__(JOIN_THREADS) void kv_shared_join_kernel(KvCache c,
         const auto &side = pl.side[which];
         const Segment sg = side.segment[seg];
         if (sg.chunks == 0) continue;
-        const int64_t units = side.units[side.segments];
-        const int shares = pl.shares[which];
+        const int64_t all_cost = side.cost[side.segments];
+        const int shares = pl.shares[which], reach = pl.reach[which];
         const int in = (token - sg.token) * pl.group + qh % pl.group, block = in / side.lines;
-        const int64_t at = side.units[seg] + ((int64_t)head * sg.blocks + block) * sg.chunks;
-        first[which] = owner_of(at, units, shares);
-        n[which] = owner_of(at + sg.chunks - 1, units, shares) - first[which] + 1;
-        in_block[which] = in % side.lines;
-        written = which && sg.start == 0 && n[1] == 1;
-    }
-    if (written) return;
-    auto place = [&](int i, const float *&ml, const float *&po) {
-        const int which = i >= n[0];
-        const auto &side = pl.side[which];
-        i -= which ? n[0] : 0;
-        const int64_t at = i == 0 ? line : (int64_t)(first[which] + i) * side.lines + in_block[which];
-        ml = (i == 0 ? side.first_ml : side.more_ml) + 2 * at;
-        po = (i == 0 ? side.first_o : side.more_o) + at * DIM + d;
-    };
-    const int parts = n[0] + n[1];
-    const float *ml, *po;
-    // The largest m, and each part's share of the sum before any meets its o: finite values cannot run over.
-    float top = NEG_INF, total = 0.f;
-    for (int i = lane; i < parts; i += 64) {
-        place(i, ml, po);
-        const float m = ml[0], up = fmaxf(top, m);
-        total = total * (top == up ? 1.f : __builtin_amdgcn_exp2f(top - up)) + ml[1] * (m == up ? 1.f : __builtin_amdgcn_exp2f(m - up));
-        top = up;
-    }
-    float all = top;
+        const int64_t first = side.cost[seg] + head * head_cost(sg);
+        const int64_t place0 = (int64_t)pl.wgs * side.lines + side.parts[seg] + (int64_t)head * sg.ranges * sg.tokens * pl.group + in;
+        for (int r0 = 0; r0 < sg.ranges; r0 += RANGES) {
+            const int r = r0 + lane, len = min(reach, sg.chunks - r * reach);
+            int n = 0, w0 = 0;
+            if (r < sg.ranges) {
+                const int64_t at = first + (int64_t)r * sg.blocks * (reach + START) + (int64_t)block * (len + START) + START;
+                w0 = owner_of(at, all_cost, shares);
+                n = min(owner_of(at + len - 1, all_cost, shares) - w0 + 1, MOST_PARTS);
+            }
+            const int upto = wave_running_sum(n), parts = __builtin_amdgcn_readlane(upto, 63);
+            if (which && sg.start == 0 && sg.ranges == 1 && parts == 1) return;  // written already
+            for (int i = 0; i < n; ++i)
+                places[upto - n + i] = (uint32_t)(i == 0 ? place0 + (int64_t)r * sg.tokens * pl.group
+                                                         : (int64_t)(w0 + i) * side.lines + in % side.lines);
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            // The largest m of them, and their sums and results from there.
+            float up = top;
+            for (int i = lane; i < parts; i += 64) up = fmaxf(up, side.ml[2 * (int64_t)places[i]]);
 #pragma unroll
-    for (int s = 1; s < 64; s <<= 1) all = fmaxf(all, __shfl_xor(all, s));
-    total *= top == all ? 1.f : __builtin_amdgcn_exp2f(top - all);
+            for (int s = 1; s < 64; s <<= 1) up = fmaxf(up, __shfl_xor(up, s));
+            const float fade = top == up ? 1.f : __builtin_amdgcn_exp2f(top - up);
+            total *= fade;
+            x *= fade;
+            top = up;
+            constexpr int AHEAD = 4;
+            for (int i0 = 0; i0 < parts; i0 += AHEAD * SLICES) {
+                f32x4_sh y[AHEAD];
+                float m[AHEAD], l[AHEAD];
 #pragma unroll
-    for (int s = 1; s < 64; s <<= 1) total += __shfl_xor(total, s);
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    f32x4_sh x = {0.f, 0.f, 0.f, 0.f};
-    constexpr int AHEAD = 4;
-    for (int i0 = 0; i0 < parts; i0 += AHEAD * SLICES) {
-        f32x4_sh y[AHEAD];
-        float m[AHEAD];
+                for (int k = 0; k < AHEAD; ++k) {
+                    const int64_t at = places[min(i0 + k * SLICES + lane / LANES, parts - 1)];
+                    m[k] = side.ml[2 * at];
+                    l[k] = side.ml[2 * at + 1];
+                    y[k] = *reinterpret_cast<const f32x4_sh *>(side.o + at * DIM + d);
+                }
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            place(min(i0 + k * SLICES + lane / LANES, parts - 1), ml, po);
-            m[k] = ml[0];
-            y[k] = *reinterpret_cast<const f32x4_sh *>(po);
+                for (int k = 0; k < AHEAD; ++k)
+                    if (i0 + k * SLICES + lane / LANES < parts) {
+                        const float f = m[k] == top ? 1.f : __builtin_amdgcn_exp2f(m[k] - top);
+                        total += l[k] * f;
+                        x += y[k] * (f * PART_BY);
+                    }
+            }
+            __builtin_amdgcn_wave_barrier();
         }
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k)
-            if (i0 + k * SLICES + lane / LANES < parts) x += y[k] * ((m[k] == all ? 1.f : __builtin_amdgcn_exp2f(m[k] - all)) * inv);
     }
 #pragma unroll
-    for (int s = LANES; s < 64; s <<= 1)
+    for (int s = LANES; s < 64; s <<= 1) {
+        total += __shfl_xor(total, s);
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] += __shfl_xor(x[e], s);
+    }
+    x *= total == 0.f ? 0.f : 1.f / (total * PART_BY);
     if (total == 0.f) x = f32x4_sh{0.f, 0.f, 0.f, 0.f};  // nothing to attend to, whatever the values are
     if (c.fp8) x *= c.v_scale[head];
     if (lane < LANES)
@@ -797,16 +921,17 @@ static int64_t shared_plan(const KvCache &c, int q_heads, int tokens, int groups
     pl->tokens = (int2 *)take((int64_t)tokens * 8);
     pl->sees = (int32_t *)take((int64_t)tokens * 4);
     pl->shares = (int32_t *)take(8);
+    pl->reach = (int32_t *)take(8);
     for (int which = 0; which < 2; ++which) {
         auto &side = pl->side[which];
-        const int64_t all = side.segments ? (int64_t)tokens * q_heads : 0;
-        const int64_t more = side.segments ? (int64_t)pl->wgs * side.lines : 0;
         side.segment = (Segment *)take((int64_t)side.segments * sizeof(Segment));
-        side.units = (int64_t *)take(((int64_t)side.segments + 1) * 8);
-        side.first_ml = (float *)take(all * 8);
-        side.first_o = (float *)take(all * c.dim * 4);
-        side.more_ml = (float *)take(more * 8);
-        side.more_o = (float *)take(more * c.dim * 4);
+        side.cost = (int64_t *)take(((int64_t)side.segments + 1) * 8);
+        side.parts = (int64_t *)take((int64_t)side.segments * 8);
+        // A line for each that a workgroup may begin within a piece; and by segment, head, range and line: with
+        // ranges no longer than needed, a block more for each workgroup than the lines there are.
+        side.places = side.segments ? 2 * (int64_t)pl->wgs * side.lines + (int64_t)tokens * q_heads : 0;
+        side.ml = (float *)take(side.places * 8);
+        side.o = (float *)take(side.places * c.dim * 4);
     }
     return at;
 }
