@@ -110,30 +110,37 @@ __device__ __forceinline__ int group_of(const KvAttendShared &a, int row) {
     return g < a.groups && a.group_rows[g] <= row ? g : -1;
 }
 
-// The sum of x over the workgroup's threads up to this one, and over all.
-template <int THREADS>
-__device__ __forceinline__ int64_t upto_mine(int64_t x, int64_t *s_wave, int64_t *all) {
+// The sums of N numbers over the workgroup's threads up to this one, in x, and over all.
+template <int N, int THREADS>
+__device__ __forceinline__ void add_up(int64_t (&x)[N], int64_t (&all)[N], int64_t (*s_wave)[N]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int64_t y = __shfl_up(x, d);
-        if (lane >= d) x += y;
-    }
-    if (lane == 63) s_wave[wave] = x;
+    for (int d = 1; d < 64; d <<= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int64_t y = __shfl_up(x[i], d);
+            if (lane >= d) x[i] += y;
+        }
+    if (lane == 63)
+#pragma unroll
+        for (int i = 0; i < N; ++i) s_wave[wave][i] = x[i];
     __syncthreads();
-    *all = 0;
-    for (int w = 0; w < THREADS / 64; ++w) {
-        if (w < wave) x += s_wave[w];
-        *all += s_wave[w];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        all[i] = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 64; ++w) {
+            if (w < wave) x[i] += s_wave[w][i];
+            all[i] += s_wave[w][i];
+        }
     }
     __syncthreads();
-    return x;
 }
 
 // The last workgroup of the launch divides the work, the others find each token's row.
 constexpr int PLAN_THREADS = 256;
 __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c, KvAttendShared a, SharedPlan pl) {
-    __shared__ int64_t s_wave[PLAN_THREADS / 64];
+    __shared__ int64_t s_wave[PLAN_THREADS / 64][4];
     const int tid = threadIdx.x;
     if (blockIdx.x + 1 < gridDim.x) {
         const int token = blockIdx.x * PLAN_THREADS + tid;
@@ -148,82 +155,91 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
         pl.sees[token] = row < 0 ? 0 : max(kv_len(a.lens, row, a.max_len) - behind, 0);
         return;
     }
-    // The segments, a strip of them for each thread, and their units.
-    int64_t units[2], blocks[2];
+    // A strip of segments for each thread; with no more segments than threads its one stays in registers.
+    auto of = [&](int which, int s) {
+        Segment x = {s, 0, 0, 0, 0, 0, 0, 0};
+        if (which) {
+            const int g = group_of(a, s), t1 = first_token(a, s + 1);
+            x.token = first_token(a, s);
+            x.tokens = max(t1 - x.token, 0);
+            x.start = g < 0 ? 0 : bounded(a.prefix[g], 0, a.max_len);
+            x.end = kv_len(a.lens, s, a.max_len);
+        } else {
+            const int r0 = bounded(a.group_rows[s], 0, c.rows), r1 = bounded(a.group_rows[s + 1], 0, c.rows);
+            x.row = r0;
+            x.token = first_token(a, r0);
+            x.tokens = r0 < r1 ? max(first_token(a, r1) - x.token, 0) : 0;
+            x.end = bounded(a.prefix[s], 0, a.max_len);
+        }
+        x.chunks = x.tokens > 0 && x.end > x.start ? (x.end - x.start + UNIT - 1) / UNIT : 0;
+        x.blocks = x.chunks ? (int)(((int64_t)x.tokens * pl.group + pl.side[which].lines - 1) / pl.side[which].lines) : 0;
+        return x;
+    };
+    int s0[2], s1[2];
+    Segment mine[2];
+    int64_t sums[4] = {0, 0, 0, 0}, all[4];  // units and blocks of both sides
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-        const auto &side = pl.side[which];
-        const int n = side.segments, strip = (n + PLAN_THREADS - 1) / PLAN_THREADS;
-        int64_t u = 0, b = 0;
-        for (int s = min(tid * strip, n); s < min((tid + 1) * strip, n); ++s) {
-            Segment x = {s, 0, 0, 0, 0, 0, 0, 0};
-            if (which) {
-                const int g = group_of(a, s), t1 = first_token(a, s + 1);
-                x.token = first_token(a, s);
-                x.tokens = max(t1 - x.token, 0);
-                x.start = g < 0 ? 0 : bounded(a.prefix[g], 0, a.max_len);
-                x.end = kv_len(a.lens, s, a.max_len);
-            } else {
-                const int r0 = bounded(a.group_rows[s], 0, c.rows), r1 = bounded(a.group_rows[s + 1], 0, c.rows);
-                x.row = r0;
-                x.token = first_token(a, r0);
-                x.tokens = r0 < r1 ? max(first_token(a, r1) - x.token, 0) : 0;
-                x.end = bounded(a.prefix[s], 0, a.max_len);
-            }
-            x.chunks = x.tokens > 0 && x.end > x.start ? (x.end - x.start + UNIT - 1) / UNIT : 0;
-            x.blocks = x.chunks ? (int)(((int64_t)x.tokens * pl.group + side.lines - 1) / side.lines) : 0;
-            side.segment[s] = x;
-            u += (int64_t)x.blocks * x.chunks;
-            b += x.blocks;
+        const int n = pl.side[which].segments, strip = (n + PLAN_THREADS - 1) / PLAN_THREADS;
+        s0[which] = min(tid * strip, n);
+        s1[which] = min(s0[which] + strip, n);
+        for (int s = s0[which]; s < s1[which]; ++s) {
+            mine[which] = of(which, s);
+            sums[which] += (int64_t)c.heads * mine[which].blocks * mine[which].chunks;
+            sums[2 + which] += (int64_t)c.heads * mine[which].blocks;
         }
-        upto_mine<PLAN_THREADS>(u * c.heads, s_wave, &units[which]);
-        upto_mine<PLAN_THREADS>(b * c.heads, s_wave, &blocks[which]);
     }
-    // Workgroups by the sides' cost, a unit of many lines taking 5/3 of the time of one of few; one for each
+    add_up<4, PLAN_THREADS>(sums, all, s_wave);
+    // Workgroups by the sides' cost, a unit of many lines taking 5/4 of the time of one of few; one for each
     // unit at the most, and one for a side that has any.
-    int64_t n0 = units[0], n1 = units[1];
-    if (n0 + n1 > pl.wgs) {
-        const int64_t w0 = (units[0] + START * blocks[0]) * (pl.side[0].lines > 32 ? 5 : 3);
-        const int64_t w1 = (units[1] + START * blocks[1]) * (pl.side[1].lines > 32 ? 5 : 3);
-        n0 = (pl.wgs * w0 + (w0 + w1) / 2) / (w0 + w1);
-        n0 = min(max(n0, (int64_t)(w0 > 0)), (int64_t)pl.wgs - (w1 > 0));
-        n0 = min(n0, units[0]);
-        n1 = min(pl.wgs - n0, units[1]);
+    int64_t shares[2] = {all[0], all[1]};
+    if (all[0] + all[1] > pl.wgs) {
+        const int64_t w0 = (all[0] + START * all[2]) * (pl.side[0].lines > 32 ? 5 : 4);
+        const int64_t w1 = (all[1] + START * all[3]) * (pl.side[1].lines > 32 ? 5 : 4);
+        const int64_t n0 = (pl.wgs * w0 + (w0 + w1) / 2) / (w0 + w1);
+        shares[0] = min(min(max(n0, (int64_t)(w0 > 0)), (int64_t)pl.wgs - (w1 > 0)), all[0]);
+        shares[1] = min(pl.wgs - shares[0], all[1]);
     }
+    // A piece has no more units than an equal share: the blocks of a range of slots then go to
+    // neighbouring workgroups, which meet its keys and values at about the same time.
+    int reach[2];
+    auto places_of = [&](int which, const Segment &x) {
+        return (int64_t)((x.chunks + reach[which] - 1) / reach[which]) * x.tokens * pl.group * c.heads;
+    };
+    int64_t next[4] = {0, 0, 0, 0};  // places and costs of both sides
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-        // A piece has no more units than an equal share: the blocks of a range of slots then go to
-        // neighbouring workgroups, which meet its keys and values at about the same time.
-        const auto &side = pl.side[which];
-        const int64_t shares = which ? n1 : n0;
-        const int reach = shares ? (int)((units[which] + shares - 1) / shares) : 1;
+        reach[which] = shares[which] ? (int)((all[which] + shares[which] - 1) / shares[which]) : 1;
         if (tid == 0) {
-            pl.shares[which] = (int)shares;
-            pl.reach[which] = reach;
+            pl.shares[which] = (int)shares[which];
+            pl.reach[which] = reach[which];
         }
-        const int n = side.segments, strip = (n + PLAN_THREADS - 1) / PLAN_THREADS, s0 = min(tid * strip, n), s1 = min(s0 + strip, n);
-        auto places_of = [&](const Segment &x) { return (int64_t)((x.chunks + reach - 1) / reach) * x.tokens * pl.group * c.heads; };
-        int64_t cost = 0, parts = 0, all;
-        for (int s = s0; s < s1; ++s) parts += places_of(side.segment[s]);
-        int64_t place = upto_mine<PLAN_THREADS>(parts, s_wave, &all) - parts;
-        for (int s = s0; s < s1; ++s) {
-            Segment x = side.segment[s];
-            const int64_t n = places_of(x);
-            // Rows that say they have the same tokens would need more places than there are.
-            if (place + n + (int64_t)pl.wgs * side.lines > side.places) x.chunks = 0;
-            x.ranges = (x.chunks + reach - 1) / reach;
-            side.segment[s].chunks = x.chunks;
-            side.segment[s].ranges = x.ranges;
+        const bool one = s1[which] - s0[which] <= 1;
+        for (int s = s0[which]; s < s1[which]; ++s) {
+            const Segment x = one ? mine[which] : of(which, s);
+            next[which] += places_of(which, x);
+            next[2 + which] += (int64_t)c.heads * x.blocks * (x.chunks + START * ((x.chunks + reach[which] - 1) / reach[which]));
+        }
+    }
+    int64_t own[4] = {next[0], next[1], next[2], next[3]};
+    add_up<4, PLAN_THREADS>(next, all, s_wave);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const auto &side = pl.side[which];
+        int64_t place = next[which] - own[which], cost = next[2 + which] - own[2 + which];
+        const bool one = s1[which] - s0[which] <= 1;
+        for (int s = s0[which]; s < s1[which]; ++s) {
+            Segment x = one ? mine[which] : of(which, s);
+            x.ranges = (x.chunks + reach[which] - 1) / reach[which];
             side.parts[s] = place;
-            place += n;
-            cost += head_cost(x) * c.heads;
+            side.cost[s] = cost;
+            place += places_of(which, x);
+            cost += (int64_t)c.heads * head_cost(x);
+            // Rows that say they have the same tokens would need more places than there are: no lines then.
+            if (place + (int64_t)pl.wgs * side.lines > side.places) x.tokens = 0;
+            side.segment[s] = x;
         }
-        int64_t at = upto_mine<PLAN_THREADS>(cost, s_wave, &all) - cost;
-        if (tid == 0) side.cost[n] = all;
-        for (int s = s0; s < s1; ++s) {
-            side.cost[s] = at;
-            at += head_cost(side.segment[s]) * c.heads;
-        }
+        if (tid == 0) side.cost[side.segments] = all[2 + which];
     }
 }
 
@@ -274,10 +290,11 @@ __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); 
 // How a workgroup takes its lines.  Few: 32, and of each 128 slots a wave has 32, in LDS of its
 // own, so that no wave waits for another.  Many: 128, 32 to a wave, over tiles in two buffers
 // that the waves fill together.
-template <int DIM, bool FEW>
+template <int DIM, bool FP8, bool FEW>
 struct Shape {
     static constexpr int LINES = FEW ? 32 : 32 * SHARED_WAVES;
-    static constexpr int SUBS = !FEW && DIM < 256 ? 2 : 1;       // runs of 32 slots that a wave takes at once
+    // Runs of 32 slots that a wave takes at once: two would leave no registers for 8-bit values on their way, or for 256 dims.
+    static constexpr int SUBS = !FEW && DIM < (FP8 ? 128 : 256) ? 2 : 1;
     static constexpr int TILE = 32 * SUBS;                       // slots in LDS, of a wave, or of all
     static constexpr int STEP = FEW ? TILE * SHARED_WAVES : TILE; // slots from one of a wave's tiles to the next
     static constexpr int PIECES = DIM / 8;                       // of a slot's row, 16 bytes each
@@ -287,15 +304,18 @@ struct Shape {
     static constexpr int ROW = DIM * 2;
     static constexpr int PART = 32 * (DIM + 4) * 4;              // a wave's o, its rows 16 bytes past the banks' turn
     static constexpr int OWN = std::max(2 * TILE * ROW, PART);   // of a wave
-    static constexpr int BYTES = FEW ? OWN * SHARED_WAVES : 4 * TILE * ROW;
+    static constexpr int TILES = FEW ? OWN * SHARED_WAVES : 4 * TILE * ROW;
+    // Queries of 256 dims would take 64 registers; each lane has its part of them in LDS instead.  (Waves with the same
+    // lines write the same there.)
+    static constexpr bool Q_LDS = DIM > 128;
+    static constexpr int BYTES = TILES + (Q_LDS ? LINES * ROW : 0);
 };
 
 // 16 bytes of each lane to LDS, side by side from `lds` on, which is the same for all of them.  Written out, as the
 // compiler puts a wait for all such loads before each transposing read, whatever that reads; what
 // has to have arrived is said by wait_loads.  No register is written but m0, which nothing else here uses.
-__device__ __forceinline__ void load_to_lds(const uint8_t *p, uint8_t *lds) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) void *)lds);
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(at) : "memory");
+__device__ __forceinline__ void load_to_lds(const uint8_t *p, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory");
 }
 
 struct SharedLds {
@@ -307,7 +327,7 @@ struct SharedLds {
 template <int DIM, bool FP8, bool FEW>
 __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendShared &a, const SharedPlan &pl, int which, int share,
                                              int shares, const SharedLds &lds) {
-    using X = Shape<DIM, FEW>;
+    using X = Shape<DIM, FP8, FEW>;
     constexpr int TILE = X::TILE, SUBS = X::SUBS, PIECES = X::PIECES, LOADS = X::LOADS, ROW = X::ROW;
     constexpr int R = 256 / DIM;  // rows of a tile in 512 bytes, one turn of the banks
     constexpr int DB = DIM / 32, QF = DIM / 16;
@@ -333,13 +353,14 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
     auto v_way = [](int s) { return DIM == 64 ? (s >> 1 ^ s >> 2) & 1 : DIM == 128 ? (s & 3) ^ (s >> 2 & 1) : s & 7; };
     const int first_row = FEW ? 0 : wave * X::FILLED;  // that the wave fills
     const int fill_row = lane / PIECES;
-    const int k_fill = ((lane % PIECES) ^ ((first_row / R + half) & (PIECES - 1))) << 4;
-    const int v_fill = ((lane % PIECES) ^ (v_way(fill_row) << 2)) << 4;
+    const int k_fill = (lane % PIECES) ^ ((first_row / R + half) & (PIECES - 1));
+    const int v_fill = (lane % PIECES) ^ (v_way(fill_row) << 2);
     const int k_read = col * ROW, k_turn = (half ^ ((col / R) & (PIECES - 1))) << 4;
     const int v_slot = 4 * half + (lane & 15) / 4;
     const int v_turn = v_way(v_slot) << 6;
     const int v_read = v_slot * ROW + (2 * ((lane >> 4) & 1) + (lane & 3) / 2) * 16 + (lane & 1) * 8;
     uint8_t *const own = lds.pool + (FEW ? wave * X::OWN : 0);
+    const uint32_t own_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) void *)own);
 
     for (;;) {  // a piece, or a part of one: chunks [c0, c1) of one block of a segment's lines
         const Segment sg = side.segment[seg];
@@ -355,16 +376,22 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
         const bool begins = off <= START;
         u += take;
         if (c0 == c1) return;  // the share ends before the piece's first unit
+        if (sg.tokens == 0) return;
         const int nlines = min(X::LINES, sg.tokens * pl.group - block * X::LINES);
         const int from = sg.start + c0 * UNIT + (FEW ? wave * TILE : 0);  // the wave's first slot
         const int32_t *table = c.table + (int64_t)sg.row * c.table_ld;
 
-        // 64 entries of the table from pages_at on, one in each lane.
-        int32_t pages;
+        // 64 pages of the table from pages_at on, one in each lane, as the number of the pool's row that the head's slots
+        // begin with there; and which of them are not there (the pool's first page is read in their place).
+        uint32_t pages;
+        uint64_t gone = 0;
         int pages_at;
         auto ask_pages = [&](int slot) {
             pages_at = min(slot, c.cap - 1) >> c.page_log2;
-            pages = table[min(pages_at + lane, c.width - 1)];
+            const int32_t page = table[min(pages_at + lane, c.width - 1)];
+            const bool there = page >= 0 && page < c.pages;
+            gone = __ballot(!there);
+            pages = ((uint32_t)(there ? page : 0) * (uint32_t)c.heads + (uint32_t)head) << c.page_log2;
         };
         ask_pages(from);
 
@@ -372,15 +399,18 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
         const bool valid = line < nlines;
         const int seg_line = block * X::LINES + (valid ? line : 0);
         const int token = sg.token + seg_line / pl.group, q_head = head * pl.group + seg_line % pl.group;
-        u32x4_kv q[QF];
+        u32x4_kv q[X::Q_LDS ? 1 : QF];
+        uint8_t *const q_own = lds.pool + X::TILES + (FEW ? 0 : wave * 32 * ROW) + k_read;
         {
             const uint16_t *src = a.q + (int64_t)token * a.q_ld + (int64_t)q_head * DIM + half * 8;
             const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
             for (int f = 0; f < QF; ++f) {
-                q[f] = *reinterpret_cast<const u32x4_kv *>(src + f * 16);
+                u32x4_kv x = *reinterpret_cast<const u32x4_kv *>(src + f * 16);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) q[f][e] = valid ? q[f][e] ^ flip : 0u;
+                for (int e = 0; e < 4; ++e) x[e] = valid ? x[e] ^ flip : 0u;
+                if constexpr (X::Q_LDS) *reinterpret_cast<u32x4_kv *>(q_own + (k_turn ^ (f << 5))) = x;
+                else q[f] = x;
             }
         }
         // The last slot that any line sees: a row's later tokens see more.
@@ -395,44 +425,40 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
         const int n = sg.end - sg.start;
         const float room = RAISE + (n > 1 ? 32 - __builtin_clz(n - 1) : 0);
 
-        // Where a tile's slots are: the numbers of the pools' rows that this lane loads a piece of.  Tells
-        // whether a slot's page is not there (in its place the pool's first page is read, and its slots left out).
+        // Where a tile's slots are: for each row that this lane loads a piece of, its place in a pool counted in pieces.
+        // Tells whether a slot's page is not there.
         uint32_t rows[LOADS];
         auto find = [&](int tile) {
-            const int slot0 = from + tile * X::STEP, slot = min(slot0 + lane % TILE, c.cap - 1);
-            if ((min(slot0 + TILE, c.cap) - 1 >> c.page_log2) - pages_at >= 64) ask_pages(slot0);
-            const int32_t page = __shfl(pages, (slot >> c.page_log2) - pages_at);
-            const bool there = page >= 0 && page < c.pages;
-            const uint32_t mine = (((uint32_t)(there ? page : 0) * (uint32_t)c.heads + (uint32_t)head) << c.page_log2) +
-                                  (uint32_t)(slot & ((1 << c.page_log2) - 1));
+            const int slot0 = min(from + tile * X::STEP, c.cap - 1), slot1 = min(slot0 + TILE, c.cap) - 1;
+            if ((slot1 >> c.page_log2) - pages_at >= 64) ask_pages(slot0);
+            const int at0 = (slot0 >> c.page_log2) - pages_at, at1 = (slot1 >> c.page_log2) - pages_at;
+            const int slot = min(slot0 + lane % TILE, slot1);
+            const uint32_t mine = (__shfl(pages, (slot >> c.page_log2) - pages_at) + (slot & ((1 << c.page_log2) - 1))) * PIECES;
             int row = first_row + fill_row;
             again(row);
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) rows[i] = __shfl(mine, row + i * X::ROWS);
-            return (bool)__any(!there);
+            return (gone << (63 - at1) >> (63 - at1 + at0)) != 0;
         };
         // 8-bit values come through registers, to be widened.
         u32x2_kv raw[FP8 ? 2 : 1][LOADS];
-        auto load = [&](bool values, uint8_t *to_lds) {
+        auto load = [&](bool values, int to_own) {
             int fill = values ? v_fill : k_fill;
             again(fill);
             const uint8_t *pool = values ? c.v : c.k;
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) {
-                const int at = values ? fill ^ (v_way(i * X::ROWS) << 6) : fill ^ (2 * i << 4);
-                if constexpr (FP8) {
-                    raw[values][i] = *reinterpret_cast<const u32x2_kv *>(pool + (int64_t)rows[i] * DIM + (at >> 1));
-                } else {
-                    load_to_lds(pool + (int64_t)rows[i] * ROW + at, to_lds + i * 1024);
-                }
+                const uint64_t at = rows[i] + (uint32_t)(values ? fill ^ (v_way(i * X::ROWS) << 2) : fill ^ 2 * i);
+                if constexpr (FP8) raw[values][i] = *reinterpret_cast<const u32x2_kv *>(pool + (at << 3));
+                else load_to_lds(pool + (at << 4), own_at + to_own + i * 1024);
             }
         };
-        auto widen = [&](bool values, uint8_t *to_lds) {
+        auto widen = [&](bool values, int to_own) {
             if constexpr (FP8) {
 #pragma unroll
                 for (int i = 0; i < LOADS; ++i) {
                     const u32x2_kv w = raw[values][i];
-                    *reinterpret_cast<u32x4_kv *>(to_lds + i * 1024 + lane * 16) =
+                    *reinterpret_cast<u32x4_kv *>(own + to_own + i * 1024 + lane * 16) =
                         u32x4_kv{fp8_widened<0>(w[0]), fp8_widened<1>(w[0]), fp8_widened<0>(w[1]), fp8_widened<1>(w[1])};
                 }
             }
@@ -447,35 +473,30 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
         f32x16_sh s[SUBS];
         u32x4_kv p[SUBS][2];
 
-        // S^T of the tile whose keys are at kb; four operands are under way while four are used.
+        // S^T of the tile whose keys are at kb; the keys AHEAD products on are under way.
+        constexpr int AHEAD = 3;
         auto scores = [&](const uint8_t *kb) {
             int row = k_read, way = k_turn;
             again(row, way);
-            constexpr int GROUPS = SUBS * QF / 4;
-            u32x4_kv kf[2][4];
-            auto ask = [&](int g) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int f = (g * 4 + i) % QF, b = (g * 4 + i) / QF;
-                    kf[g & 1][i] = *reinterpret_cast<const u32x4_kv *>(kb + b * 32 * ROW + row + (way ^ (f << 5)));
-                }
+            constexpr int PRODUCTS = SUBS * QF;
+            u32x4_kv kf[AHEAD + 1], qf[X::Q_LDS ? AHEAD + 1 : 1];
+            auto ask = [&](int j) {
+                kf[j % (AHEAD + 1)] = *reinterpret_cast<const u32x4_kv *>(kb + j / QF * 32 * ROW + row + (way ^ (j % QF << 5)));
+                if constexpr (X::Q_LDS) qf[j % (AHEAD + 1)] = *reinterpret_cast<const u32x4_kv *>(q_own + (way ^ (j % QF << 5)));
             };
-            ask(0);
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) ask(j);
 #pragma unroll
             for (int b = 0; b < SUBS; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
 #pragma unroll
-            for (int g = 0; g < GROUPS; ++g) {
-                if (g + 1 < GROUPS) ask(g + 1);
+            for (int j = 0; j < PRODUCTS; ++j) {
+                if (j + AHEAD < PRODUCTS) ask(j + AHEAD);
                 in_order();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int f = (g * 4 + i) % QF, b = (g * 4 + i) / QF;
-                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_sh, kf[g & 1][i]),
-                                                                   __builtin_bit_cast(bf16x8_sh, q[f]), s[b], 0, 0, 0);
-                }
-                in_order();
+                const u32x4_kv &qj = X::Q_LDS ? qf[j % (AHEAD + 1)] : q[j % QF];
+                s[j / QF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_sh, kf[j % (AHEAD + 1)]),
+                                                                    __builtin_bit_cast(bf16x8_sh, qj), s[j / QF], 0, 0, 0);
             }
         };
         // The running maximum, for the scores in s; gives what the weights are taken from.  `first` is the
@@ -520,39 +541,34 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
             part = __builtin_amdgcn_fdot2_f32_bf16(two, bf16x2_sh{(__bf16)1.f, (__bf16)1.f}, part, false);
             p[b][i / 4][i % 4] = __builtin_bit_cast(uint32_t, two);
         };
-        // O^T with the values at vb.  Step k is 16 slots: while its products run, the next step's values are
-        // under way and its weights are worked out.
+        // O^T with the values at vb.  Step k is 16 slots: while its products run, the values three products on are under
+        // way and the next step's weights are worked out.
         auto add = [&](const uint8_t *vb, float ref) {
             int row = v_read, way = v_turn;
             again(row, way);
-            constexpr int STEPS = 2 * SUBS;
-            u32x4_kv vf[2][DB];
-            auto ask = [&](int k) {
-#pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    const uint8_t *src = vb + 16 * k * ROW + row + ((d << 6) ^ way);
-                    const u32x2_kv v0 = transposed(src), v1 = transposed(src + 8 * ROW);
-                    vf[k & 1][d] = u32x4_kv{v0[0], v0[1], v1[0], v1[1]};
-                }
+            constexpr int PRODUCTS = 2 * SUBS * DB;
+            u32x4_kv vf[AHEAD + 1];
+            auto ask = [&](int j) {
+                const uint8_t *src = vb + 16 * (j / DB) * ROW + row + ((j % DB << 6) ^ way);
+                const u32x2_kv v0 = transposed(src), v1 = transposed(src + 8 * ROW);
+                vf[j % (AHEAD + 1)] = u32x4_kv{v0[0], v0[1], v1[0], v1[1]};
             };
             float part = 0.f;  // of a long sum, so that few roundings follow each other
-            ask(0);
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) ask(j);
             in_order();
 #pragma unroll
             for (int i = 0; i < 4; ++i) weigh(0, i, ref, part);
 #pragma unroll
-            for (int k = 0; k < STEPS; ++k) {
-                if (k + 1 < STEPS) ask(k + 1);
+            for (int j = 0; j < PRODUCTS; ++j) {
+                const int k = j / DB, d = j % DB;
+                if (j + AHEAD < PRODUCTS) ask(j + AHEAD);
                 in_order();
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_sh, vf[j % (AHEAD + 1)]),
+                                                               __builtin_bit_cast(bf16x8_sh, p[k / 2][k % 2]), o[d], 0, 0, 0);
+                if (j + DB < PRODUCTS)
 #pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_sh, vf[k & 1][d]),
-                                                                   __builtin_bit_cast(bf16x8_sh, p[k / 2][k % 2]), o[d], 0, 0, 0);
-                    if (k + 1 < STEPS)
-#pragma unroll
-                        for (int i = d * 4 / DB; i < (d + 1) * 4 / DB; ++i) weigh((k + 1) / 2, (k + 1) % 2 * 4 + i, ref, part);
-                    in_order();
-                }
+                    for (int i = d * 4 / DB; i < (d + 1) * 4 / DB; ++i) weigh((k + 1) / 2, (k + 1) % 2 * 4 + i, ref, part);
             }
             sum += part;
         };
@@ -647,37 +663,38 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
         if constexpr (FEW) {
             // Keys and values in turn: as soon as a tile's keys are used the next one's are asked for, and so
             // the values, so that one half or the other is always under way.
-            uint8_t *kb = own, *vb = own + TILE * ROW;
+            constexpr int KEYS = 0, VALUES = TILE * ROW;
+            const uint8_t *kb = own + KEYS, *vb = own + VALUES;
             bool missing = false;
             if (tiles > 0) {
                 missing = find(0);
-                load(false, kb);
-                load(true, vb);
+                load(false, KEYS);
+                load(true, VALUES);
             }
             auto step = [&](int t, auto all) {
                 const int first = from + t * X::STEP;
-                if constexpr (FP8) widen(false, kb);
+                if constexpr (FP8) widen(false, KEYS);
                 else wait_loads<LOADS>();  // the values
                 scores(kb);
                 wait_lds();
                 uint32_t there[SUBS];
                 if constexpr (!decltype(all)::value) present(first, missing, there);
                 missing = find(min(t + 1, tiles - 1));
-                if constexpr (FP8) widen(true, vb);
-                load(false, kb);
+                if constexpr (FP8) widen(true, VALUES);
+                load(false, KEYS);
                 const float ref = raise(first, all, there);
                 if constexpr (!FP8) wait_loads<LOADS>();  // the next keys
                 if constexpr (decltype(all)::value) add(vb, ref);
                 else add_with_care(vb, first, there, ref);
                 wait_lds();
-                load(true, vb);
+                load(true, VALUES);
             };
             int t = 0;
             for (; t < tiles && from + t * X::STEP + TILE <= least && !missing; ++t) step(t, std::true_type());
             for (; t < tiles; ++t) step(t, std::false_type());
             if constexpr (!FP8) wait_loads<0>();
         } else {
-            auto buf = [&](int t) { return own + (t & 1) * 2 * TILE * ROW; };
+            auto buf = [&](int t) { return (t & 1) * 2 * TILE * ROW; };
             auto fill = [&](int t) {
                 load(false, buf(t) + first_row * ROW);
                 load(true, buf(t) + (TILE + first_row) * ROW);
@@ -700,16 +717,19 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
             }
             // Each wave meets the others once a tile, whichever of the two loops it is in.
             auto step = [&](int t, auto all) {
-                if (t + 1 < tiles) fill(t + 1);
                 const int first = from + t * X::STEP;
-                const uint8_t *kb = buf(t), *vb = kb + TILE * ROW;
+                const uint8_t *kb = own + buf(t), *vb = kb + TILE * ROW;
+                const bool some = decltype(all)::value || first < most;
+                uint32_t there[SUBS];
+                if constexpr (!decltype(all)::value)
+                    if (some) present(first, missing, there);
+                // 8-bit values take registers that the scores' operands need
+                if (!FP8 && t + 1 < tiles) fill(t + 1);
+                if (some) scores(kb);
+                if (FP8 && t + 1 < tiles) fill(t + 1);
                 if constexpr (decltype(all)::value) {
-                    scores(kb);
-                    add(vb, raise(first, all, nullptr));
-                } else if (first < most) {
-                    uint32_t there[SUBS];
-                    present(first, missing, there);
-                    scores(kb);
+                    add(vb, raise(first, all, there));
+                } else if (some) {
                     add_with_care(vb, first, there, raise(first, all, there));
                 }
                 if (t + 1 < tiles) {
@@ -789,7 +809,7 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
 
 template <int DIM, bool FP8>
 __global__ __launch_bounds__(SHARED_THREADS, DIM > 128 ? 1 : 2) void kv_shared_kernel(KvCache c, KvAttendShared a, SharedPlan pl) {
-    __shared__ __align__(16) uint8_t pool[std::max(Shape<DIM, true>::BYTES, Shape<DIM, false>::BYTES)];
+    __shared__ __align__(16) uint8_t pool[std::max(Shape<DIM, FP8, true>::BYTES, Shape<DIM, FP8, false>::BYTES)];
     __shared__ float s_m[SHARED_WAVES][32], s_l[SHARED_WAVES][32];
     const SharedLds lds = {pool, s_m, s_l};
     const int n0 = pl.shares[0], n1 = pl.shares[1], b = (int)blockIdx.x;
@@ -798,7 +818,7 @@ __global__ __launch_bounds__(SHARED_THREADS, DIM > 128 ? 1 : 2) void kv_shared_k
     // Workgroups go to the 8 XCDs in turn; neighbouring shares, which meet the same keys, go to one.
     int share = b - n0;
     if (!which) share = b % 8 * (n0 / 8) + min(b % 8, n0 % 8) + b / 8;
-    if (pl.side[which].lines == Shape<DIM, true>::LINES) attend_share<DIM, FP8, true>(c, a, pl, which, share, which ? n1 : n0, lds);
+    if (pl.side[which].lines == Shape<DIM, FP8, true>::LINES) attend_share<DIM, FP8, true>(c, a, pl, which, share, which ? n1 : n0, lds);
     else attend_share<DIM, FP8, false>(c, a, pl, which, share, which ? n1 : n0, lds);
 }
 
@@ -814,77 +834,85 @@ __global__ __launch_bounds__(JOIN_THREADS) void kv_shared_join_kernel(KvCache c,
     const int token = line / a.q_heads, qh = line % a.q_heads, head = qh / pl.group;
     const int2 of = pl.tokens[token];
     if (of.x < 0) return;
-    // Where the line's parts are, RANGES ranges at a time: of each the part that begins it and those that
-    // workgroups begin within it, 3 at the most: a share is more than half of a piece.
-    constexpr int RANGES = 64, MOST_PARTS = 4;
-    __shared__ uint32_t s_place[JOIN_THREADS / 64][RANGES * MOST_PARTS];
+    // Where the line's parts are, 32 ranges of each side at a time, side 0 in lanes 0..31: of each range the part that
+    // begins it and those that workgroups begin within it, 3 at the most, a share being more than half of a piece.
+    constexpr int RANGES = 32, MOST_PARTS = 4;
+    __shared__ uint32_t s_place[JOIN_THREADS / 64][2 * RANGES * MOST_PARTS];
     uint32_t *const places = s_place[threadIdx.x >> 6];
+    const int which = lane / RANGES, seg = which ? of.x : of.y;
+    const auto &side = which ? pl.side[1] : pl.side[0];
+    Segment sg = {0, 0, 0, 0, 0, 0, 0, 0};
+    int64_t first = 0, place0 = 0, all_cost = 1;
+    int shares = 0, reach = 1, block = 0, in = 0;
+    if (seg >= 0) {
+        sg = side.segment[seg];
+        all_cost = side.cost[side.segments];
+        first = side.cost[seg];
+        place0 = side.parts[seg];
+        shares = pl.shares[which];
+        reach = pl.reach[which];
+        in = (token - sg.token) * pl.group + qh % pl.group;
+        block = in / side.lines;
+        first += head * head_cost(sg);
+        place0 += (int64_t)pl.wgs * side.lines + (int64_t)head * sg.ranges * sg.tokens * pl.group + in;
+        if (sg.tokens == 0) sg.ranges = 0;
+    }
+    const int most = max(__builtin_amdgcn_readlane(sg.ranges, 0), __builtin_amdgcn_readlane(sg.ranges, RANGES));
     float top = NEG_INF, total = 0.f;
     f32x4_sh x = {0.f, 0.f, 0.f, 0.f};
+    for (int r0 = 0; r0 < most; r0 += RANGES) {
+        const int r = r0 + lane % RANGES, len = min(reach, sg.chunks - r * reach);
+        int n = 0, w0 = 0;
+        if (r < sg.ranges) {
+            const int64_t at = first + (int64_t)r * sg.blocks * (reach + START) + (int64_t)block * (len + START) + START;
+            w0 = owner_of(at, all_cost, shares);
+            n = min(owner_of(at + len - 1, all_cost, shares) - w0 + 1, MOST_PARTS);
+        }
+        const int upto = wave_running_sum(n), parts = __builtin_amdgcn_readlane(upto, 63);
+        if (__any(which && sg.start == 0 && sg.ranges == 1 && n == 1)) return;  // written already
+        for (int i = 0; i < n; ++i)
+            places[upto - n + i] = (uint32_t)which << 31 | (uint32_t)(i == 0 ? place0 + (int64_t)r * sg.tokens * pl.group
+                                                                             : (int64_t)(w0 + i) * side.lines + in % side.lines);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        constexpr int AHEAD = 8;
+        for (int i0 = 0; i0 < parts; i0 += AHEAD * SLICES) {
+            f32x4_sh y[AHEAD];
+            float2 ml[AHEAD];
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        const int seg = which ? of.x : of.y;
-        if (seg < 0) continue;
-        const auto &side = pl.side[which];
-        const Segment sg = side.segment[seg];
-        if (sg.chunks == 0) continue;
-        const int64_t all_cost = side.cost[side.segments];
-        const int shares = pl.shares[which], reach = pl.reach[which];
-        const int in = (token - sg.token) * pl.group + qh % pl.group, block = in / side.lines;
-        const int64_t first = side.cost[seg] + head * head_cost(sg);
-        const int64_t place0 = (int64_t)pl.wgs * side.lines + side.parts[seg] + (int64_t)head * sg.ranges * sg.tokens * pl.group + in;
-        for (int r0 = 0; r0 < sg.ranges; r0 += RANGES) {
-            const int r = r0 + lane, len = min(reach, sg.chunks - r * reach);
-            int n = 0, w0 = 0;
-            if (r < sg.ranges) {
-                const int64_t at = first + (int64_t)r * sg.blocks * (reach + START) + (int64_t)block * (len + START) + START;
-                w0 = owner_of(at, all_cost, shares);
-                n = min(owner_of(at + len - 1, all_cost, shares) - w0 + 1, MOST_PARTS);
+            for (int k = 0; k < AHEAD; ++k) {
+                const uint32_t at = places[min(i0 + k * SLICES + lane / LANES, parts - 1)];
+                const auto &from = at >> 31 ? pl.side[1] : pl.side[0];
+                const int64_t place = at & 0x7FFFFFFFu;
+                ml[k] = *reinterpret_cast<const float2 *>(from.ml + 2 * place);
+                y[k] = *reinterpret_cast<const f32x4_sh *>(from.o + place * DIM + d);
             }
-            const int upto = wave_running_sum(n), parts = __builtin_amdgcn_readlane(upto, 63);
-            if (which && sg.start == 0 && sg.ranges == 1 && parts == 1) return;  // written already
-            for (int i = 0; i < n; ++i)
-                places[upto - n + i] = (uint32_t)(i == 0 ? place0 + (int64_t)r * sg.tokens * pl.group
-                                                         : (int64_t)(w0 + i) * side.lines + in % side.lines);
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-            // The largest m of them, and their sums and results from there.
             float up = top;
-            for (int i = lane; i < parts; i += 64) up = fmaxf(up, side.ml[2 * (int64_t)places[i]]);
 #pragma unroll
-            for (int s = 1; s < 64; s <<= 1) up = fmaxf(up, __shfl_xor(up, s));
+            for (int k = 0; k < AHEAD; ++k) up = fmaxf(up, ml[k].x);
             const float fade = top == up ? 1.f : __builtin_amdgcn_exp2f(top - up);
             total *= fade;
             x *= fade;
             top = up;
-            constexpr int AHEAD = 4;
-            for (int i0 = 0; i0 < parts; i0 += AHEAD * SLICES) {
-                f32x4_sh y[AHEAD];
-                float m[AHEAD], l[AHEAD];
 #pragma unroll
-                for (int k = 0; k < AHEAD; ++k) {
-                    const int64_t at = places[min(i0 + k * SLICES + lane / LANES, parts - 1)];
-                    m[k] = side.ml[2 * at];
-                    l[k] = side.ml[2 * at + 1];
-                    y[k] = *reinterpret_cast<const f32x4_sh *>(side.o + at * DIM + d);
+            for (int k = 0; k < AHEAD; ++k)
+                if (i0 + k * SLICES + lane / LANES < parts) {
+                    const float f = ml[k].x == top ? 1.f : __builtin_amdgcn_exp2f(ml[k].x - top);
+                    total += ml[k].y * f;
+                    x += y[k] * (f * PART_BY);
                 }
-#pragma unroll
-                for (int k = 0; k < AHEAD; ++k)
-                    if (i0 + k * SLICES + lane / LANES < parts) {
-                        const float f = m[k] == top ? 1.f : __builtin_amdgcn_exp2f(m[k] - top);
-                        total += l[k] * f;
-                        x += y[k] * (f * PART_BY);
-                    }
-            }
-            __builtin_amdgcn_wave_barrier();
         }
+        __builtin_amdgcn_wave_barrier();
     }
 #pragma unroll
     for (int s = LANES; s < 64; s <<= 1) {
-        total += __shfl_xor(total, s);
+        const float other = __shfl_xor(top, s), up = fmaxf(top, other);
+        const float f = top == up ? 1.f : __builtin_amdgcn_exp2f(top - up), g = other == up ? 1.f : __builtin_amdgcn_exp2f(other - up);
+        total = total * f + __shfl_xor(total, s) * g;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] += __shfl_xor(x[e], s);
+        for (int e = 0; e < 4; ++e) x[e] = x[e] * f + __shfl_xor(x[e], s) * g;
+        top = up;
     }
     x *= total == 0.f ? 0.f : 1.f / (total * PART_BY);
     if (total == 0.f) x = f32x4_sh{0.f, 0.f, 0.f, 0.f};  // nothing to attend to, whatever the values are
@@ -897,7 +925,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void kv_shared_join_kernel(KvCache c,
 // The plan, its scratch laid out from `base`; returns the bytes (-1: more than a launch takes).
 static int64_t shared_plan(const KvCache &c, int q_heads, int tokens, int groups, int max_len, int cu_count, uint8_t *base,
                            SharedPlan *pl) {
-    if ((c.pages * c.heads) >> (32 - c.page_log2)) return -1;  // a pool's rows are counted in 32 bits
+    if ((((int64_t)c.pages * c.heads) << c.page_log2) * (c.dim / 8) >> 32) return -1;  // a pool's pieces are counted in 32 bits
     pl->group = q_heads / c.heads;
     const int64_t lines = (int64_t)tokens * pl->group, chunks = (max_len + UNIT - 1) / UNIT;
     int64_t units = 0;
