@@ -72,10 +72,10 @@ struct SharedPlan {
     int32_t *reach;              // [2] units of a piece at most
     struct Side {                // 0: the groups' prefixes, 1: the rows' own slots
         int lines, segments;     // lines of a block
-        int64_t places;          // that there are
+        uint32_t places;         // that there are
         Segment *segment;        // [segments]
-        int64_t *cost;           // [segments + 1] of the segments before each
-        int64_t *parts;          // [segments] places of parts before each segment's
+        uint32_t *cost;          // [segments + 1] of the segments before each
+        uint32_t *parts;         // [segments] places of parts before each segment's
         float *ml, *o;           // [place][2] and [place][dim]: a line's part, its m and sum, and o.  First the
                                  // [wgs][lines] that a workgroup begins within a piece, then a place for
                                  // each piece's beginning: by segment, head, range and line
@@ -85,8 +85,20 @@ struct SharedPlan {
 // A piece costs as much as its units and START more, for the loads that depend on each other at its
 // start and the result at its end (few lines: 7 us beside 3 for a unit; many: 8 beside 5).
 constexpr int START = 2;
-__device__ __forceinline__ int64_t head_cost(const Segment &s) {
-    return (int64_t)s.blocks * (s.chunks + START * s.ranges);
+__device__ __forceinline__ uint32_t head_cost(const Segment &s) {
+    return (uint32_t)s.blocks * (uint32_t)(s.chunks + START * s.ranges);
+}
+
+// All of a call's units, costs and places are below 2^31 (shared_plan); sums that say otherwise, of rows that are not
+// what they should be, stay there.
+constexpr uint32_t MOST = 0x7FFFFFFFu;
+__device__ __forceinline__ uint32_t plus(uint32_t a, uint32_t b) { return min(a + b, MOST); }  // of two up to MOST
+__device__ __forceinline__ uint32_t bounded(uint64_t x) { return (uint32_t)min(x, (uint64_t)MOST); }
+
+// a * b / c, rounded down, of a below 2^31, b below 2^20 and c not 0: in fp64 exact, as no quotient is closer to the next
+// whole number than 1 / c.  (A 64-bit division takes some 200 instructions.)
+__device__ __forceinline__ uint32_t share_of(uint32_t a, uint32_t b, uint32_t c, double less = 0.0) {
+    return (uint32_t)(((double)a * b - less) / c);
 }
 
 __device__ __forceinline__ int bounded(int x, int low, int high) { return min(max(x, low), high); }
@@ -94,33 +106,49 @@ __device__ __forceinline__ int first_token(const KvAttendShared &a, int row) {
     return a.cu ? bounded(a.cu[row], 0, a.tokens) : row;
 }
 
-// The number of entries 1 .. n of an ascending array that are at most x.
-__device__ __forceinline__ int ended_by(const int32_t *ends, int n, int x) {
-    int low = 0, high = n;
-    while (low < high) {
-        const int mid = (low + high) / 2;
-        if (ends[mid + 1] <= x) low = mid + 1;
-        else high = mid;
+// Entries 1 .. n of an ascending array, the ends of n runs that begin at entry 0: every stride-th of them in LDS, so
+// that a search waits for memory only within a stride.
+constexpr int PLAN_THREADS = 256;
+constexpr int ENDS = 1024;
+struct Ends {
+    const int32_t *runs;
+    int n, stride, kept;
+    int32_t *s_ends;
+    __device__ __forceinline__ void keep(const int32_t *r, int count, int32_t *lds) {
+        runs = r;
+        n = r ? count : 0;
+        stride = max((n + ENDS - 1) / ENDS, 1);
+        kept = (n + stride - 1) / stride;
+        s_ends = lds;
+        for (int i = threadIdx.x; i < kept; i += PLAN_THREADS) s_ends[i] = runs[min((i + 1) * stride, n)];
     }
-    return low;
-}
-__device__ __forceinline__ int group_of(const KvAttendShared &a, int row) {
-    if (!a.group_rows) return -1;
-    const int g = ended_by(a.group_rows, a.groups, row);
-    return g < a.groups && a.group_rows[g] <= row ? g : -1;
-}
+    // The run that x is in, or -1.
+    __device__ __forceinline__ int find(int x) const {
+        int low = 0, high = kept;  // the first kept end past x
+        while (low < high) {
+            const int mid = (low + high) / 2;
+            if (s_ends[mid] <= x) low = mid + 1;
+            else high = mid;
+        }
+        if (low == kept) return -1;
+        low *= stride;
+        high = min(low + stride, n) - 1;
+        while (low < high) {
+            const int mid = (low + high) / 2;
+            if (runs[mid + 1] <= x) low = mid + 1;
+            else high = mid;
+        }
+        return runs[low] <= x ? low : -1;
+    }
+};
 
 // The sums of N numbers over the workgroup's threads up to this one, in x, and over all.
 template <int N, int THREADS>
-__device__ __forceinline__ void add_up(int64_t (&x)[N], int64_t (&all)[N], int64_t (*s_wave)[N]) {
+__device__ __forceinline__ void add_up(uint32_t (&x)[N], uint32_t (&all)[N], uint32_t (*s_wave)[N]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int64_t y = __shfl_up(x[i], d);
-            if (lane >= d) x[i] += y;
-        }
+    for (int i = 0; i < N; ++i)
+        x[i] = (uint32_t)wave_running((int32_t)x[i], 0, [](int32_t a, int32_t b) { return (int32_t)plus((uint32_t)a, (uint32_t)b); });
     if (lane == 63)
 #pragma unroll
         for (int i = 0; i < N; ++i) s_wave[wave][i] = x[i];
@@ -130,38 +158,42 @@ __device__ __forceinline__ void add_up(int64_t (&x)[N], int64_t (&all)[N], int64
         all[i] = 0;
 #pragma unroll
         for (int w = 0; w < THREADS / 64; ++w) {
-            if (w < wave) x[i] += s_wave[w][i];
-            all[i] += s_wave[w][i];
+            if (w < wave) x[i] = plus(x[i], s_wave[w][i]);
+            all[i] = plus(all[i], s_wave[w][i]);
         }
     }
     __syncthreads();
 }
 
 // The last workgroup of the launch divides the work, the others find each token's row.
-constexpr int PLAN_THREADS = 256;
 __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c, KvAttendShared a, SharedPlan pl) {
-    __shared__ int64_t s_wave[PLAN_THREADS / 64][4];
+    __shared__ uint32_t s_wave[PLAN_THREADS / 64][4];
+    __shared__ int32_t s_ends[2][ENDS];
     const int tid = threadIdx.x;
+    Ends groups, rows;
+    groups.keep(a.group_rows, a.groups, s_ends[0]);
     if (blockIdx.x + 1 < gridDim.x) {
+        rows.keep(a.cu, c.rows, s_ends[1]);
+        __syncthreads();
         const int token = blockIdx.x * PLAN_THREADS + tid;
         if (token >= a.tokens) return;
         int row = token, behind = 0;
         if (a.cu) {
-            row = ended_by(a.cu, c.rows, token);
-            if (row < c.rows && a.cu[row] <= token) behind = min(a.cu[row + 1], a.tokens) - 1 - token;
-            else row = -1;
+            row = rows.find(token);
+            if (row >= 0) behind = min(a.cu[row + 1], a.tokens) - 1 - token;
         }
-        pl.tokens[token] = int2{row, row < 0 ? -1 : group_of(a, row)};
+        pl.tokens[token] = int2{row, row < 0 ? -1 : groups.find(row)};
         pl.sees[token] = row < 0 ? 0 : max(kv_len(a.lens, row, a.max_len) - behind, 0);
         return;
     }
+    __syncthreads();
     // A strip of segments for each thread; with no more segments than threads its one stays in registers.
     auto of = [&](int which, int s) {
         Segment x = {s, 0, 0, 0, 0, 0, 0, 0};
         if (which) {
-            const int g = group_of(a, s), t1 = first_token(a, s + 1);
-            x.token = first_token(a, s);
-            x.tokens = max(t1 - x.token, 0);
+            const int t0 = first_token(a, s), t1 = first_token(a, s + 1), g = groups.find(s);
+            x.token = t0;
+            x.tokens = max(t1 - t0, 0);
             x.start = g < 0 ? 0 : bounded(a.prefix[g], 0, a.max_len);
             x.end = kv_len(a.lens, s, a.max_len);
         } else {
@@ -177,75 +209,75 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
     };
     int s0[2], s1[2];
     Segment mine[2];
-    int64_t sums[4] = {0, 0, 0, 0}, all[4];  // units and blocks of both sides
+    uint32_t sums[4] = {0, 0, 0, 0}, all[4];  // units and blocks of both sides
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         const int n = pl.side[which].segments, strip = (n + PLAN_THREADS - 1) / PLAN_THREADS;
         s0[which] = min(tid * strip, n);
         s1[which] = min(s0[which] + strip, n);
         for (int s = s0[which]; s < s1[which]; ++s) {
-            mine[which] = of(which, s);
-            sums[which] += (int64_t)c.heads * mine[which].blocks * mine[which].chunks;
-            sums[2 + which] += (int64_t)c.heads * mine[which].blocks;
+            const Segment x = mine[which] = of(which, s);
+            const uint32_t blocks = bounded((uint64_t)c.heads * x.blocks);
+            sums[which] = plus(sums[which], bounded((uint64_t)blocks * x.chunks));
+            sums[2 + which] = plus(sums[2 + which], blocks);
         }
     }
     add_up<4, PLAN_THREADS>(sums, all, s_wave);
     // Workgroups by the sides' cost, a unit of many lines taking 5/4 of the time of one of few; one for each
     // unit at the most, and one for a side that has any.
-    int64_t shares[2] = {all[0], all[1]};
-    if (all[0] + all[1] > pl.wgs) {
-        const int64_t w0 = (all[0] + START * all[2]) * (pl.side[0].lines > 32 ? 5 : 4);
-        const int64_t w1 = (all[1] + START * all[3]) * (pl.side[1].lines > 32 ? 5 : 4);
-        const int64_t n0 = (pl.wgs * w0 + (w0 + w1) / 2) / (w0 + w1);
-        shares[0] = min(min(max(n0, (int64_t)(w0 > 0)), (int64_t)pl.wgs - (w1 > 0)), all[0]);
+    uint32_t shares[2] = {all[0], all[1]};
+    if (plus(all[0], all[1]) > (uint32_t)pl.wgs) {
+        const double w0 = ((double)all[0] + START * (double)all[2]) * (pl.side[0].lines > 32 ? 5 : 4);
+        const double w1 = ((double)all[1] + START * (double)all[3]) * (pl.side[1].lines > 32 ? 5 : 4);
+        const uint32_t n0 = (uint32_t)(pl.wgs * w0 / (w0 + w1) + 0.5);
+        shares[0] = min(min(max(n0, (uint32_t)(w0 > 0)), (uint32_t)pl.wgs - (w1 > 0)), all[0]);
         shares[1] = min(pl.wgs - shares[0], all[1]);
     }
     // A piece has no more units than an equal share: the blocks of a range of slots then go to
     // neighbouring workgroups, which meet its keys and values at about the same time.
     int reach[2];
-    auto places_of = [&](int which, const Segment &x) {
-        return (int64_t)((x.chunks + reach[which] - 1) / reach[which]) * x.tokens * pl.group * c.heads;
-    };
-    int64_t next[4] = {0, 0, 0, 0};  // places and costs of both sides
+    auto ranges_of = [&](int which, const Segment &x) { return x.chunks ? (x.chunks - 1) / reach[which] + 1 : 0; };
+    auto places_of = [&](const Segment &x) { return bounded((uint64_t)x.ranges * c.heads * ((uint64_t)x.tokens * pl.group)); };
+    auto cost_of = [&](const Segment &x) { return bounded((uint64_t)c.heads * x.blocks * (uint64_t)(x.chunks + START * x.ranges)); };
+    uint32_t next[4] = {0, 0, 0, 0};  // places and costs of both sides
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-        reach[which] = shares[which] ? (int)((all[which] + shares[which] - 1) / shares[which]) : 1;
+        reach[which] = shares[which] ? (int)((all[which] - 1) / shares[which] + 1) : 1;
         if (tid == 0) {
             pl.shares[which] = (int)shares[which];
             pl.reach[which] = reach[which];
         }
         const bool one = s1[which] - s0[which] <= 1;
         for (int s = s0[which]; s < s1[which]; ++s) {
-            const Segment x = one ? mine[which] : of(which, s);
-            next[which] += places_of(which, x);
-            next[2 + which] += (int64_t)c.heads * x.blocks * (x.chunks + START * ((x.chunks + reach[which] - 1) / reach[which]));
+            if (!one) mine[which] = of(which, s);
+            mine[which].ranges = ranges_of(which, mine[which]);
+            next[which] = plus(next[which], places_of(mine[which]));
+            next[2 + which] = plus(next[2 + which], cost_of(mine[which]));
         }
     }
-    int64_t own[4] = {next[0], next[1], next[2], next[3]};
+    const uint32_t own[4] = {next[0], next[1], next[2], next[3]};
     add_up<4, PLAN_THREADS>(next, all, s_wave);
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         const auto &side = pl.side[which];
-        int64_t place = next[which] - own[which], cost = next[2 + which] - own[2 + which];
+        uint32_t place = next[which] - own[which], cost = next[2 + which] - own[2 + which];
         const bool one = s1[which] - s0[which] <= 1;
         for (int s = s0[which]; s < s1[which]; ++s) {
-            Segment x = one ? mine[which] : of(which, s);
-            x.ranges = (x.chunks + reach[which] - 1) / reach[which];
+            if (!one) {
+                mine[which] = of(which, s);
+                mine[which].ranges = ranges_of(which, mine[which]);
+            }
+            Segment x = mine[which];
             side.parts[s] = place;
             side.cost[s] = cost;
-            place += places_of(which, x);
-            cost += (int64_t)c.heads * head_cost(x);
+            place = plus(place, places_of(x));
+            cost = plus(cost, cost_of(x));
             // Rows that say they have the same tokens would need more places than there are: no lines then.
-            if (place + (int64_t)pl.wgs * side.lines > side.places) x.tokens = 0;
+            if (plus(place, (uint32_t)(pl.wgs * side.lines)) > side.places) x.tokens = 0;
             side.segment[s] = x;
         }
         if (tid == 0) side.cost[side.segments] = all[2 + which];
     }
-}
-
-// The share that a place among all costs is in.
-__device__ __forceinline__ int owner_of(int64_t at, int64_t all, int shares) {
-    return (int)(((at + 1) * shares - 1) / all);
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
@@ -334,10 +366,10 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int half = lane >> 5, col = lane & 31;
     const auto &side = pl.side[which];
-    const int64_t all_cost = side.cost[side.segments];
-    const int reach = pl.reach[which];
-    int64_t u = all_cost * share / shares;
-    const int64_t u1 = all_cost * (share + 1) / shares;
+    const uint32_t all_cost = side.cost[side.segments];
+    const int most_reach = pl.reach[which];
+    uint32_t u = share_of(all_cost, share, shares);
+    const uint32_t u1 = share_of(all_cost, share + 1, shares);
     int seg = 0;  // segments that end at or before u
     for (int at = 0; at < side.segments; at += 64) {
         const int n = __popcll(__ballot(at + lane < side.segments && side.cost[at + lane + 1] <= u));
@@ -364,14 +396,15 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
 
     for (;;) {  // a piece, or a part of one: chunks [c0, c1) of one block of a segment's lines
         const Segment sg = side.segment[seg];
-        const int64_t in = u - side.cost[seg], per_head = head_cost(sg), per_range = (int64_t)sg.blocks * (reach + START);
+        const int reach = min(most_reach, sg.chunks);
+        const uint32_t in = u - side.cost[seg], per_head = head_cost(sg), per_range = (uint32_t)sg.blocks * (uint32_t)(reach + START);
         const int head = (int)(in / per_head);
-        int64_t rest = in % per_head;
-        const int range = (int)min(rest / per_range, (int64_t)sg.ranges - 1);
-        rest -= range * per_range;
+        const uint32_t in_head = in - head * per_head;
+        const int range = min((int)(in_head / per_range), sg.ranges - 1);
+        const uint32_t in_range = in_head - range * per_range;
         const int len = min(reach, sg.chunks - range * reach);
-        const int block = (int)(rest / (len + START)), off = (int)(rest % (len + START));
-        const int take = (int)min(u1 - u, (int64_t)(len + START - off));
+        const int block = (int)(in_range / (uint32_t)(len + START)), off = (int)in_range - block * (len + START);
+        const int take = (int)min(u1 - u, (uint32_t)(len + START - off));
         const int c0 = range * reach + max(off - START, 0), c1 = range * reach + max(off + take - START, 0);
         const bool begins = off <= START;
         u += take;
@@ -747,9 +780,9 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
         sum += __shfl_xor(sum, 32);
         const bool sole = which && sg.start == 0 && c1 - c0 == sg.chunks;
         const float v_by = FP8 ? c.v_scale[head] : 1.f;
-        const int64_t part0 = begins ? (int64_t)pl.wgs * X::LINES + side.parts[seg] +
-                                           ((int64_t)head * sg.ranges + range) * sg.tokens * pl.group + block * X::LINES
-                                     : (int64_t)share * X::LINES;
+        const uint32_t part0 = begins ? pl.wgs * X::LINES + side.parts[seg] + (head * sg.ranges + range) * sg.tokens * pl.group +
+                                            block * X::LINES
+                                      : share * X::LINES;
         auto store = [&](int ln, int d, f32x4_sh x, float mm, float total) {  // dims d..d+3 of a line of the block
             const int sl = block * X::LINES + ln;
             const int64_t t = sg.token + sl / pl.group, qh = head * pl.group + sl % pl.group;
@@ -826,7 +859,7 @@ __global__ __launch_bounds__(SHARED_THREADS, DIM > 128 ? 1 : 2) void kv_shared_k
 constexpr int JOIN_THREADS = 256;
 constexpr float PART_BY = 1.f / (1 << 20);  // each part's weights sum to 1 at the most, and there are fewer than 2^20 of them
 template <int DIM>
-__global__ __launch_bounds__(JOIN_THREADS) void kv_shared_join_kernel(KvCache c, KvAttendShared a, SharedPlan pl) {
+__global__ __launch_bounds__(JOIN_THREADS, 6) void kv_shared_join_kernel(KvCache c, KvAttendShared a, SharedPlan pl) {
     constexpr int LANES = DIM / 4, SLICES = 64 / LANES;  // lanes of a part, four dims each, and parts taken side by side
     const int lane = threadIdx.x & 63, d = lane % LANES * 4;
     const int line = __builtin_amdgcn_readfirstlane((int)((int64_t)blockIdx.x * (JOIN_THREADS / 64) + (threadIdx.x >> 6)));
@@ -842,7 +875,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void kv_shared_join_kernel(KvCache c,
     const int which = lane / RANGES, seg = which ? of.x : of.y;
     const auto &side = which ? pl.side[1] : pl.side[0];
     Segment sg = {0, 0, 0, 0, 0, 0, 0, 0};
-    int64_t first = 0, place0 = 0, all_cost = 1;
+    uint32_t first = 0, place0 = 0, all_cost = 1;
     int shares = 0, reach = 1, block = 0, in = 0;
     if (seg >= 0) {
         sg = side.segment[seg];
@@ -850,11 +883,11 @@ __global__ __launch_bounds__(JOIN_THREADS) void kv_shared_join_kernel(KvCache c,
         first = side.cost[seg];
         place0 = side.parts[seg];
         shares = pl.shares[which];
-        reach = pl.reach[which];
+        reach = min(pl.reach[which], max(sg.chunks, 1));
         in = (token - sg.token) * pl.group + qh % pl.group;
         block = in / side.lines;
         first += head * head_cost(sg);
-        place0 += (int64_t)pl.wgs * side.lines + (int64_t)head * sg.ranges * sg.tokens * pl.group + in;
+        place0 += pl.wgs * side.lines + head * sg.ranges * sg.tokens * pl.group + in;
         if (sg.tokens == 0) sg.ranges = 0;
     }
     const int most = max(__builtin_amdgcn_readlane(sg.ranges, 0), __builtin_amdgcn_readlane(sg.ranges, RANGES));
@@ -864,19 +897,20 @@ __global__ __launch_bounds__(JOIN_THREADS) void kv_shared_join_kernel(KvCache c,
         const int r = r0 + lane % RANGES, len = min(reach, sg.chunks - r * reach);
         int n = 0, w0 = 0;
         if (r < sg.ranges) {
-            const int64_t at = first + (int64_t)r * sg.blocks * (reach + START) + (int64_t)block * (len + START) + START;
-            w0 = owner_of(at, all_cost, shares);
-            n = min(owner_of(at + len - 1, all_cost, shares) - w0 + 1, MOST_PARTS);
+            // the shares that its first and its last unit are in
+            const uint32_t at = first + r * sg.blocks * (reach + START) + block * (len + START) + START;
+            w0 = (int)share_of(at + 1, shares, all_cost, 1.0);
+            n = min((int)share_of(at + len, shares, all_cost, 1.0) - w0 + 1, MOST_PARTS);
         }
         const int upto = wave_running_sum(n), parts = __builtin_amdgcn_readlane(upto, 63);
         if (__any(which && sg.start == 0 && sg.ranges == 1 && n == 1)) return;  // written already
         for (int i = 0; i < n; ++i)
-            places[upto - n + i] = (uint32_t)which << 31 | (uint32_t)(i == 0 ? place0 + (int64_t)r * sg.tokens * pl.group
-                                                                             : (int64_t)(w0 + i) * side.lines + in % side.lines);
+            places[upto - n + i] = (uint32_t)which << 31 | (i == 0 ? place0 + r * sg.tokens * pl.group
+                                                                   : (w0 + i) * side.lines + in % side.lines);
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        constexpr int AHEAD = 8;
+        constexpr int AHEAD = 4;
         for (int i0 = 0; i0 < parts; i0 += AHEAD * SLICES) {
             f32x4_sh y[AHEAD];
             float2 ml[AHEAD];
@@ -935,7 +969,7 @@ static int64_t shared_plan(const KvCache &c, int q_heads, int tokens, int groups
         const int64_t mean = side.segments ? (lines + side.segments - 1) / side.segments : 0;  // lines of a segment
         side.lines = mean <= 32 ? 32 : 128;
         if (side.segments) units += (lines / side.lines + side.segments) * c.heads * chunks;
-        if (units > INT32_MAX) return -1;
+        if (units > INT32_MAX / (1 + START)) return -1;
     }
     // As many workgroups as run at once: two on a CU, one at 256 dims (registers, LDS).
     pl->wgs = (int)std::min<int64_t>(units, (int64_t)cu_count * (c.dim > 128 ? 1 : 2));
@@ -953,13 +987,13 @@ static int64_t shared_plan(const KvCache &c, int q_heads, int tokens, int groups
     for (int which = 0; which < 2; ++which) {
         auto &side = pl->side[which];
         side.segment = (Segment *)take((int64_t)side.segments * sizeof(Segment));
-        side.cost = (int64_t *)take(((int64_t)side.segments + 1) * 8);
-        side.parts = (int64_t *)take((int64_t)side.segments * 8);
+        side.cost = (uint32_t *)take(((int64_t)side.segments + 1) * 4);
+        side.parts = (uint32_t *)take((int64_t)side.segments * 4);
         // A line for each that a workgroup may begin within a piece; and by segment, head, range and line: with
         // ranges no longer than needed, a block more for each workgroup than the lines there are.
-        side.places = side.segments ? 2 * (int64_t)pl->wgs * side.lines + (int64_t)tokens * q_heads : 0;
-        side.ml = (float *)take(side.places * 8);
-        side.o = (float *)take(side.places * c.dim * 4);
+        side.places = side.segments ? 2u * pl->wgs * side.lines + (uint32_t)tokens * q_heads : 0;
+        side.ml = (float *)take((int64_t)side.places * 8);
+        side.o = (float *)take((int64_t)side.places * c.dim * 4);
     }
     return at;
 }
