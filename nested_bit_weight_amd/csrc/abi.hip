@@ -684,6 +684,9 @@ nbw_status nbw_verify_drafts(const nbw_verify_args *args, void *stream) {
         !aligned(g.accepted, 4) || !aligned(g.next, 4) || !aligned(g.workspace, 256))
         return NBW_EALIGN;
     if (!g.workspace || g.workspace_bytes < need) return NBW_ESCRATCH;
+    int cus = 0;
+    const nbw_status st = cu_count(&cus);
+    if (st != NBW_OK) return st;
     nbw::VerifyDrafts a = {};
     a.target = g.target;
     a.draft = g.draft;
@@ -699,7 +702,7 @@ nbw_status nbw_verify_drafts(const nbw_verify_args *args, void *stream) {
     a.accepted = g.accepted;
     a.next = g.next;
     a.ws = (uint8_t *)g.workspace;
-    const hipError_t e = nbw::launch_verify_drafts(a, (hipStream_t)stream);
+    const hipError_t e = nbw::launch_verify_drafts(a, cus, (hipStream_t)stream);
     return e == hipSuccess ? NBW_OK : hip_failed(e);
 }
 

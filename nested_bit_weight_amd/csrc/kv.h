@@ -109,7 +109,7 @@ hipError_t launch_kv_reserve(const KvCache &c, const KvReserve &a, int cu_count,
 int64_t kv_attend_shared_workspace_bytes(const KvCache &c, int q_heads, int tokens, int groups, int max_len, int cu_count);
 hipError_t launch_kv_attend_shared(const KvCache &c, const KvAttendShared &a, int cu_count, hipStream_t stream);
 int64_t verify_drafts_workspace_bytes(int rows, int vocab);
-hipError_t launch_verify_drafts(const VerifyDrafts &a, hipStream_t stream);
+hipError_t launch_verify_drafts(const VerifyDrafts &a, int cu_count, hipStream_t stream);
 
 typedef uint32_t u32x2_kv __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_kv __attribute__((ext_vector_type(4)));

@@ -4,12 +4,12 @@
 // one, and the first that is refused ends the row's run.  u q < p in fp64 is exact,
 // the product of two numbers of 24 bits having 48.
 //
-// The next token is found in the running sum of one line's weights, max(p - q, 0) or p,
-// which a first launch cuts into chunks of 4096 and sums, each chunk in a workgroup of
-// its own whatever the rows; a second one, a workgroup for each row, finds the chunk
-// that the sum passes u times the whole in, and then the place in it.  All sums
-// are in fp64 and in a fixed order: of 128 thousand weights they are off by about
-// 1e-14, so that the place is the exact one but for one draw in 1e9.
+// The next token is found in the running sum of one line's weights, max(p - q, 0) or p.
+// A first launch sums spans of 1024 of them, a wave a span, or a few one after the other where
+// there are more than run at once; a second one, a wave a row, finds the span in which the sum passes
+// u times the whole, and then the place in it.  Nothing is shared between waves, so there is no barrier.
+// Sums are in fp64 and in a fixed order: of 128 thousand weights they are off by about 1e-14, so that the
+// place is the exact one but for one draw in 1e9.
 //
 // Bound: memory, one line a row, or two where a draft was refused; for few rows the
 // chain of loads (cu -> tokens -> p, q -> line) and the second launch.
@@ -20,9 +20,8 @@
 namespace nbw {
 
 constexpr int VERIFY_THREADS = 256;
-constexpr int VERIFY_WAVES = VERIFY_THREADS / 64;
-constexpr int EACH = 16;                        // weights of a thread
-constexpr int SPAN = VERIFY_THREADS * EACH;     // weights of a chunk
+constexpr int EACH = 16;         // weights of a lane
+constexpr int SPAN = 64 * EACH;  // of a wave
 
 // A row's lines.
 struct Lines {
@@ -40,24 +39,7 @@ __device__ __forceinline__ float prob(const void *p, int64_t i) {
     else return ((const float *)p)[i];
 }
 
-// Eight bf16 or four fp32 numbers from an address that is only theirs to be aligned by.
-template <bool BF16>
-struct Pack {
-    static constexpr int N = BF16 ? 8 : 4;
-    u32x4_kv w;
-    __device__ __forceinline__ void load(const void *p, int64_t i) {
-        __builtin_memcpy(&w, (const uint8_t *)p + i * (BF16 ? 2 : 4), 16);
-    }
-    __device__ __forceinline__ float get(int i) const {
-        if constexpr (BF16) return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
-        else return __uint_as_float(w[i]);
-    }
-};
-
-// What a difference counts as a weight.
-__device__ __forceinline__ double weight(double x) { return x > 0.0 && x < __builtin_inf() ? x : 0.0; }
-
-// How many of a row's drafts stand; the same in all lanes of the wave that asks.
+// How many of a row's drafts stand; the same in all lanes.
 template <bool BF16>
 __device__ __forceinline__ int standing(const VerifyDrafts &a, const Lines &l) {
     const int lane = threadIdx.x & 63;
@@ -79,39 +61,71 @@ __device__ __forceinline__ int standing(const VerifyDrafts &a, const Lines &l) {
     return l.count - 1;
 }
 
-// The weights of elements [at, at + N) of a line, w, and what they are where no difference
-// is above 0, p; elements past the vocabulary count as 0.
+// A line's weights.
 template <bool BF16>
 struct Line {
     const void *target, *draft;  // draft: null if p alone counts
     int64_t p0, q0;              // the line's first element in each
     int vocab, out;              // the one token whose weight is 0 (-1: none)
 
-    template <int N, class F>
-    __device__ __forceinline__ void weights(int at, F use) const {
-        if (at + N <= vocab) {
-            Pack<BF16> p[N / Pack<BF16>::N], q[N / Pack<BF16>::N];
+    static constexpr int N = BF16 ? 8 : 4;  // in 16 bytes
+
+    // What p - q counts as: itself, in fp64, if it is positive and finite, else 0.
+    __device__ __forceinline__ double weight(int i, float p, float q) const {
+        const float inf = __builtin_inff();
+        const bool counts = p > q && p < inf && q > -inf && i != out;
+        return (double)(counts ? p : 0.f) - (double)(counts ? q : 0.f);
+    }
+    __device__ __forceinline__ static float get(const u32x4_kv &w, int i) {
+        if constexpr (BF16) return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+        else return __uint_as_float(w[i]);
+    }
+    // use(p, q) for a lane's elements of a whole span, a wave's loads side by side.
+    template <bool DRAFT, class F>
+    __device__ __forceinline__ void raw(int64_t at, F use) const {
+        constexpr int PACKS = EACH / N, SIZE = BF16 ? 2 : 4;
+        u32x4_kv p[PACKS], q[PACKS];  // at any address: no more aligned than an element
+        const int64_t i = at + (threadIdx.x & 63) * N;
 #pragma unroll
-            for (int k = 0; k < N / Pack<BF16>::N; ++k) {
-                p[k].load(target, p0 + at + k * Pack<BF16>::N);
-                if (draft) q[k].load(draft, q0 + at + k * Pack<BF16>::N);
+        for (int k = 0; k < PACKS; ++k) {
+            __builtin_memcpy(&p[k], (const uint8_t *)target + (p0 + i + k * 64 * N) * SIZE, 16);
+            if (DRAFT) __builtin_memcpy(&q[k], (const uint8_t *)draft + (q0 + i + k * 64 * N) * SIZE, 16);
+        }
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k)
+#pragma unroll
+            for (int e = 0; e < N; ++e) use(get(p[k], e), DRAFT ? get(q[k], e) : 0.f);
+    }
+    // use(i, weight) for a lane's weights of span `span`, in packs of N: pack k begins at
+    // k * STEP + lane * FIRST within the span.
+    template <int STEP, int FIRST, class F>
+    __device__ __forceinline__ void weights(int span, F use) const {
+        constexpr int PACKS = EACH / N;
+        const int64_t at = (int64_t)span * SPAN;
+        const int mine = (threadIdx.x & 63) * FIRST;
+        if (at + SPAN <= vocab) {
+            u32x4_kv p[PACKS], q[PACKS];  // at any address: no more aligned than an element
+#pragma unroll
+            for (int k = 0; k < PACKS; ++k) {
+                const int64_t i = at + mine + k * STEP;
+                __builtin_memcpy(&p[k], (const uint8_t *)target + (p0 + i) * (BF16 ? 2 : 4), 16);
+                if (draft) __builtin_memcpy(&q[k], (const uint8_t *)draft + (q0 + i) * (BF16 ? 2 : 4), 16);
+                else q[k] = u32x4_kv{0, 0, 0, 0};
             }
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const double x = p[i / Pack<BF16>::N].get(i % Pack<BF16>::N);
-                const double y = draft ? (double)q[i / Pack<BF16>::N].get(i % Pack<BF16>::N) : 0.0;
-                use(i, at + i == out ? 0.0 : weight(x - y), weight(x));
-            }
+            for (int k = 0; k < PACKS; ++k)
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    use(k * N + e, weight((int)at + mine + k * STEP + e, get(p[k], e), get(q[k], e)));
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                double x = 0.0, y = 0.0;
-                if (at + i < vocab) {
-                    x = prob<BF16>(target, p0 + at + i);
-                    if (draft) y = prob<BF16>(draft, q0 + at + i);
+            for (int k = 0; k < PACKS; ++k)
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const int64_t i = at + mine + k * STEP + e;
+                    const bool there = i < vocab;
+                    use(k * N + e, there ? weight((int)i, prob<BF16>(target, p0 + i), draft ? prob<BF16>(draft, q0 + i) : 0.f) : 0.0);
                 }
-                use(i, at + i == out ? 0.0 : weight(x - y), weight(x));
-            }
         }
     }
 };
@@ -123,192 +137,172 @@ __device__ __forceinline__ Line<BF16> line_of(const VerifyDrafts &a, const Lines
             refused && !a.draft ? a.ids[t + 1] : -1};
 }
 
-__device__ __forceinline__ double wave_sum64(double x) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
-    return x;
+// Sums of fp64 over this lane and those before it, in register-to-register steps (as wave_running).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double from_lane64(double x) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)from_lane<CTRL, ROWS>(0, (int32_t)(uint32_t)b), hi = (uint32_t)from_lane<CTRL, ROWS>(0, (int32_t)(b >> 32));
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-
-// The first launch: the sums of each row's chunks, of the weights and of p.
+__device__ __forceinline__ double running_sum(double x) {
+    x += from_lane64<0x111, 0xF>(x);
+    x += from_lane64<0x112, 0xF>(x);
+    x += from_lane64<0x114, 0xF>(x);
+    x += from_lane64<0x118, 0xF>(x);
+    x += from_lane64<0x142, 0xA>(x);
+    return x + from_lane64<0x143, 0xC>(x);
+}
+__device__ __forceinline__ double at_lane(double x, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, lane), hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 template <bool BF16>
-__global__ __launch_bounds__(VERIFY_THREADS) void verify_sums_kernel(VerifyDrafts a, int chunks, double *sums) {
-    __shared__ double s_w[VERIFY_WAVES], s_p[VERIFY_WAVES];
-    const int row = blockIdx.x / chunks, chunk = blockIdx.x % chunks, tid = threadIdx.x, wave = tid >> 6;
-    const Lines l = lines_of(a, row);
-    double w = 0.0, p = 0.0;
-    if (l.count > 0) {
-        const int stands = standing<BF16>(a, l);
-        if (chunk == 0 && tid == 0) a.accepted[row] = stands;
-        const Line<BF16> line = line_of<BF16>(a, l, stands);
-        constexpr int N = Pack<BF16>::N;
-#pragma unroll
-        for (int k = 0; k < EACH / N; ++k) {
-            // a wave's loads side by side
-            const int64_t at = (int64_t)chunk * SPAN + k * (VERIFY_THREADS * N) + tid * N;
-            if (at < a.vocab)
-                line.template weights<N>((int)at, [&](int, double x, double y) {
-                    w += x;
-                    p += y;
-                });
-        }
-    } else if (chunk == 0 && tid == 0) {
-        a.accepted[row] = 0;
+__device__ __forceinline__ double span_sum(const Line<BF16> &line, int span) {
+    double w = 0.0;
+    const int64_t at = (int64_t)span * SPAN;
+    // In a whole span without the token left out a weight is max(p - q, 0), a NaN giving 0; only should the sum not
+    // be finite is each looked at.  (The arithmetic of a weight decides: 256 lines of 160001 25 us with
+    // all its comparisons, 19 so.)
+    if (at + SPAN <= line.vocab && (line.out < at || line.out >= at + SPAN)) {
+        if (line.draft) line.template raw<true>(at, [&](float p, float q) { w += fmax((double)p - (double)q, 0.0); });
+        else line.template raw<false>(at, [&](float p, float) { w += (double)fmaxf(p, 0.f); });
+        w = at_lane(running_sum(w), 63);
+        if (w < __builtin_inf()) return w;
+        w = 0.0;
     }
-    w = wave_sum64(w);
-    p = wave_sum64(p);
-    if ((tid & 63) == 0) {
-        s_w[wave] = w;
-        s_p[wave] = p;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        for (int i = 1; i < VERIFY_WAVES; ++i) {
-            w += s_w[i];
-            p += s_p[i];
-        }
-        sums[2 * (int64_t)blockIdx.x] = w;
-        sums[2 * (int64_t)blockIdx.x + 1] = p;
-    }
+    // a wave's loads side by side
+    line.template weights<64 * Line<BF16>::N, Line<BF16>::N>(span, [&](int, double x) { w += x; });
+    return at_lane(running_sum(w), 63);
 }
 
-// The sum of x over the workgroup's threads before this one, and over all.
-struct Before {
-    double mine, all;
-};
-__device__ __forceinline__ Before before_mine(double x, double *s_wave) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    double upto = x;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double y = __shfl_up(upto, d);
-        if (lane >= d) upto += y;
+// The first launch: the sums of each row's spans, `run` of them to a wave.
+template <bool BF16>
+__global__ __launch_bounds__(VERIFY_THREADS) void verify_sums_kernel(VerifyDrafts a, int spans, int run, double *sums) {
+    const int runs = (spans + run - 1) / run;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (VERIFY_THREADS / 64) + (threadIdx.x >> 6)));
+    const int row = wave / runs, first = wave % runs * run;
+    if (row >= a.rows) return;
+    const bool one = (threadIdx.x & 63) == 0;
+    const Lines l = lines_of(a, row);
+    if (l.count <= 0) {
+        if (first == 0 && one) a.accepted[row] = 0;
+        return;
     }
-    if (lane == 63) s_wave[wave] = upto;
-    double mine = __shfl_up(upto, 1);
-    if (lane == 0) mine = 0.0;
-    __syncthreads();
-    double lead = 0.0, all = 0.0;
-    for (int w = 0; w < VERIFY_WAVES; ++w) {
-        if (w < wave) lead += s_wave[w];
-        all += s_wave[w];
+    const int stands = standing<BF16>(a, l);
+    if (first == 0 && one) a.accepted[row] = stands;
+    const Line<BF16> line = line_of<BF16>(a, l, stands);
+    for (int s = first; s < min(first + run, spans); ++s) {
+        const double w = span_sum(line, s);
+        if (one) sums[(int64_t)row * spans + s] = w;
     }
-    __syncthreads();
-    return {lead + mine, all};
 }
 
 // The second launch: each row's next token.
 template <bool BF16>
-__global__ __launch_bounds__(VERIFY_THREADS) void verify_next_kernel(VerifyDrafts a, int chunks, const double *sums) {
-    __shared__ double s_wave[VERIFY_WAVES];
-    __shared__ int s_first, s_last;
-    __shared__ double s_before;
-    const int row = blockIdx.x, tid = threadIdx.x;
+__global__ __launch_bounds__(64) void verify_next_kernel(VerifyDrafts a, int spans, const double *sums) {
+    const int row = blockIdx.x, lane = threadIdx.x;
+    const double *const mine = sums + (int64_t)row * spans;
+    constexpr int KEPT = 4;  // a lane keeps the sums of so many spans: of 64 of them each
+    double kept[KEPT];
+#pragma unroll
+    for (int i = 0; i < KEPT; ++i) kept[i] = i * 64 + lane < spans ? mine[i * 64 + lane] : 0.0;
+    const int stands = a.accepted[row];
     const Lines l = lines_of(a, row);
     if (l.count <= 0) {
-        if (tid == 0) a.next[row] = -1;
+        if (lane == 0) a.next[row] = -1;
         return;
     }
-    Line<BF16> line = line_of<BF16>(a, l, a.accepted[row]);
-    const double *mine = sums + 2 * (int64_t)row * chunks;
-    if (tid == 0) {
-        s_first = INT32_MAX;
-        s_last = -1;
-        s_before = 0.0;
-    }
-    // A thread has a run of chunks.
-    const int run = (chunks + VERIFY_THREADS - 1) / VERIFY_THREADS, c0 = min(tid * run, chunks), c1 = min(c0 + run, chunks);
-    double x = 0.0;
-    for (int c = c0; c < c1; ++c) x += mine[2 * c];
-    Before b = before_mine(x, s_wave);
-    int of = 0;
-    if (b.all == 0.0) {  // no difference above 0: p itself
-        of = 1;
-        line.draft = nullptr;
-        line.out = -1;
-        x = 0.0;
-        for (int c = c0; c < c1; ++c) x += mine[2 * c + 1];
-        b = before_mine(x, s_wave);
-    }
-    if (b.all == 0.0) {
-        if (tid == 0) a.next[row] = -1;
-        return;
-    }
+    Line<BF16> line = line_of<BF16>(a, l, stands);
     const float u32 = a.u[l.first + l.count - 1];
-    const double u = u32 > 0.f ? (u32 < 1.f ? (double)u32 : 1.0) : 0.0, goal = u * b.all;
-    // The first chunk whose end is past the goal; should rounding leave none, the last that has any weight.
-    double at = b.mine;
-    for (int c = c0; c < c1; ++c) {
-        const double own = mine[2 * c + of];
-        if (own > 0.0) {
-            atomicMax(&s_last, c);
-            if (at + own > goal) {
-                atomicMin(&s_first, c);
-                break;
-            }
-        }
-        at += own;
-    }
-    __syncthreads();
-    const int chunk = s_first != INT32_MAX ? s_first : s_last;
-    if (chunk >= c0 && chunk < c1) {
-        at = b.mine;
-        for (int c = c0; c < chunk; ++c) at += mine[2 * c + of];
-        s_before = at;
-    }
-    __syncthreads();
-    const double lead = s_before;
-    if (tid == 0) {
-        s_first = INT32_MAX;
-        s_last = -1;
-    }
-    // The same in the chunk: a thread has EACH weights in a row.
-    const int64_t first = (int64_t)chunk * SPAN + tid * EACH;
-    double w[EACH];
-    x = 0.0;
-    if (first < a.vocab) {
-        line.template weights<EACH>((int)first, [&](int i, double v, double) {
-            w[i] = v;
-            x += v;
-        });
-    } else {
+    const double u = u32 > 0.f ? (u32 < 1.f ? (double)u32 : 1.0) : 0.0;
+    bool again = false;  // no difference is above 0: p itself, whose sums are formed here
+    auto sums_from = [&](int s0) {  // 64 spans' sums from s0 on, one in each lane
+        if (!again) {
+            if (s0 < KEPT * 64) {
+                double x = 0.0;
 #pragma unroll
-        for (int i = 0; i < EACH; ++i) w[i] = 0.0;
-    }
-    b = before_mine(x, s_wave);
-    if (x > 0.0) {
-        at = lead + b.mine;
-        int pick = -1, last = -1;
-#pragma unroll
-        for (int i = 0; i < EACH; ++i) {
-            at += w[i];
-            if (w[i] > 0.0) {
-                last = i;
-                if (pick < 0 && at > goal) pick = i;
+                for (int i = 0; i < KEPT; ++i) x = i * 64 == s0 ? kept[i] : x;
+                return x;
             }
+            return s0 + lane < spans ? mine[s0 + lane] : 0.0;
         }
-        atomicMax(&s_last, (int)first + last);
-        if (pick >= 0) atomicMin(&s_first, (int)first + pick);
+        double x = 0.0;
+        for (int s = s0; s < min(s0 + 64, spans); ++s) {
+            const double w = span_sum(line, s);
+            x = s - s0 == lane ? w : x;
+        }
+        return x;
+    };
+    double all = 0.0;
+    for (int pass = 0; pass < 2 && all == 0.0; ++pass) {
+        if (pass == 1) {
+            again = true;
+            line.draft = nullptr;
+            line.out = -1;
+        }
+        for (int s0 = 0; s0 < spans; s0 += 64) all += at_lane(running_sum(sums_from(s0)), 63);
     }
-    __syncthreads();
-    if (tid == 0) a.next[row] = s_first != INT32_MAX ? s_first : s_last;
+    if (all == 0.0) {
+        if (lane == 0) a.next[row] = -1;
+        return;
+    }
+    const double goal = u * all;
+    // The first span whose end is past the goal; should rounding leave none, the last that has any weight.
+    int span = -1;
+    double lead = 0.0, before = 0.0;
+    for (int s0 = 0; s0 < spans; s0 += 64) {
+        const double x = sums_from(s0), upto = running_sum(x);
+        const unsigned long long some = __ballot(x > 0.0), past = __ballot(x > 0.0 && lead + upto > goal);
+        if (some) {
+            const int at = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some);
+            span = s0 + at;
+            before = lead + at_lane(upto - x, at);
+        }
+        if (past) break;
+        lead += at_lane(upto, 63);
+    }
+    // The same in the span, of which a lane has its weights in a row.
+    double w[EACH], x = 0.0;
+    line.template weights<Line<BF16>::N, EACH>(span, [&](int i, double v) {
+        w[i] = v;
+        x += v;
+    });
+    double at = before + (running_sum(x) - x);
+    int pick = -1, last = -1;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        at += w[i];
+        if (w[i] > 0.0) {
+            last = i;
+            if (pick < 0 && at > goal) pick = i;
+        }
+    }
+    const unsigned long long picked = __ballot(pick >= 0), some = __ballot(last >= 0);
+    const int from = picked ? __builtin_ctzll(picked) : 63 - __builtin_clzll(some);
+    if (lane == from) a.next[row] = span * SPAN + lane * EACH + (picked ? pick : last);
 }
 
-static int chunks_of(int vocab) { return (int)(((int64_t)vocab + SPAN - 1) / SPAN); }
+static int spans_of(int vocab) { return (int)(((int64_t)vocab + SPAN - 1) / SPAN); }
 
 int64_t verify_drafts_workspace_bytes(int rows, int vocab) {
-    if (!fits_launch((int64_t)rows * chunks_of(vocab), VERIFY_THREADS)) return -1;
-    return (int64_t)rows * chunks_of(vocab) * 16;
+    const int64_t spans = (int64_t)rows * spans_of(vocab);
+    return fits_launch(spans, 64) ? spans * 8 : -1;
 }
 
-hipError_t launch_verify_drafts(const VerifyDrafts &a, hipStream_t stream) {
-    const int chunks = chunks_of(a.vocab);
-    const dim3 grid((unsigned)((int64_t)a.rows * chunks)), rows((unsigned)a.rows), threads(VERIFY_THREADS);
+hipError_t launch_verify_drafts(const VerifyDrafts &a, int cu_count, hipStream_t stream) {
+    const int spans = spans_of(a.vocab);
+    // As many waves as run at once, 16 on a CU, each then with the same drafts to look at for several spans.
+    const int64_t most = (int64_t)cu_count * 16;
+    const int run = (int)std::min<int64_t>(spans, ((int64_t)a.rows * spans + most - 1) / most);
+    const int64_t waves = (int64_t)a.rows * ((spans + run - 1) / run);
+    const dim3 grid((unsigned)((waves + VERIFY_THREADS / 64 - 1) / (VERIFY_THREADS / 64))), threads(VERIFY_THREADS);
     if (a.bf16) {
-        hipLaunchKernelGGL(verify_sums_kernel<true>, grid, threads, 0, stream, a, chunks, (double *)a.ws);
-        hipLaunchKernelGGL(verify_next_kernel<true>, rows, threads, 0, stream, a, chunks, (const double *)a.ws);
+        hipLaunchKernelGGL(verify_sums_kernel<true>, grid, threads, 0, stream, a, spans, run, (double *)a.ws);
+        hipLaunchKernelGGL(verify_next_kernel<true>, dim3((unsigned)a.rows), dim3(64), 0, stream, a, spans, (const double *)a.ws);
     } else {
-        hipLaunchKernelGGL(verify_sums_kernel<false>, grid, threads, 0, stream, a, chunks, (double *)a.ws);
-        hipLaunchKernelGGL(verify_next_kernel<false>, rows, threads, 0, stream, a, chunks, (const double *)a.ws);
+        hipLaunchKernelGGL(verify_sums_kernel<false>, grid, threads, 0, stream, a, spans, run, (double *)a.ws);
+        hipLaunchKernelGGL(verify_next_kernel<false>, dim3((unsigned)a.rows), dim3(64), 0, stream, a, spans, (const double *)a.ws);
     }
     return hipGetLastError();
 }
