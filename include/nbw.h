@@ -535,7 +535,7 @@ typedef struct nbw_kv_reserve_args {
                                  give back (a prefix that other rows have too) */
     const int32_t *seen;      /* NULL (lens), or [rows]: position of the row's first new token */
     int32_t *free;            /* [free_size] numbers of the free pages, a stack: the last is taken first */
-    int64_t free_size;        /* 1..2^31 - 1: pages that can be free at once */
+    int64_t free_size;        /* 1..2^30: pages that can be free at once */
     const int32_t *count;     /* [1] free pages */
     int64_t max_tokens;       /* 0..2^24 - 2^13: places for tokens */
     int32_t *cu;              /* [rows + 1] */
@@ -605,6 +605,11 @@ typedef struct nbw_kv_attend_shared_args {
  * a NaN among the scores or values that a token sees gives NaN, and so does an
  * infinite value whose weight is 0.  What a token does not see has no part in
  * its result.  Tokens from cu[rows] on are left as they are.  Deterministic.
+ * Workspaces are as for nbw_kv_attend: two calls that may run at the same time
+ * have one each.  out does not overlap an input.
+ * Refused (NBW_EINVAL) is what its 32-bit numbers do not reach: a pool of
+ * 2^35 elements or more (64 GiB of bf16), and batches of more than some 7e8
+ * runs of 128 slots with 32 lines each, rows and groups counted at max_len.
  * Errors: as nbw_kv_attend. */
 nbw_status nbw_kv_attend_shared(const nbw_kvcache *cache, const nbw_kv_attend_shared_args *args, void *stream);
 

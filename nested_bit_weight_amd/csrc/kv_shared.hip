@@ -370,11 +370,11 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
     const int most_reach = pl.reach[which];
     uint32_t u = share_of(all_cost, share, shares);
     const uint32_t u1 = share_of(all_cost, share + 1, shares);
-    int seg = 0;  // segments that end at or before u
-    for (int at = 0; at < side.segments; at += 64) {
-        const int n = __popcll(__ballot(at + lane < side.segments && side.cost[at + lane + 1] <= u));
-        seg += n;
-        if (n < 64) break;
+    int seg = 0;  // segments that end at or before u: 64 places looked at together, then 64 between two of them
+    for (int high = side.segments; seg < high;) {
+        const int step = (high - seg + 63) / 64, at = seg + (lane + 1) * step;
+        seg += step * __popcll(__ballot(at <= high && side.cost[at] <= u));
+        high = min(seg + step - 1, high);
     }
 
     // A row of a tile has its pieces at places turned by the row's number s.  Keys, whose readers have 32 rows side by
@@ -452,7 +452,8 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
         const int tiles = to > from ? (to - from + X::STEP - 1) / X::STEP : 0;
         const int sees = valid ? min(pl.sees[token], to) : INT32_MAX;
         const int least = -wave_max(-sees), most = wave_max(valid ? sees : 0);
-        const float by = fabsf(a.scale) * 1.44269504088896340736f * (FP8 ? c.k_scale[head] : 1.f);
+        // (Not 0, which an infinite score would make a NaN of: what is smaller tells no two finite scores apart.)
+        const float by = fmaxf(fabsf(a.scale) * 1.44269504088896340736f * (FP8 ? c.k_scale[head] : 1.f), 0x1p-126f);
         // Weights are up to 2^RAISE, and as many meet the values as the segment has slots: times a
         // power of two, in their exponent, they sum to 1 at the most, and finite values cannot run over.
         const int n = sg.end - sg.start;
@@ -836,7 +837,8 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
         }
         if (u >= u1) return;
         meet();  // the pool and the sums are free
-        while (side.cost[seg + 1] <= u) ++seg;
+        for (int n = 64; n == 64; seg += n)  // past the segments without work
+            n = __popcll(__ballot(seg + lane < side.segments && side.cost[seg + lane + 1] <= u));
     }
 }
 
@@ -884,7 +886,8 @@ __global__ __launch_bounds__(JOIN_THREADS, 6) void kv_shared_join_kernel(KvCache
         place0 = side.parts[seg];
         shares = pl.shares[which];
         reach = min(pl.reach[which], max(sg.chunks, 1));
-        in = (token - sg.token) * pl.group + qh % pl.group;
+        // (Within the segment, whatever the runs of tokens say.)
+        in = bounded((token - sg.token) * pl.group + qh % pl.group, 0, max(sg.tokens * pl.group - 1, 0));
         block = in / side.lines;
         first += head * head_cost(sg);
         place0 += pl.wgs * side.lines + head * sg.ranges * sg.tokens * pl.group + in;
@@ -906,7 +909,7 @@ __global__ __launch_bounds__(JOIN_THREADS, 6) void kv_shared_join_kernel(KvCache
         if (__any(which && sg.start == 0 && sg.ranges == 1 && n == 1)) return;  // written already
         for (int i = 0; i < n; ++i)
             places[upto - n + i] = (uint32_t)which << 31 | (i == 0 ? place0 + r * sg.tokens * pl.group
-                                                                   : (w0 + i) * side.lines + in % side.lines);
+                                                                   : min(w0 + i, shares - 1) * side.lines + in % side.lines);
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
