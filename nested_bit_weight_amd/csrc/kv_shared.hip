@@ -70,6 +70,7 @@ struct SharedPlan {
     int32_t *sees;               // [tokens] slots that it sees
     int32_t *shares;             // [2] of the workgroups, those of each side
     int32_t *reach;              // [2] units of a piece at most
+    int32_t *whole;              // [2] whether shares end between pieces
     struct Side {                // 0: the groups' prefixes, 1: the rows' own slots
         int lines, segments;     // lines of a block
         uint32_t places;         // that there are
@@ -85,6 +86,8 @@ struct SharedPlan {
 // A piece costs as much as its units and START more, for the loads that depend on each other at its
 // start and the result at its end (few lines: 7 us beside 3 for a unit; many: 8 beside 5).
 constexpr int START = 2;
+constexpr float CUT = 2.f;
+constexpr float JOINED_MANY = 1.f / 22000, JOINED_FEW = 1.f / 13000;
 __device__ __forceinline__ uint32_t head_cost(const Segment &s) {
     return (uint32_t)s.blocks * (uint32_t)(s.chunks + START * s.ranges);
 }
@@ -100,6 +103,10 @@ __device__ __forceinline__ uint32_t bounded(uint64_t x) { return (uint32_t)min(x
 __device__ __forceinline__ uint32_t share_of(uint32_t a, uint32_t b, uint32_t c, double less = 0.0) {
     return (uint32_t)(((double)a * b - less) / c);
 }
+
+// A row's later blocks see more slots than its earlier ones, so they are taken in turn from its beginning and its end.
+__device__ __forceinline__ int block_of(int nth, int blocks) { return nth & 1 ? blocks - 1 - nth / 2 : nth / 2; }
+__device__ __forceinline__ int nth_of(int block, int blocks) { return block < (blocks + 1) / 2 ? 2 * block : 2 * (blocks - 1 - block) + 1; }
 
 __device__ __forceinline__ int bounded(int x, int low, int high) { return min(max(x, low), high); }
 __device__ __forceinline__ int first_token(const KvAttendShared &a, int row) {
@@ -142,9 +149,11 @@ struct Ends {
     }
 };
 
+constexpr int N_SUMS = 5;  // at a time
+
 // The sums of N numbers over the workgroup's threads up to this one, in x, and over all.
 template <int N, int THREADS>
-__device__ __forceinline__ void add_up(uint32_t (&x)[N], uint32_t (&all)[N], uint32_t (*s_wave)[N]) {
+__device__ __forceinline__ void add_up(uint32_t (&x)[N], uint32_t (&all)[N], uint32_t (*s_wave)[N_SUMS]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -167,8 +176,9 @@ __device__ __forceinline__ void add_up(uint32_t (&x)[N], uint32_t (&all)[N], uin
 
 // The last workgroup of the launch divides the work, the others find each token's row.
 __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c, KvAttendShared a, SharedPlan pl) {
-    __shared__ uint32_t s_wave[PLAN_THREADS / 64][4];
+    __shared__ uint32_t s_wave[PLAN_THREADS / 64][N_SUMS];
     __shared__ int32_t s_ends[2][ENDS];
+    __shared__ int s_longest[PLAN_THREADS / 64];
     const int tid = threadIdx.x;
     Ends groups, rows;
     groups.keep(a.group_rows, a.groups, s_ends[0]);
@@ -209,7 +219,8 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
     };
     int s0[2], s1[2];
     Segment mine[2];
-    uint32_t sums[4] = {0, 0, 0, 0}, all[4];  // units and blocks of both sides
+    int own_units = 0;  // the most of a row's own slots
+    uint32_t sums[5] = {0, 0, 0, 0, 0}, all[5];  // units and blocks of both sides, and tokens that see no prefix
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         const int n = pl.side[which].segments, strip = (n + PLAN_THREADS - 1) / PLAN_THREADS;
@@ -220,9 +231,16 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
             const uint32_t blocks = bounded((uint64_t)c.heads * x.blocks);
             sums[which] = plus(sums[which], bounded((uint64_t)blocks * x.chunks));
             sums[2 + which] = plus(sums[2 + which], blocks);
+            if (which) own_units = max(own_units, x.chunks);
+            if (which && x.start == 0) sums[4] = plus(sums[4], (uint32_t)x.tokens);
         }
     }
-    add_up<4, PLAN_THREADS>(sums, all, s_wave);
+    own_units = wave_max(own_units);
+    if ((tid & 63) == 0) s_longest[tid >> 6] = own_units;
+    add_up<5, PLAN_THREADS>(sums, all, s_wave);
+    int longest = 0;
+#pragma unroll
+    for (int w = 0; w < PLAN_THREADS / 64; ++w) longest = max(longest, s_longest[w]);
     // Workgroups by the sides' cost, a unit of many lines taking 5/4 of the time of one of few; one for each
     // unit at the most, and one for a side that has any.
     uint32_t shares[2] = {all[0], all[1]};
@@ -234,18 +252,25 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
         shares[1] = min(pl.wgs - shares[0], all[1]);
     }
     // A piece has no more units than an equal share: the blocks of a range of slots then go to
-    // neighbouring workgroups, which meet its keys and values at about the same time.
-    int reach[2];
-    auto ranges_of = [&](int which, const Segment &x) { return x.chunks ? (x.chunks - 1) / reach[which] + 1 : 0; };
+    // neighbouring workgroups, which meet its keys and values at about the same time.  Of rows' own slots the shares
+    // may be of whole pieces instead: they differ by up to a piece, but no line is cut, none that sees
+    // nothing else has to be joined, and no piece is begun twice.
+    const int reach[2] = {shares[0] ? (int)((all[0] - 1) / shares[0] + 1) : 1, shares[1] ? (int)((all[1] - 1) / shares[1] + 1) : 1};
+    const float shares1 = (float)max(shares[1], 1u), piece = (float)(longest + START);
+    const float takes = all[3] <= shares[1] ? piece : ((float)all[1] + START * (float)all[3]) / shares1 + piece;
+    const float cut = ((float)all[1] + START * ((float)all[3] + 0.5f * shares1)) / shares1 + START + CUT +
+                      (float)all[4] * pl.group * c.heads * (pl.side[1].lines > 32 ? JOINED_MANY : JOINED_FEW);
+    const int whole[2] = {0, longest <= reach[1] || all[3] <= shares[1] ? takes < cut : 0};
+    auto ranges_of = [&](int which, const Segment &x) { return x.chunks ? whole[which] ? 1 : (x.chunks - 1) / reach[which] + 1 : 0; };
     auto places_of = [&](const Segment &x) { return bounded((uint64_t)x.ranges * c.heads * ((uint64_t)x.tokens * pl.group)); };
     auto cost_of = [&](const Segment &x) { return bounded((uint64_t)c.heads * x.blocks * (uint64_t)(x.chunks + START * x.ranges)); };
-    uint32_t next[4] = {0, 0, 0, 0};  // places and costs of both sides
+    uint32_t next[4] = {0, 0, 0, 0}, next_all[4];  // places and costs of both sides
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-        reach[which] = shares[which] ? (int)((all[which] - 1) / shares[which] + 1) : 1;
         if (tid == 0) {
+            pl.whole[which] = whole[which];
             pl.shares[which] = (int)shares[which];
-            pl.reach[which] = reach[which];
+            pl.reach[which] = whole[which] ? max(reach[which], longest) : reach[which];
         }
         const bool one = s1[which] - s0[which] <= 1;
         for (int s = s0[which]; s < s1[which]; ++s) {
@@ -256,7 +281,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
         }
     }
     const uint32_t own[4] = {next[0], next[1], next[2], next[3]};
-    add_up<4, PLAN_THREADS>(next, all, s_wave);
+    add_up<4, PLAN_THREADS>(next, next_all, s_wave);
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         const auto &side = pl.side[which];
@@ -276,7 +301,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
             if (plus(place, (uint32_t)(pl.wgs * side.lines)) > side.places) x.tokens = 0;
             side.segment[s] = x;
         }
-        if (tid == 0) side.cost[side.segments] = all[2 + which];
+        if (tid == 0) side.cost[side.segments] = next_all[2 + which];
     }
 }
 
@@ -368,6 +393,7 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
     const auto &side = pl.side[which];
     const uint32_t all_cost = side.cost[side.segments];
     const int most_reach = pl.reach[which];
+    const bool whole = pl.whole[which];
     uint32_t u = share_of(all_cost, share, shares);
     const uint32_t u1 = share_of(all_cost, share + 1, shares);
     int seg = 0;  // segments that end at or before u: 64 places looked at together, then 64 between two of them
@@ -394,8 +420,15 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
     uint8_t *const own = lds.pool + (FEW ? wave * X::OWN : 0);
     const uint32_t own_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) void *)own);
 
-    for (;;) {  // a piece, or a part of one: chunks [c0, c1) of one block of a segment's lines
-        const Segment sg = side.segment[seg];
+    auto next_segment = [&] {  // past the ones without work
+        for (int n = 64; n == 64; seg += n)
+            n = __popcll(__ballot(seg + lane < side.segments && side.cost[seg + lane + 1] <= u));
+    };
+    // The piece that u is in: `nth` of the blocks of a head's range, whose pieces have `len` units, and how far in.
+    struct Piece {
+        int head, range, reach, len, nth, off;
+    };
+    auto piece_at = [&](const Segment &sg) {
         const int reach = min(most_reach, sg.chunks);
         const uint32_t in = u - side.cost[seg], per_head = head_cost(sg), per_range = (uint32_t)sg.blocks * (uint32_t)(reach + START);
         const int head = (int)(in / per_head);
@@ -403,8 +436,20 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
         const int range = min((int)(in_head / per_range), sg.ranges - 1);
         const uint32_t in_range = in_head - range * per_range;
         const int len = min(reach, sg.chunks - range * reach);
-        const int block = (int)(in_range / (uint32_t)(len + START)), off = (int)in_range - block * (len + START);
-        const int take = (int)min(u1 - u, (uint32_t)(len + START - off));
+        const int nth = (int)(in_range / (uint32_t)(len + START));
+        return Piece{head, range, reach, len, nth, (int)in_range - nth * (len + START)};
+    };
+    if (whole) {  // a piece that the share before has begun is its own
+        const Piece p = piece_at(side.segment[seg]);
+        if (p.off) u += p.len + START - p.off;
+        if (u >= u1) return;
+        next_segment();
+    }
+    for (;;) {  // a piece, or a part of one: chunks [c0, c1) of one block of a segment's lines
+        const Segment sg = side.segment[seg];
+        const auto [head, range, reach, len, nth, off] = piece_at(sg);
+        const int rest = len + START - off, take = whole ? rest : (int)min(u1 - u, (uint32_t)rest);
+        const int block = which ? block_of(nth, sg.blocks) : nth;
         const int c0 = range * reach + max(off - START, 0), c1 = range * reach + max(off + take - START, 0);
         const bool begins = off <= START;
         u += take;
@@ -837,8 +882,7 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
         }
         if (u >= u1) return;
         meet();  // the pool and the sums are free
-        for (int n = 64; n == 64; seg += n)  // past the segments without work
-            n = __popcll(__ballot(seg + lane < side.segments && side.cost[seg + lane + 1] <= u));
+        next_segment();
     }
 }
 
@@ -858,55 +902,74 @@ __global__ __launch_bounds__(SHARED_THREADS, DIM > 128 ? 1 : 2) void kv_shared_k
 }
 
 // The last launch: each line's parts, in a fixed order, by a wave.
-constexpr int JOIN_THREADS = 256;
+constexpr int JOIN_THREADS = 256, JOIN_WAVES = 24;  // of a workgroup, and of a CU
 constexpr float PART_BY = 1.f / (1 << 20);  // each part's weights sum to 1 at the most, and there are fewer than 2^20 of them
 template <int DIM>
-__global__ __launch_bounds__(JOIN_THREADS, 6) void kv_shared_join_kernel(KvCache c, KvAttendShared a, SharedPlan pl) {
+__global__ __launch_bounds__(JOIN_THREADS, JOIN_WAVES / 4) void kv_shared_join_kernel(KvCache c, KvAttendShared a, SharedPlan pl, int each) {
     constexpr int LANES = DIM / 4, SLICES = 64 / LANES;  // lanes of a part, four dims each, and parts taken side by side
     const int lane = threadIdx.x & 63, d = lane % LANES * 4;
-    const int line = __builtin_amdgcn_readfirstlane((int)((int64_t)blockIdx.x * (JOIN_THREADS / 64) + (threadIdx.x >> 6)));
-    if (line >= a.tokens * a.q_heads) return;
-    const int token = line / a.q_heads, qh = line % a.q_heads, head = qh / pl.group;
-    const int2 of = pl.tokens[token];
-    if (of.x < 0) return;
-    // Where the line's parts are, 32 ranges of each side at a time, side 0 in lanes 0..31: of each range the part that
+    const int wave = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (JOIN_THREADS / 64) + (threadIdx.x >> 6)));
+    const int all_lines = a.tokens * a.q_heads, line1 = (int)min((int64_t)(wave + 1) * each, (int64_t)all_lines);
+    // Where a line's parts are, 32 ranges of each side at a time, side 0 in lanes 0..31: of each range the part that
     // begins it and those that workgroups begin within it, 3 at the most, a share being more than half of a piece.
     constexpr int RANGES = 32, MOST_PARTS = 4;
     __shared__ uint32_t s_place[JOIN_THREADS / 64][2 * RANGES * MOST_PARTS];
     uint32_t *const places = s_place[threadIdx.x >> 6];
-    const int which = lane / RANGES, seg = which ? of.x : of.y;
+    const int which = lane / RANGES;
     const auto &side = which ? pl.side[1] : pl.side[0];
-    Segment sg = {0, 0, 0, 0, 0, 0, 0, 0};
-    uint32_t first = 0, place0 = 0, all_cost = 1;
-    int shares = 0, reach = 1, block = 0, in = 0;
-    if (seg >= 0) {
-        sg = side.segment[seg];
-        all_cost = side.cost[side.segments];
-        first = side.cost[seg];
-        place0 = side.parts[seg];
-        shares = pl.shares[which];
-        reach = min(pl.reach[which], max(sg.chunks, 1));
-        // (Within the segment, whatever the runs of tokens say.)
-        in = bounded((token - sg.token) * pl.group + qh % pl.group, 0, max(sg.tokens * pl.group - 1, 0));
-        block = in / side.lines;
-        first += head * head_cost(sg);
-        place0 += pl.wgs * side.lines + head * sg.ranges * sg.tokens * pl.group + in;
-        if (sg.tokens == 0) sg.ranges = 0;
+    const int shares = pl.shares[which], most_reach = pl.reach[which];
+    const bool whole = pl.whole[which];
+    Segment sg;
+    uint32_t all_cost = 1, first0 = 0, parts0 = 0;
+    int token = -1, reach = 1;
+    for (int line = (int)min((int64_t)wave * each, (int64_t)all_lines); line < line1;) {
+    const int q_head0 = line - line / a.q_heads * a.q_heads;
+    if (line / a.q_heads != token) {
+        token = line / a.q_heads;
+        const int2 of = pl.tokens[token];
+        const int seg = which ? of.x : of.y;
+        sg = Segment{0, 0, 0, 0, 0, 0, 0, 0};
+        if (seg >= 0) {
+            sg = side.segment[seg];
+            all_cost = side.cost[side.segments];
+            first0 = side.cost[seg];
+            parts0 = side.parts[seg];
+            reach = min(most_reach, max(sg.chunks, 1));
+            if (sg.tokens == 0) sg.ranges = 0;
+        }
+        // of no row, or written already
+        if (of.x < 0 || __any(which && whole && sg.start == 0 && sg.ranges == 1)) {
+            line = (token + 1) * a.q_heads;
+            continue;
+        }
     }
+    const int qh = q_head0, head = qh / pl.group;
+    ++line;
+    // (Within the segment, whatever the runs of tokens say.)
+    const int in = bounded((token - sg.token) * pl.group + qh % pl.group, 0, max(sg.tokens * pl.group - 1, 0));
+    const int block = in / side.lines, nth = which ? nth_of(block, sg.blocks) : block;
+    const uint32_t first = first0 + head * head_cost(sg);
+    const uint32_t place0 = parts0 + pl.wgs * side.lines + head * sg.ranges * sg.tokens * pl.group + in;
     const int most = max(__builtin_amdgcn_readlane(sg.ranges, 0), __builtin_amdgcn_readlane(sg.ranges, RANGES));
+    bool done = false;
     float top = NEG_INF, total = 0.f;
     f32x4_sh x = {0.f, 0.f, 0.f, 0.f};
     for (int r0 = 0; r0 < most; r0 += RANGES) {
         const int r = r0 + lane % RANGES, len = min(reach, sg.chunks - r * reach);
         int n = 0, w0 = 0;
-        if (r < sg.ranges) {
+        if (r < sg.ranges && whole) {
+            n = 1;
+        } else if (r < sg.ranges) {
             // the shares that its first and its last unit are in
-            const uint32_t at = first + r * sg.blocks * (reach + START) + block * (len + START) + START;
+            const uint32_t at = first + r * sg.blocks * (reach + START) + nth * (len + START) + START;
             w0 = (int)share_of(at + 1, shares, all_cost, 1.0);
             n = min((int)share_of(at + len, shares, all_cost, 1.0) - w0 + 1, MOST_PARTS);
         }
         const int upto = wave_running_sum(n), parts = __builtin_amdgcn_readlane(upto, 63);
-        if (__any(which && sg.start == 0 && sg.ranges == 1 && n == 1)) return;  // written already
+        if (__any(which && sg.start == 0 && sg.ranges == 1 && n == 1)) {  // written already
+            done = true;
+            break;
+        }
         for (int i = 0; i < n; ++i)
             places[upto - n + i] = (uint32_t)which << 31 | (i == 0 ? place0 + r * sg.tokens * pl.group
                                                                    : min(w0 + i, shares - 1) * side.lines + in % side.lines);
@@ -942,6 +1005,7 @@ __global__ __launch_bounds__(JOIN_THREADS, 6) void kv_shared_join_kernel(KvCache
         }
         __builtin_amdgcn_wave_barrier();
     }
+    if (done) continue;
 #pragma unroll
     for (int s = LANES; s < 64; s <<= 1) {
         const float other = __shfl_xor(top, s), up = fmaxf(top, other);
@@ -957,6 +1021,7 @@ __global__ __launch_bounds__(JOIN_THREADS, 6) void kv_shared_join_kernel(KvCache
     if (lane < LANES)
         *reinterpret_cast<u32x2_kv *>(a.out + (int64_t)token * a.out_ld + (int64_t)qh * DIM + d) =
             u32x2_kv{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
+    }
 }
 
 // The plan, its scratch laid out from `base`; returns the bytes (-1: more than a launch takes).
@@ -987,6 +1052,7 @@ static int64_t shared_plan(const KvCache &c, int q_heads, int tokens, int groups
     pl->sees = (int32_t *)take((int64_t)tokens * 4);
     pl->shares = (int32_t *)take(8);
     pl->reach = (int32_t *)take(8);
+    pl->whole = (int32_t *)take(8);
     for (int which = 0; which < 2; ++which) {
         auto &side = pl->side[which];
         side.segment = (Segment *)take((int64_t)side.segments * sizeof(Segment));
@@ -1007,14 +1073,15 @@ int64_t kv_attend_shared_workspace_bytes(const KvCache &c, int q_heads, int toke
 }
 
 template <int DIM>
-static void launch_shared(const KvCache &c, const KvAttendShared &a, const SharedPlan &pl, hipStream_t stream) {
+static void launch_shared(const KvCache &c, const KvAttendShared &a, const SharedPlan &pl, int cu_count, hipStream_t stream) {
     const dim3 grid((unsigned)pl.wgs), threads(SHARED_THREADS);
     if (c.fp8) hipLaunchKernelGGL((kv_shared_kernel<DIM, true>), grid, threads, 0, stream, c, a, pl);
     else hipLaunchKernelGGL((kv_shared_kernel<DIM, false>), grid, threads, 0, stream, c, a, pl);
-    const int64_t lines = (int64_t)a.tokens * a.q_heads;
-    constexpr int EACH = JOIN_THREADS / 64;
-    hipLaunchKernelGGL((kv_shared_join_kernel<DIM>), dim3((unsigned)((lines + EACH - 1) / EACH)), dim3(JOIN_THREADS), 0, stream,
-                       c, a, pl);
+    // A wave for each line, up to as many as run at once; then each wave takes several, of few tokens.
+    const int64_t lines = (int64_t)a.tokens * a.q_heads, most = (int64_t)cu_count * JOIN_WAVES;
+    const int each = (int)((lines + most - 1) / most);
+    const unsigned wgs = (unsigned)((lines + (int64_t)each * (JOIN_THREADS / 64) - 1) / ((int64_t)each * (JOIN_THREADS / 64)));
+    hipLaunchKernelGGL((kv_shared_join_kernel<DIM>), dim3(wgs), dim3(JOIN_THREADS), 0, stream, c, a, pl, each);
 }
 
 hipError_t launch_kv_attend_shared(const KvCache &c, const KvAttendShared &a, int cu_count, hipStream_t stream) {
@@ -1023,9 +1090,9 @@ hipError_t launch_kv_attend_shared(const KvCache &c, const KvAttendShared &a, in
     const unsigned finders = (unsigned)((a.tokens + PLAN_THREADS - 1) / PLAN_THREADS);
     hipLaunchKernelGGL(kv_shared_plan_kernel, dim3(finders + 1), dim3(PLAN_THREADS), 0, stream, c, a, pl);
     switch (c.dim) {
-    case 64: launch_shared<64>(c, a, pl, stream); break;
-    case 128: launch_shared<128>(c, a, pl, stream); break;
-    default: launch_shared<256>(c, a, pl, stream); break;
+    case 64: launch_shared<64>(c, a, pl, cu_count, stream); break;
+    case 128: launch_shared<128>(c, a, pl, cu_count, stream); break;
+    default: launch_shared<256>(c, a, pl, cu_count, stream); break;
     }
     return hipGetLastError();
 }

@@ -58,6 +58,16 @@ def test_attend_shared_all_tokens_of_long_rows(nbw, dim, dtype):  # noqa: F811
     s.check(s.call())
 
 
+@pytest.mark.parametrize("prefix", [0, 20])
+@pytest.mark.parametrize("rows,new,tail,q_heads,heads", [(70, 40, 60, 8, 8), (300, 1, 200, 2, 2), (90, 3, 300, 24, 6)])
+def test_attend_shared_more_rows_than_workgroups_take_at_once(nbw, rows, new, tail, q_heads, heads, prefix):  # noqa: F811
+    """Short rows of many sizes, several of them a workgroup's."""
+    r = random.Random(rows)
+    sizes = [(max(n, r.randrange(1, tail)), n) for n in (r.randrange(0, new + 1) for _ in range(rows))]
+    s = Shared(nbw, [(prefix, sizes)], q_heads, heads, 64, 16, seed=rows + prefix)
+    s.check(s.call())
+
+
 def test_attend_shared_a_table_of_which_part_is_used(nbw):  # noqa: F811
     s = Shared(nbw, [(48, [(6, 5), (33, 1)])], 4, 2, 128, 16, seed=8)
     wide = torch.full((s.table_np.shape[0], 50), -5, dtype=torch.int32, device="cuda")
