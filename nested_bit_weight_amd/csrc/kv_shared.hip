@@ -69,7 +69,6 @@ struct SharedPlan {
     int2 *tokens;                // [tokens] the token's row, or -1, and that row's group, or -1
     int32_t *sees;               // [tokens] slots that it sees
     int32_t *shares;             // [2] of the workgroups, those of each side
-    int32_t *reach;              // [2] units of a piece at most
     int32_t *whole;              // [2] whether shares end between pieces
     struct Side {                // 0: the groups' prefixes, 1: the rows' own slots
         int lines, segments;     // lines of a block
@@ -88,6 +87,7 @@ struct SharedPlan {
 constexpr int START = 2;
 constexpr float CUT = 2.f;
 constexpr float JOINED_MANY = 1.f / 22000, JOINED_FEW = 1.f / 13000;
+__device__ __forceinline__ int reach_of(const Segment &s) { return (s.chunks - 1) / s.ranges + 1; }  // units of a piece
 __device__ __forceinline__ uint32_t head_cost(const Segment &s) {
     return (uint32_t)s.blocks * (uint32_t)(s.chunks + START * s.ranges);
 }
@@ -198,19 +198,20 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
     }
     __syncthreads();
     // A strip of segments for each thread; with no more segments than threads its one stays in registers.
+    auto alone = [&](int g) { return a.group_rows[g + 1] - a.group_rows[g] == 1; };  // one row shares with no other
     auto of = [&](int which, int s) {
         Segment x = {s, 0, 0, 0, 0, 0, 0, 0};
         if (which) {
             const int t0 = first_token(a, s), t1 = first_token(a, s + 1), g = groups.find(s);
             x.token = t0;
             x.tokens = max(t1 - t0, 0);
-            x.start = g < 0 ? 0 : bounded(a.prefix[g], 0, a.max_len);
+            x.start = g < 0 || alone(g) ? 0 : bounded(a.prefix[g], 0, a.max_len);
             x.end = kv_len(a.lens, s, a.max_len);
         } else {
             const int r0 = bounded(a.group_rows[s], 0, c.rows), r1 = bounded(a.group_rows[s + 1], 0, c.rows);
             x.row = r0;
             x.token = first_token(a, r0);
-            x.tokens = r0 < r1 ? max(first_token(a, r1) - x.token, 0) : 0;
+            x.tokens = r0 < r1 && !alone(s) ? max(first_token(a, r1) - x.token, 0) : 0;
             x.end = bounded(a.prefix[s], 0, a.max_len);
         }
         x.chunks = x.tokens > 0 && x.end > x.start ? (x.end - x.start + UNIT - 1) / UNIT : 0;
@@ -252,16 +253,17 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
         shares[1] = min(pl.wgs - shares[0], all[1]);
     }
     // A piece has no more units than an equal share: the blocks of a range of slots then go to
-    // neighbouring workgroups, which meet its keys and values at about the same time.  Of rows' own slots the shares
-    // may be of whole pieces instead: they differ by up to a piece, but no line is cut, none that sees
-    // nothing else has to be joined, and no piece is begun twice.
-    const int reach[2] = {shares[0] ? (int)((all[0] - 1) / shares[0] + 1) : 1, shares[1] ? (int)((all[1] - 1) / shares[1] + 1) : 1};
+    // neighbouring workgroups, which meet its keys and values at about the same time.  Of rows' own slots the
+    // shares may be of whole blocks: they differ by up to a block, but none that sees nothing else
+    // has to be joined, and no piece is begun twice.
+    int reach[2] = {shares[0] ? (int)((all[0] - 1) / shares[0] + 1) : 1, shares[1] ? (int)((all[1] - 1) / shares[1] + 1) : 1};
     const float shares1 = (float)max(shares[1], 1u), piece = (float)(longest + START);
     const float takes = all[3] <= shares[1] ? piece : ((float)all[1] + START * (float)all[3]) / shares1 + piece;
     const float cut = ((float)all[1] + START * ((float)all[3] + 0.5f * shares1)) / shares1 + START + CUT +
                       (float)all[4] * pl.group * c.heads * (pl.side[1].lines > 32 ? JOINED_MANY : JOINED_FEW);
     const int whole[2] = {0, longest <= reach[1] || all[3] <= shares[1] ? takes < cut : 0};
-    auto ranges_of = [&](int which, const Segment &x) { return x.chunks ? whole[which] ? 1 : (x.chunks - 1) / reach[which] + 1 : 0; };
+    if (whole[1]) reach[1] = max(reach[1], longest);
+    auto ranges_of = [&](int which, const Segment &x) { return x.chunks ? (x.chunks - 1) / reach[which] + 1 : 0; };
     auto places_of = [&](const Segment &x) { return bounded((uint64_t)x.ranges * c.heads * ((uint64_t)x.tokens * pl.group)); };
     auto cost_of = [&](const Segment &x) { return bounded((uint64_t)c.heads * x.blocks * (uint64_t)(x.chunks + START * x.ranges)); };
     uint32_t next[4] = {0, 0, 0, 0}, next_all[4];  // places and costs of both sides
@@ -270,7 +272,6 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
         if (tid == 0) {
             pl.whole[which] = whole[which];
             pl.shares[which] = (int)shares[which];
-            pl.reach[which] = whole[which] ? max(reach[which], longest) : reach[which];
         }
         const bool one = s1[which] - s0[which] <= 1;
         for (int s = s0[which]; s < s1[which]; ++s) {
@@ -392,7 +393,6 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
     const int half = lane >> 5, col = lane & 31;
     const auto &side = pl.side[which];
     const uint32_t all_cost = side.cost[side.segments];
-    const int most_reach = pl.reach[which];
     const bool whole = pl.whole[which];
     uint32_t u = share_of(all_cost, share, shares);
     const uint32_t u1 = share_of(all_cost, share + 1, shares);
@@ -429,7 +429,7 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
         int head, range, reach, len, nth, off;
     };
     auto piece_at = [&](const Segment &sg) {
-        const int reach = min(most_reach, sg.chunks);
+        const int reach = reach_of(sg);
         const uint32_t in = u - side.cost[seg], per_head = head_cost(sg), per_range = (uint32_t)sg.blocks * (uint32_t)(reach + START);
         const int head = (int)(in / per_head);
         const uint32_t in_head = in - head * per_head;
@@ -902,125 +902,142 @@ __global__ __launch_bounds__(SHARED_THREADS, DIM > 128 ? 1 : 2) void kv_shared_k
 }
 
 // The last launch: each line's parts, in a fixed order, by a wave.
-constexpr int JOIN_THREADS = 256, JOIN_WAVES = 24;  // of a workgroup, and of a CU
+constexpr int JOIN_THREADS = 256, JOIN_WAVES = 20;  // of a workgroup, and of a CU
 constexpr float PART_BY = 1.f / (1 << 20);  // each part's weights sum to 1 at the most, and there are fewer than 2^20 of them
 template <int DIM>
 __global__ __launch_bounds__(JOIN_THREADS, JOIN_WAVES / 4) void kv_shared_join_kernel(KvCache c, KvAttendShared a, SharedPlan pl, int each) {
     constexpr int LANES = DIM / 4, SLICES = 64 / LANES;  // lanes of a part, four dims each, and parts taken side by side
     const int lane = threadIdx.x & 63, d = lane % LANES * 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (JOIN_THREADS / 64) + (threadIdx.x >> 6)));
-    const int all_lines = a.tokens * a.q_heads, line1 = (int)min((int64_t)(wave + 1) * each, (int64_t)all_lines);
-    // Where a line's parts are, 32 ranges of each side at a time, side 0 in lanes 0..31: of each range the part that
+    const int all_lines = a.tokens * a.q_heads, last = (int)min((int64_t)(wave + 1) * each, (int64_t)all_lines);
+    // Where a run's parts are, 32 ranges of each side at a time, side 0 in lanes 0..31: of each range the part that
     // begins it and those that workgroups begin within it, 3 at the most, a share being more than half of a piece.
     constexpr int RANGES = 32, MOST_PARTS = 4;
     __shared__ uint32_t s_place[JOIN_THREADS / 64][2 * RANGES * MOST_PARTS];
     uint32_t *const places = s_place[threadIdx.x >> 6];
     const int which = lane / RANGES;
     const auto &side = which ? pl.side[1] : pl.side[0];
-    const int shares = pl.shares[which], most_reach = pl.reach[which];
+    const uint32_t wgs_places = pl.wgs * side.lines;
+    const int shares = pl.shares[which];
     const bool whole = pl.whole[which];
-    Segment sg;
-    uint32_t all_cost = 1, first0 = 0, parts0 = 0;
-    int token = -1, reach = 1;
-    for (int line = (int)min((int64_t)wave * each, (int64_t)all_lines); line < line1;) {
-    const int q_head0 = line - line / a.q_heads * a.q_heads;
-    if (line / a.q_heads != token) {
-        token = line / a.q_heads;
-        const int2 of = pl.tokens[token];
+    // A row's lines are counted by head, then token and query head, as its parts are.
+    for (int at = (int)min((int64_t)wave * each, (int64_t)all_lines); at < last;) {
+        const int2 of = pl.tokens[at / a.q_heads];
+        if (of.x < 0) {  // of no row
+            at += a.q_heads - at % a.q_heads;
+            continue;
+        }
+        Segment sg = {0, 0, 0, 0, 0, 0, 0, 0};
+        uint32_t all_cost = 1, first0 = 0, parts0 = 0;
         const int seg = which ? of.x : of.y;
-        sg = Segment{0, 0, 0, 0, 0, 0, 0, 0};
         if (seg >= 0) {
             sg = side.segment[seg];
             all_cost = side.cost[side.segments];
             first0 = side.cost[seg];
             parts0 = side.parts[seg];
-            reach = min(most_reach, max(sg.chunks, 1));
             if (sg.tokens == 0) sg.ranges = 0;
         }
-        // of no row, or written already
-        if (of.x < 0 || __any(which && whole && sg.start == 0 && sg.ranges == 1)) {
-            line = (token + 1) * a.q_heads;
+        const int token0 = first_token(a, of.x), per_head = (first_token(a, of.x + 1) - token0) * pl.group;
+        const int end = min((token0 * a.q_heads) + per_head * c.heads, last);
+        if (per_head <= 0 || end <= at) return;  // runs of tokens that are none
+        if (__any(which && whole && sg.start == 0 && sg.ranges == 1)) {  // written already
+            at = end;
             continue;
         }
-    }
-    const int qh = q_head0, head = qh / pl.group;
-    ++line;
-    // (Within the segment, whatever the runs of tokens say.)
-    const int in = bounded((token - sg.token) * pl.group + qh % pl.group, 0, max(sg.tokens * pl.group - 1, 0));
-    const int block = in / side.lines, nth = which ? nth_of(block, sg.blocks) : block;
-    const uint32_t first = first0 + head * head_cost(sg);
-    const uint32_t place0 = parts0 + pl.wgs * side.lines + head * sg.ranges * sg.tokens * pl.group + in;
-    const int most = max(__builtin_amdgcn_readlane(sg.ranges, 0), __builtin_amdgcn_readlane(sg.ranges, RANGES));
-    bool done = false;
-    float top = NEG_INF, total = 0.f;
-    f32x4_sh x = {0.f, 0.f, 0.f, 0.f};
-    for (int r0 = 0; r0 < most; r0 += RANGES) {
-        const int r = r0 + lane % RANGES, len = min(reach, sg.chunks - r * reach);
-        int n = 0, w0 = 0;
-        if (r < sg.ranges && whole) {
-            n = 1;
-        } else if (r < sg.ranges) {
-            // the shares that its first and its last unit are in
-            const uint32_t at = first + r * sg.blocks * (reach + START) + nth * (len + START) + START;
-            w0 = (int)share_of(at + 1, shares, all_cost, 1.0);
-            n = min((int)share_of(at + len, shares, all_cost, 1.0) - w0 + 1, MOST_PARTS);
-        }
-        const int upto = wave_running_sum(n), parts = __builtin_amdgcn_readlane(upto, 63);
-        if (__any(which && sg.start == 0 && sg.ranges == 1 && n == 1)) {  // written already
-            done = true;
-            break;
-        }
-        for (int i = 0; i < n; ++i)
-            places[upto - n + i] = (uint32_t)which << 31 | (i == 0 ? place0 + r * sg.tokens * pl.group
-                                                                   : min(w0 + i, shares - 1) * side.lines + in % side.lines);
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        constexpr int AHEAD = 4;
-        for (int i0 = 0; i0 < parts; i0 += AHEAD * SLICES) {
-            f32x4_sh y[AHEAD];
-            float2 ml[AHEAD];
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                const uint32_t at = places[min(i0 + k * SLICES + lane / LANES, parts - 1)];
-                const auto &from = at >> 31 ? pl.side[1] : pl.side[0];
-                const int64_t place = at & 0x7FFFFFFFu;
-                ml[k] = *reinterpret_cast<const float2 *>(from.ml + 2 * place);
-                y[k] = *reinterpret_cast<const f32x4_sh *>(from.o + place * DIM + d);
-            }
-            float up = top;
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k) up = fmaxf(up, ml[k].x);
-            const float fade = top == up ? 1.f : __builtin_amdgcn_exp2f(top - up);
-            total *= fade;
-            x *= fade;
-            top = up;
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k)
-                if (i0 + k * SLICES + lane / LANES < parts) {
-                    const float f = ml[k].x == top ? 1.f : __builtin_amdgcn_exp2f(ml[k].x - top);
-                    total += ml[k].y * f;
-                    x += y[k] * (f * PART_BY);
+        const int reach = sg.ranges ? reach_of(sg) : 1;
+        while (at < end) {
+            // A run of lines of a head, in one block of each side.
+            const int head = (at - token0 * a.q_heads) / per_head, line = at - token0 * a.q_heads - head * per_head;
+            // (Within the segment, whatever the runs of tokens say.)
+            const int in = bounded((token0 - sg.token) * pl.group + line, 0, max(sg.tokens * pl.group - 1, 0));
+            const int block = in / side.lines, nth = which ? nth_of(block, sg.blocks) : block;
+            const int left = sg.ranges ? min((block + 1) * side.lines, sg.tokens * pl.group) - in : INT32_MAX;  // of the block
+            const int run = min(min(min(__builtin_amdgcn_readlane(left, 0), __builtin_amdgcn_readlane(left, RANGES)), per_head - line),
+                                end - at);
+            const uint32_t first = first0 + head * head_cost(sg);
+            const uint32_t place0 = parts0 + wgs_places + head * sg.ranges * sg.tokens * pl.group + in;
+            const int most = max(__builtin_amdgcn_readlane(sg.ranges, 0), __builtin_amdgcn_readlane(sg.ranges, RANGES));
+            at += run;
+            int parts = 0;
+            auto find = [&](int r0) {  // true: written already
+                const int r = r0 + lane % RANGES, len = min(reach, sg.chunks - r * reach);
+                int n = 0, w0 = 0;
+                if (r < sg.ranges) {
+                    n = 1;
+                    if (!whole) {  // the shares that its first and its last unit are in
+                        const uint32_t u = first + r * sg.blocks * (reach + START) + nth * (len + START) + START;
+                        w0 = (int)share_of(u + 1, shares, all_cost, 1.0);
+                        n = min((int)share_of(u + len, shares, all_cost, 1.0) - w0 + 1, MOST_PARTS);
+                    }
                 }
+                const int upto = wave_running_sum(n);
+                parts = __builtin_amdgcn_readlane(upto, 63);
+                if (__any(which && sg.start == 0 && sg.ranges == 1 && n == 1)) return true;
+                for (int i = 0; i < n; ++i)
+                    places[upto - n + i] = (uint32_t)which << 31 | (i == 0 ? place0 + r * sg.tokens * pl.group
+                                                                           : min(w0 + i, shares - 1) * side.lines + in % side.lines);
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+                return false;
+            };
+            if (find(0)) continue;
+            for (int i = 0; i < run; ++i) {
+                float top = NEG_INF, total = 0.f;
+                f32x4_sh x = {0.f, 0.f, 0.f, 0.f};
+                for (int r0 = 0;;) {
+                    constexpr int AHEAD = 4;
+                    for (int i0 = 0; i0 < parts; i0 += AHEAD * SLICES) {
+                        f32x4_sh y[AHEAD];
+                        float2 ml[AHEAD];
+#pragma unroll
+                        for (int k = 0; k < AHEAD; ++k) {
+                            const uint32_t from = places[min(i0 + k * SLICES + lane / LANES, parts - 1)];
+                            const auto &f = from >> 31 ? pl.side[1] : pl.side[0];
+                            const int64_t place = (from & 0x7FFFFFFFu) + i;
+                            ml[k] = *reinterpret_cast<const float2 *>(f.ml + 2 * place);
+                            y[k] = *reinterpret_cast<const f32x4_sh *>(f.o + place * DIM + d);
+                        }
+                        float up = top;
+#pragma unroll
+                        for (int k = 0; k < AHEAD; ++k) up = fmaxf(up, ml[k].x);
+                        const float fade = top == up ? 1.f : __builtin_amdgcn_exp2f(top - up);
+                        total *= fade;
+                        x *= fade;
+                        top = up;
+#pragma unroll
+                        for (int k = 0; k < AHEAD; ++k)
+                            if (i0 + k * SLICES + lane / LANES < parts) {
+                                const float f = ml[k].x == top ? 1.f : __builtin_amdgcn_exp2f(ml[k].x - top);
+                                total += ml[k].y * f;
+                                x += y[k] * (f * PART_BY);
+                            }
+                    }
+                    if (most <= RANGES) break;
+                    r0 = r0 + RANGES < most ? r0 + RANGES : 0;
+                    __builtin_amdgcn_wave_barrier();
+                    find(r0);  // the next ranges, or the first ones for the next line
+                    if (r0 == 0) break;
+                }
+#pragma unroll
+                for (int s = LANES; s < 64; s <<= 1) {
+                    const float other = __shfl_xor(top, s), up = fmaxf(top, other);
+                    const float f = top == up ? 1.f : __builtin_amdgcn_exp2f(top - up);
+                    const float g = other == up ? 1.f : __builtin_amdgcn_exp2f(other - up);
+                    total = total * f + __shfl_xor(total, s) * g;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = x[e] * f + __shfl_xor(x[e], s) * g;
+                    top = up;
+                }
+                x *= total == 0.f ? 0.f : 1.f / (total * PART_BY);
+                if (total == 0.f) x = f32x4_sh{0.f, 0.f, 0.f, 0.f};  // nothing to attend to, whatever the values are
+                if (c.fp8) x *= c.v_scale[head];
+                const int64_t token = token0 + (line + i) / pl.group, qh = head * pl.group + (line + i) % pl.group;
+                if (lane < LANES)
+                    *reinterpret_cast<u32x2_kv *>(a.out + token * a.out_ld + qh * DIM + d) =
+                        u32x2_kv{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
+            }
         }
-        __builtin_amdgcn_wave_barrier();
-    }
-    if (done) continue;
-#pragma unroll
-    for (int s = LANES; s < 64; s <<= 1) {
-        const float other = __shfl_xor(top, s), up = fmaxf(top, other);
-        const float f = top == up ? 1.f : __builtin_amdgcn_exp2f(top - up), g = other == up ? 1.f : __builtin_amdgcn_exp2f(other - up);
-        total = total * f + __shfl_xor(total, s) * g;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = x[e] * f + __shfl_xor(x[e], s) * g;
-        top = up;
-    }
-    x *= total == 0.f ? 0.f : 1.f / (total * PART_BY);
-    if (total == 0.f) x = f32x4_sh{0.f, 0.f, 0.f, 0.f};  // nothing to attend to, whatever the values are
-    if (c.fp8) x *= c.v_scale[head];
-    if (lane < LANES)
-        *reinterpret_cast<u32x2_kv *>(a.out + (int64_t)token * a.out_ld + (int64_t)qh * DIM + d) =
-            u32x2_kv{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
     }
 }
 
@@ -1051,7 +1068,6 @@ static int64_t shared_plan(const KvCache &c, int q_heads, int tokens, int groups
     pl->tokens = (int2 *)take((int64_t)tokens * 8);
     pl->sees = (int32_t *)take((int64_t)tokens * 4);
     pl->shares = (int32_t *)take(8);
-    pl->reach = (int32_t *)take(8);
     pl->whole = (int32_t *)take(8);
     for (int which = 0; which < 2; ++which) {
         auto &side = pl->side[which];
