@@ -12,7 +12,8 @@
 // ends in a walk through a run.
 //
 // Bound: the chain of loads (lengths -> sums -> page numbers -> stores) of one
-// launch.
+// launch: 3.5 us for one row, 6.5 for 256 rows with up to 6 tokens each, 6.8 for 96 prompts of up to
+// 8192 tokens (4.8 MB written); a call takes 9 us with the host's checks of its tensors.
 #include <algorithm>
 
 #include "kv.h"

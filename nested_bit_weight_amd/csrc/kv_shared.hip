@@ -7,17 +7,19 @@
 // prefix, with all lines of the group, and each row's own slots behind it, with the row's
 // lines.  What a segment gives a line, (m, sum, o), is joined in a last launch.
 //
-// Four launches: the segments' sizes; the prefixes; the rows' own slots; the join.  In the
-// middle two a workgroup takes a block of 32 LW lines of one head over a run of slots, its
-// SW waves along the slots sharing each tile of them: many lines (LW = 4, SW = 1) read
-// each key and value from LDS for 32 lines each, few lines (LW = 1, SW = 4) are bound by
-// the cache's bytes, of which each wave takes its own 32 slots.  The units of all segments, 128
-// slots of a block, are divided in equal shares over as many workgroups as run at once,
-// whatever the lengths.
+// Three launches.  The first divides the work: blocks of lines of a head (32, or 128 where segments have more) times runs
+// of 128 slots, in equal shares over as many workgroups as run at once, whatever the lengths; so nothing but the
+// device's own numbers says how long a row is, and a captured call stays valid as rows grow.  The second
+// attends, prefixes and own slots side by side; the third joins the parts of each line.
 //
-// A tile goes from memory through registers, asked for a tile ahead, to LDS (8-bit
-// values widened to bf16 on the way), in 16-byte pieces whose place within a row is turned by the
-// row's number so that no two lanes of a half wave meet in a bank.  Then on
+// Few lines are bound by the cache's bytes: each of a workgroup's four waves has 32 of each 128 slots to itself, in LDS of its
+// own, and never waits for the others until a piece ends.  Many lines are bound by the matrix units and the
+// exponentials: each wave has 32 of the 128 lines, and the four share each tile's keys and values,
+// so that LDS is read once for 32 lines but filled once for 128.
+//
+// Keys and values of bf16 go from memory straight to LDS, 16 bytes a lane, a tile (few lines: half a tile) ahead of their
+// use; 8-bit ones through registers, widened to bf16, which holds them exactly.  The place of each 16-byte piece within a
+// row is turned by the row's number so that readers do not meet in a bank.  Then on
 // v_mfma_f32_32x32x16_bf16, with a line in each lane throughout:
 //  - S^T = K Q^T: lane l has line l % 32 and of 32 slots the ones 8 (i / 4) + 4 (l / 32) + i % 4
 //    in its registers i = 0..15, so the maximum and the sum need one exchange, between the halves;
@@ -33,6 +35,12 @@
 //
 // The running maximum m of a line is only raised, and o and the sum rescaled, when a score
 // passes it by more than 8 (a factor of 2^8).
+//
+// Measured (32 query heads over 8 of 128 dims, bf16; the second launch, then all three): 64 rows behind a prefix of
+// 8192, 600 slots of their own each, 122 MB: 37 and 53 us; 16 rows of 4096 slots with 5 tokens, 148 MB: 32 us (4.6 TB/s)
+// and 44; 96 rows with 5 tokens behind a prefix of 32767, 140 GFLOP with what the mask covers: 189 us (740 TFLOP/s; matrix
+// units busy 37% of the time, VALU at least 30) and 204.  Loads through registers and barriers, prefixes and
+// own slots in launches of their own: 148 us, 87 and 295 in all.
 #include <algorithm>
 #include <type_traits>
 
@@ -58,9 +66,10 @@ struct Segment {
     int row;             // whose table holds its slots
     int token, tokens;   // its lines' tokens
     int start, end;      // its slots
-    int chunks, blocks;  // units of a block of lines of a head, and blocks
-    int ranges;          // pieces that those units are cut into
+    int blocks;          // of lines, of a head
+    int ranges, reach;   // pieces that the units of a block are cut into, and units of one
 };
+__device__ __forceinline__ int units_of(const Segment &s) { return (s.end - s.start + UNIT - 1) / UNIT; }  // of a block
 
 // The call's division of work and its scratch.
 struct SharedPlan {
@@ -68,8 +77,10 @@ struct SharedPlan {
     int wgs;                     // workgroups of the launch that attends
     int2 *tokens;                // [tokens] the token's row, or -1, and that row's group, or -1
     int32_t *sees;               // [tokens] slots that it sees
-    int32_t *shares;             // [2] of the workgroups, those of each side
-    int32_t *whole;              // [2] whether shares end between pieces
+    struct Division {
+        int32_t shares[2];       // of the workgroups, those of each side
+        int32_t whole[2];        // whether shares end between pieces
+    } *division;
     struct Side {                // 0: the groups' prefixes, 1: the rows' own slots
         int lines, segments;     // lines of a block
         uint32_t places;         // that there are
@@ -85,11 +96,14 @@ struct SharedPlan {
 // A piece costs as much as its units and START more, for the loads that depend on each other at its
 // start and the result at its end (few lines: 7 us beside 3 for a unit; many: 8 beside 5).
 constexpr int START = 2;
+// Units that a share which ends within a piece costs beyond that, for what it writes and the join reads; and units that the
+// join takes for each line that whole pieces would spare it (0.23 ns each, beside units of 5 and 3 us).  13 rows of 500 new tokens
+// of 50 query heads, in all: divided 179 us, whole 110.  Where pieces are long, whole ones lose, as in the prefixes too: the
+// second launch of 64 rows behind one of 8192 slots 37 us divided, 52 with whole pieces of both sides.
 constexpr float CUT = 2.f;
 constexpr float JOINED_MANY = 1.f / 22000, JOINED_FEW = 1.f / 13000;
-__device__ __forceinline__ int reach_of(const Segment &s) { return (s.chunks - 1) / s.ranges + 1; }  // units of a piece
 __device__ __forceinline__ uint32_t head_cost(const Segment &s) {
-    return (uint32_t)s.blocks * (uint32_t)(s.chunks + START * s.ranges);
+    return (uint32_t)s.blocks * (uint32_t)(units_of(s) + START * s.ranges);
 }
 
 // All of a call's units, costs and places are below 2^31 (shared_plan); sums that say otherwise, of rows that are not
@@ -200,7 +214,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
     // A strip of segments for each thread; with no more segments than threads its one stays in registers.
     auto alone = [&](int g) { return a.group_rows[g + 1] - a.group_rows[g] == 1; };  // one row shares with no other
     auto of = [&](int which, int s) {
-        Segment x = {s, 0, 0, 0, 0, 0, 0, 0};
+        Segment x = {s, 0, 0, 0, 0, 0, 0, 1};
         if (which) {
             const int t0 = first_token(a, s), t1 = first_token(a, s + 1), g = groups.find(s);
             x.token = t0;
@@ -214,8 +228,9 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
             x.tokens = r0 < r1 && !alone(s) ? max(first_token(a, r1) - x.token, 0) : 0;
             x.end = bounded(a.prefix[s], 0, a.max_len);
         }
-        x.chunks = x.tokens > 0 && x.end > x.start ? (x.end - x.start + UNIT - 1) / UNIT : 0;
-        x.blocks = x.chunks ? (int)(((int64_t)x.tokens * pl.group + pl.side[which].lines - 1) / pl.side[which].lines) : 0;
+        if (x.tokens == 0) x.end = x.start;
+        x.end = max(x.end, x.start);
+        x.blocks = units_of(x) ? (int)(((int64_t)x.tokens * pl.group + pl.side[which].lines - 1) / pl.side[which].lines) : 0;
         return x;
     };
     int s0[2], s1[2];
@@ -230,9 +245,9 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
         for (int s = s0[which]; s < s1[which]; ++s) {
             const Segment x = mine[which] = of(which, s);
             const uint32_t blocks = bounded((uint64_t)c.heads * x.blocks);
-            sums[which] = plus(sums[which], bounded((uint64_t)blocks * x.chunks));
+            sums[which] = plus(sums[which], bounded((uint64_t)blocks * units_of(x)));
             sums[2 + which] = plus(sums[2 + which], blocks);
-            if (which) own_units = max(own_units, x.chunks);
+            if (which) own_units = max(own_units, units_of(x));
             if (which && x.start == 0) sums[4] = plus(sums[4], (uint32_t)x.tokens);
         }
     }
@@ -259,24 +274,27 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
     int reach[2] = {shares[0] ? (int)((all[0] - 1) / shares[0] + 1) : 1, shares[1] ? (int)((all[1] - 1) / shares[1] + 1) : 1};
     const float shares1 = (float)max(shares[1], 1u), piece = (float)(longest + START);
     const float takes = all[3] <= shares[1] ? piece : ((float)all[1] + START * (float)all[3]) / shares1 + piece;
-    const float cut = ((float)all[1] + START * ((float)all[3] + 0.5f * shares1)) / shares1 + START + CUT +
+    const float divided = ((float)all[1] + START * ((float)all[3] + 0.5f * shares1)) / shares1 + START + CUT +
                       (float)all[4] * pl.group * c.heads * (pl.side[1].lines > 32 ? JOINED_MANY : JOINED_FEW);
-    const int whole[2] = {0, longest <= reach[1] || all[3] <= shares[1] ? takes < cut : 0};
+    const int whole[2] = {0, longest <= reach[1] || all[3] <= shares[1] ? takes < divided : 0};
     if (whole[1]) reach[1] = max(reach[1], longest);
-    auto ranges_of = [&](int which, const Segment &x) { return x.chunks ? (x.chunks - 1) / reach[which] + 1 : 0; };
+    auto cut = [&](int which, Segment &x) {
+        x.ranges = units_of(x) ? (units_of(x) - 1) / reach[which] + 1 : 0;
+        x.reach = x.ranges ? (units_of(x) - 1) / x.ranges + 1 : 1;
+    };
     auto places_of = [&](const Segment &x) { return bounded((uint64_t)x.ranges * c.heads * ((uint64_t)x.tokens * pl.group)); };
-    auto cost_of = [&](const Segment &x) { return bounded((uint64_t)c.heads * x.blocks * (uint64_t)(x.chunks + START * x.ranges)); };
+    auto cost_of = [&](const Segment &x) { return bounded((uint64_t)c.heads * x.blocks * (uint64_t)(units_of(x) + START * x.ranges)); };
     uint32_t next[4] = {0, 0, 0, 0}, next_all[4];  // places and costs of both sides
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         if (tid == 0) {
-            pl.whole[which] = whole[which];
-            pl.shares[which] = (int)shares[which];
+            pl.division->whole[which] = whole[which];
+            pl.division->shares[which] = (int)shares[which];
         }
         const bool one = s1[which] - s0[which] <= 1;
         for (int s = s0[which]; s < s1[which]; ++s) {
             if (!one) mine[which] = of(which, s);
-            mine[which].ranges = ranges_of(which, mine[which]);
+            cut(which, mine[which]);
             next[which] = plus(next[which], places_of(mine[which]));
             next[2 + which] = plus(next[2 + which], cost_of(mine[which]));
         }
@@ -291,7 +309,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
         for (int s = s0[which]; s < s1[which]; ++s) {
             if (!one) {
                 mine[which] = of(which, s);
-                mine[which].ranges = ranges_of(which, mine[which]);
+                cut(which, mine[which]);
             }
             Segment x = mine[which];
             side.parts[s] = place;
@@ -384,7 +402,7 @@ struct SharedLds {
 // One workgroup's share of a side's units.
 template <int DIM, bool FP8, bool FEW>
 __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendShared &a, const SharedPlan &pl, int which, int share,
-                                             int shares, const SharedLds &lds) {
+                                             int shares, bool whole, const SharedLds &lds) {
     using X = Shape<DIM, FP8, FEW>;
     constexpr int TILE = X::TILE, SUBS = X::SUBS, PIECES = X::PIECES, LOADS = X::LOADS, ROW = X::ROW;
     constexpr int R = 256 / DIM;  // rows of a tile in 512 bytes, one turn of the banks
@@ -393,7 +411,6 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
     const int half = lane >> 5, col = lane & 31;
     const auto &side = pl.side[which];
     const uint32_t all_cost = side.cost[side.segments];
-    const bool whole = pl.whole[which];
     uint32_t u = share_of(all_cost, share, shares);
     const uint32_t u1 = share_of(all_cost, share + 1, shares);
     int seg = 0;  // segments that end at or before u: 64 places looked at together, then 64 between two of them
@@ -429,13 +446,13 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
         int head, range, reach, len, nth, off;
     };
     auto piece_at = [&](const Segment &sg) {
-        const int reach = reach_of(sg);
+        const int reach = sg.reach;
         const uint32_t in = u - side.cost[seg], per_head = head_cost(sg), per_range = (uint32_t)sg.blocks * (uint32_t)(reach + START);
         const int head = (int)(in / per_head);
         const uint32_t in_head = in - head * per_head;
         const int range = min((int)(in_head / per_range), sg.ranges - 1);
         const uint32_t in_range = in_head - range * per_range;
-        const int len = min(reach, sg.chunks - range * reach);
+        const int len = min(reach, units_of(sg) - range * reach);
         const int nth = (int)(in_range / (uint32_t)(len + START));
         return Piece{head, range, reach, len, nth, (int)in_range - nth * (len + START)};
     };
@@ -445,7 +462,7 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
         if (u >= u1) return;
         next_segment();
     }
-    for (;;) {  // a piece, or a part of one: chunks [c0, c1) of one block of a segment's lines
+    for (;;) {  // a piece, or a part of one: units [c0, c1) of one block of a segment's lines
         const Segment sg = side.segment[seg];
         const auto [head, range, reach, len, nth, off] = piece_at(sg);
         const int rest = len + START - off, take = whole ? rest : (int)min(u1 - u, (uint32_t)rest);
@@ -824,7 +841,7 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
 
         // The piece's result.  One that has all that its lines see is the result; others wait for the join.
         sum += __shfl_xor(sum, 32);
-        const bool sole = which && sg.start == 0 && c1 - c0 == sg.chunks;
+        const bool sole = which && sg.start == 0 && c1 - c0 == units_of(sg);
         const float v_by = FP8 ? c.v_scale[head] : 1.f;
         const uint32_t part0 = begins ? pl.wgs * X::LINES + side.parts[seg] + (head * sg.ranges + range) * sg.tokens * pl.group +
                                             block * X::LINES
@@ -891,18 +908,19 @@ __global__ __launch_bounds__(SHARED_THREADS, DIM > 128 ? 1 : 2) void kv_shared_k
     __shared__ __align__(16) uint8_t pool[std::max(Shape<DIM, FP8, true>::BYTES, Shape<DIM, FP8, false>::BYTES)];
     __shared__ float s_m[SHARED_WAVES][32], s_l[SHARED_WAVES][32];
     const SharedLds lds = {pool, s_m, s_l};
-    const int n0 = pl.shares[0], n1 = pl.shares[1], b = (int)blockIdx.x;
+    const SharedPlan::Division dv = *pl.division;
+    const int n0 = dv.shares[0], n1 = dv.shares[1], b = (int)blockIdx.x;
     if (b >= n0 + n1) return;
     const int which = b >= n0;
     // Workgroups go to the 8 XCDs in turn; neighbouring shares, which meet the same keys, go to one.
     int share = b - n0;
     if (!which) share = b % 8 * (n0 / 8) + min(b % 8, n0 % 8) + b / 8;
-    if (pl.side[which].lines == Shape<DIM, FP8, true>::LINES) attend_share<DIM, FP8, true>(c, a, pl, which, share, which ? n1 : n0, lds);
-    else attend_share<DIM, FP8, false>(c, a, pl, which, share, which ? n1 : n0, lds);
+    if (pl.side[which].lines == Shape<DIM, FP8, true>::LINES) attend_share<DIM, FP8, true>(c, a, pl, which, share, which ? n1 : n0, (which ? dv.whole[1] : dv.whole[0]), lds);
+    else attend_share<DIM, FP8, false>(c, a, pl, which, share, which ? n1 : n0, (which ? dv.whole[1] : dv.whole[0]), lds);
 }
 
 // The last launch: each line's parts, in a fixed order, by a wave.
-constexpr int JOIN_THREADS = 256, JOIN_WAVES = 20;  // of a workgroup, and of a CU
+constexpr int JOIN_THREADS = 256, JOIN_WAVES = 20;  // of a workgroup, and of a CU (24: registers in scratch)
 constexpr float PART_BY = 1.f / (1 << 20);  // each part's weights sum to 1 at the most, and there are fewer than 2^20 of them
 template <int DIM>
 __global__ __launch_bounds__(JOIN_THREADS, JOIN_WAVES / 4) void kv_shared_join_kernel(KvCache c, KvAttendShared a, SharedPlan pl, int each) {
@@ -918,8 +936,9 @@ __global__ __launch_bounds__(JOIN_THREADS, JOIN_WAVES / 4) void kv_shared_join_k
     const int which = lane / RANGES;
     const auto &side = which ? pl.side[1] : pl.side[0];
     const uint32_t wgs_places = pl.wgs * side.lines;
-    const int shares = pl.shares[which];
-    const bool whole = pl.whole[which];
+    const SharedPlan::Division dv = *pl.division;
+    const int shares = which ? dv.shares[1] : dv.shares[0];
+    const bool whole = which ? dv.whole[1] : dv.whole[0];
     // A row's lines are counted by head, then token and query head, as its parts are.
     for (int at = (int)min((int64_t)wave * each, (int64_t)all_lines); at < last;) {
         const int2 of = pl.tokens[at / a.q_heads];
@@ -927,7 +946,7 @@ __global__ __launch_bounds__(JOIN_THREADS, JOIN_WAVES / 4) void kv_shared_join_k
             at += a.q_heads - at % a.q_heads;
             continue;
         }
-        Segment sg = {0, 0, 0, 0, 0, 0, 0, 0};
+        Segment sg = {0, 0, 0, 0, 0, 0, 0, 1};
         uint32_t all_cost = 1, first0 = 0, parts0 = 0;
         const int seg = which ? of.x : of.y;
         if (seg >= 0) {
@@ -944,7 +963,7 @@ __global__ __launch_bounds__(JOIN_THREADS, JOIN_WAVES / 4) void kv_shared_join_k
             at = end;
             continue;
         }
-        const int reach = sg.ranges ? reach_of(sg) : 1;
+        const int reach = sg.reach;
         while (at < end) {
             // A run of lines of a head, in one block of each side.
             const int head = (at - token0 * a.q_heads) / per_head, line = at - token0 * a.q_heads - head * per_head;
@@ -960,7 +979,7 @@ __global__ __launch_bounds__(JOIN_THREADS, JOIN_WAVES / 4) void kv_shared_join_k
             at += run;
             int parts = 0;
             auto find = [&](int r0) {  // true: written already
-                const int r = r0 + lane % RANGES, len = min(reach, sg.chunks - r * reach);
+                const int r = r0 + lane % RANGES, len = min(reach, units_of(sg) - r * reach);
                 int n = 0, w0 = 0;
                 if (r < sg.ranges) {
                     n = 1;
@@ -1067,8 +1086,7 @@ static int64_t shared_plan(const KvCache &c, int q_heads, int tokens, int groups
     };
     pl->tokens = (int2 *)take((int64_t)tokens * 8);
     pl->sees = (int32_t *)take((int64_t)tokens * 4);
-    pl->shares = (int32_t *)take(8);
-    pl->whole = (int32_t *)take(8);
+    pl->division = (SharedPlan::Division *)take(sizeof(SharedPlan::Division));
     for (int which = 0; which < 2; ++which) {
         auto &side = pl->side[which];
         side.segment = (Segment *)take((int64_t)side.segments * sizeof(Segment));
