@@ -82,7 +82,7 @@ struct SharedPlan {
         int32_t whole[2];        // whether shares end between pieces
     } *division;
     struct Side {                // 0: the groups' prefixes, 1: the rows' own slots
-        int lines, segments;     // lines of a block
+        int lines, segments;     // lines of a block, a power of two
         uint32_t places;         // that there are
         Segment *segment;        // [segments]
         uint32_t *cost;          // [segments + 1] of the segments before each
@@ -230,7 +230,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
         }
         if (x.tokens == 0) x.end = x.start;
         x.end = max(x.end, x.start);
-        x.blocks = units_of(x) ? (int)(((int64_t)x.tokens * pl.group + pl.side[which].lines - 1) / pl.side[which].lines) : 0;
+        x.blocks = units_of(x) ? (int)(((int64_t)x.tokens * pl.group + pl.side[which].lines - 1) >> __builtin_ctz(pl.side[which].lines)) : 0;
         return x;
     };
     int s0[2], s1[2];
@@ -936,6 +936,7 @@ __global__ __launch_bounds__(JOIN_THREADS, JOIN_WAVES / 4) void kv_shared_join_k
     const int which = lane / RANGES;
     const auto &side = which ? pl.side[1] : pl.side[0];
     const uint32_t wgs_places = pl.wgs * side.lines;
+    const int lines_log2 = __builtin_ctz(side.lines);
     const SharedPlan::Division dv = *pl.division;
     const int shares = which ? dv.shares[1] : dv.shares[0];
     const bool whole = which ? dv.whole[1] : dv.whole[0];
@@ -969,7 +970,7 @@ __global__ __launch_bounds__(JOIN_THREADS, JOIN_WAVES / 4) void kv_shared_join_k
             const int head = (at - token0 * a.q_heads) / per_head, line = at - token0 * a.q_heads - head * per_head;
             // (Within the segment, whatever the runs of tokens say.)
             const int in = bounded((token0 - sg.token) * pl.group + line, 0, max(sg.tokens * pl.group - 1, 0));
-            const int block = in / side.lines, nth = which ? nth_of(block, sg.blocks) : block;
+            const int block = in >> lines_log2, nth = which ? nth_of(block, sg.blocks) : block;
             const int left = sg.ranges ? min((block + 1) * side.lines, sg.tokens * pl.group) - in : INT32_MAX;  // of the block
             const int run = min(min(min(__builtin_amdgcn_readlane(left, 0), __builtin_amdgcn_readlane(left, RANGES)), per_head - line),
                                 end - at);
@@ -994,7 +995,7 @@ __global__ __launch_bounds__(JOIN_THREADS, JOIN_WAVES / 4) void kv_shared_join_k
                 if (__any(which && sg.start == 0 && sg.ranges == 1 && n == 1)) return true;
                 for (int i = 0; i < n; ++i)
                     places[upto - n + i] = (uint32_t)which << 31 | (i == 0 ? place0 + r * sg.tokens * pl.group
-                                                                           : min(w0 + i, shares - 1) * side.lines + in % side.lines);
+                                                                           : min(w0 + i, shares - 1) * side.lines + (in & (side.lines - 1)));
                 __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
                 __builtin_amdgcn_wave_barrier();
                 __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");

@@ -8,13 +8,14 @@
 // A first launch sums spans of 1024 of them, a wave a span, or a few one after the other where
 // there are more than run at once; a second one, a wave a row, finds the span in which the sum passes
 // u times the whole, and then the place in it.  Nothing is shared between waves, so there is no barrier.
+// (A few short rows: a workgroup each, both in one launch.)
 // Sums are in fp64 and in a fixed order: of 128 thousand weights they are off by about 1e-14, so that the
 // place is the exact one but for one draw in 1e9.
 //
 // Bound: memory, one line a row, or two where a draft was refused; for few rows the
-// chain of loads (cu -> tokens -> p, q -> line) and the second launch.  One row of 32000 weights
-// 4.0 + 3.3 us, 64 rows of 128000 (56 MB) 11.4 + 4.5, 256 lines of 160001 in bf16 (82 MB) 17.4 + 4.7: 4.7 TB/s, held up by
-// the arithmetic of the weights.  (A workgroup a span, with barriers: 12.3 us for one row, 43 for the 256 lines; 32 weights a
+// chain of loads (cu -> tokens -> p, q -> line) and the second launch.  One row of 32000 weights 6.8 us,
+// 64 rows of 128000 (56 MB) 11.4 + 4.5, 256 lines of 160001 in bf16 (82 MB) 17.4 + 4.7: 4.7 TB/s, held up
+// by the arithmetic of the weights.  (A workgroup a span, with barriers: 12.3 us for one row, 43 for the 256 lines; 32 weights a
 // lane 28 in place of 25, loads at shifted, aligned addresses 27, six waves a SIMD 26.)
 #include <algorithm>
 
@@ -201,21 +202,12 @@ __global__ __launch_bounds__(VERIFY_THREADS) void verify_sums_kernel(VerifyDraft
     }
 }
 
-// The second launch: each row's next token.
-template <bool BF16>
-__global__ __launch_bounds__(64) void verify_next_kernel(VerifyDrafts a, int spans, const double *sums) {
-    const int row = blockIdx.x, lane = threadIdx.x;
-    const double *const mine = sums + (int64_t)row * spans;
-    constexpr int KEPT = 4;  // a lane keeps the sums of so many spans: of 64 of them each
-    double kept[KEPT];
-#pragma unroll
-    for (int i = 0; i < KEPT; ++i) kept[i] = i * 64 + lane < spans ? mine[i * 64 + lane] : 0.0;
-    const int stands = a.accepted[row];
-    const Lines l = lines_of(a, row);
-    if (l.count <= 0) {
-        if (lane == 0) a.next[row] = -1;
-        return;
-    }
+// A row's next token from its spans' sums, by a wave.  A lane keeps the sums of KEPT spans, of 64 of them each; `mine`
+// has all of them.
+template <bool BF16, int KEPT>
+__device__ __forceinline__ void pick_next(const VerifyDrafts &a, int row, const Lines &l, int stands, int spans,
+                                          const double (&kept)[KEPT], const double *mine) {
+    const int lane = threadIdx.x & 63;
     Line<BF16> line = line_of<BF16>(a, l, stands);
     const float u32 = a.u[l.first + l.count - 1];
     const double u = u32 > 0.f ? (u32 < 1.f ? (double)u32 : 1.0) : 0.0;
@@ -228,7 +220,7 @@ __global__ __launch_bounds__(64) void verify_next_kernel(VerifyDrafts a, int spa
                 for (int i = 0; i < KEPT; ++i) x = i * 64 == s0 ? kept[i] : x;
                 return x;
             }
-            return s0 + lane < spans ? mine[s0 + lane] : 0.0;
+            return mine && s0 + lane < spans ? mine[s0 + lane] : 0.0;
         }
         double x = 0.0;
         for (int s = s0; s < min(s0 + 64, spans); ++s) {
@@ -286,6 +278,51 @@ __global__ __launch_bounds__(64) void verify_next_kernel(VerifyDrafts a, int spa
     if (lane == from) a.next[row] = span * SPAN + lane * EACH + (picked ? pick : last);
 }
 
+// The second launch: each row's next token.
+template <bool BF16>
+__global__ __launch_bounds__(64) void verify_next_kernel(VerifyDrafts a, int spans, const double *sums) {
+    const int row = blockIdx.x, lane = threadIdx.x;
+    const double *const mine = sums + (int64_t)row * spans;
+    constexpr int KEPT = 4;
+    double kept[KEPT];
+#pragma unroll
+    for (int i = 0; i < KEPT; ++i) kept[i] = i * 64 + lane < spans ? mine[i * 64 + lane] : 0.0;
+    const int stands = a.accepted[row];
+    const Lines l = lines_of(a, row);
+    if (l.count <= 0) {
+        if (lane == 0) a.next[row] = -1;
+        return;
+    }
+    pick_next<BF16>(a, row, l, stands, spans, kept, mine);
+}
+
+// Both in one launch, a workgroup a row, for few rows of few spans.
+constexpr int ROW_WAVES = 16, ROW_SPANS = 64;
+template <bool BF16>
+__global__ __launch_bounds__(64 * ROW_WAVES) void verify_row_kernel(VerifyDrafts a, int spans) {
+    __shared__ double s_sums[ROW_SPANS];
+    const int row = blockIdx.x, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const Lines l = lines_of(a, row);
+    if (l.count <= 0) {
+        if (threadIdx.x == 0) {
+            a.accepted[row] = 0;
+            a.next[row] = -1;
+        }
+        return;
+    }
+    const int stands = standing<BF16>(a, l);
+    if (threadIdx.x == 0) a.accepted[row] = stands;
+    const Line<BF16> line = line_of<BF16>(a, l, stands);
+    for (int s = wave; s < spans; s += ROW_WAVES) {
+        const double w = span_sum(line, s);
+        if (lane == 0) s_sums[s] = w;
+    }
+    __syncthreads();
+    if (wave) return;
+    const double kept[1] = {lane < spans ? s_sums[lane] : 0.0};
+    pick_next<BF16>(a, row, l, stands, spans, kept, nullptr);
+}
+
 static int spans_of(int vocab) { return (int)(((int64_t)vocab + SPAN - 1) / SPAN); }
 
 int64_t verify_drafts_workspace_bytes(int rows, int vocab) {
@@ -295,6 +332,14 @@ int64_t verify_drafts_workspace_bytes(int rows, int vocab) {
 
 hipError_t launch_verify_drafts(const VerifyDrafts &a, int cu_count, hipStream_t stream) {
     const int spans = spans_of(a.vocab);
+    // A workgroup a row spares a launch where a row is short and there is a CU for each: 1 row of 32000 12.2 -> 8.2 us a call,
+    // 256 of 32000 14.4 -> 12.4, 256 of 65536 23 -> 19; one row of more weights is too much for one CU.
+    if (spans <= ROW_SPANS && a.rows <= cu_count) {
+        const dim3 grid((unsigned)a.rows), threads(64 * ROW_WAVES);
+        if (a.bf16) hipLaunchKernelGGL(verify_row_kernel<true>, grid, threads, 0, stream, a, spans);
+        else hipLaunchKernelGGL(verify_row_kernel<false>, grid, threads, 0, stream, a, spans);
+        return hipGetLastError();
+    }
     // As many waves as run at once, 16 on a CU, each then with the same drafts to look at for several spans.
     const int64_t most = (int64_t)cu_count * 16;
     const int run = (int)std::min<int64_t>(spans, ((int64_t)a.rows * spans + most - 1) / most);

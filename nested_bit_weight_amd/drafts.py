@@ -46,6 +46,11 @@ def verify_workspace_bytes(rows: int, vocab: int) -> int:
 
 def _lines(t, name: str, dtype, shape, index: int):
     """Address of a [tokens][vocab] tensor with unit column stride and its stride from line to line."""
+    try:
+        if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
+            return t.data_ptr(), shape[1]
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:

@@ -264,3 +264,23 @@ def test_reserve_a_batch_that_starts_and_ends_at_once(nbw):  # noqa: F811
     assert got.slots.unique().numel() == rows * 20 and torch.equal(got.positions, torch.arange(20, device="cuda").repeat(rows).int())
     back = nbw.kv_reserve(cache, zero, zero, got.held, free, got.count, 0)
     assert int(back.count) == 2 * rows and torch.equal(free, before)
+
+
+@pytest.mark.parametrize("vocab", [33, 5000, 65536, 65537])
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+def test_verify_gives_a_row_the_same_in_any_batch(nbw, vocab, dtype):  # noqa: F811
+    """Few rows of few weights take one launch, others two."""
+    rows = 600 if vocab < 60000 else 5
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    target, draft = (torch.softmax(torch.randn(2 * rows, vocab, generator=g, device="cuda") * 2, dim=1).to(dtype) for _ in "pq")
+    ids = torch.randint(0, vocab, (2 * rows,), generator=g, device="cuda").int()
+    u = torch.rand(2 * rows, generator=g, device="cuda")
+    cu = torch.arange(0, 2 * rows + 1, 2, device="cuda").int()
+    accepted, after = nbw.verify_drafts(target, ids, u, draft=draft, cu=cu)
+    some = min(rows, 60)
+    for r in range(0, rows, max(1, rows // some)):
+        a, x = nbw.verify_drafts(target[2 * r:2 * r + 2], ids[2 * r:2 * r + 2], u[2 * r:2 * r + 2], draft=draft[2 * r:2 * r + 2], cu=cu[:2])
+        assert int(a) == int(accepted[r]) and int(x) == int(after[r])
+    n = min(rows, 40)
+    ref = odrafts.verify(f64(target[:2 * n]), ids[:2 * n].tolist(), f64(u[:2 * n]), cu[:n + 1].tolist(), f64(draft[:2 * n]))
+    assert accepted[:n].tolist() == ref[0] and after[:n].tolist() == ref[1]
