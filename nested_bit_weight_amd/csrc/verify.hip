@@ -8,7 +8,7 @@
 // A first launch sums spans of 1024 of them, a wave a span, or a few one after the other where
 // there are more than run at once; a second one, a wave a row, finds the span in which the sum passes
 // u times the whole, and then the place in it.  Nothing is shared between waves, so there is no barrier.
-// (A few short rows: a workgroup each, both in one launch.)
+// (A few short rows: a workgroup each, both in one launch, with a barrier between.)
 // Sums are in fp64 and in a fixed order: of 128 thousand weights they are off by about 1e-14, so that the
 // place is the exact one but for one draw in 1e9.
 //
