@@ -596,8 +596,9 @@ typedef struct nbw_kv_attend_shared_args {
  *     s_i = scale * q_g . k_i,  p = softmax over what the token sees,  out_g = sum_i p_i v_i
  * with query heads as in nbw_kv_attend.  The first prefix[g] slots of group g's
  * rows are read once for all of the group's tokens, through the table of the
- * group's first row: the other rows must hold the same there.  (A row shorter
- * than the prefix has as much of it as it is long.)
+ * group's first row that is as long as the prefix, or of the longest (the first
+ * such) if none is: the other rows must hold the same there.  A row shorter than
+ * the prefix, one that has ended among them, has as much of it as it is long.
  * Scores, softmax and sums are in fp32; the weights are rounded to bf16 for the
  * product with the values, and so divided by the sum of what they were rounded
  * to: an average of equal values is exact.  out is rounded once.  A token that

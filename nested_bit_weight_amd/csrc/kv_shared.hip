@@ -4,7 +4,7 @@
 // For a line, a query head of a new token, with the n slots that the token sees
 //     s_j = scale q.k_j,   o = sum_j 2^(s_j' - m) v_j / sum_j 2^(s_j' - m),
 // s' = s log2(e), with any m near the largest s'.  Slots are cut in segments: a group's
-// prefix, with all lines of the group, and each row's own slots behind it, with the row's
+// prefix (in the pages of its first row that has all of it), with all lines of the group, and each row's own slots behind it, with the row's
 // lines.  What a segment gives a line, (m, sum, o), is joined in a last launch.
 //
 // Three launches.  The first divides the work: blocks of lines of a head (32, or 128 where segments have more) times runs
@@ -213,20 +213,55 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
     __syncthreads();
     // A strip of segments for each thread; with no more segments than threads its one stays in registers.
     auto alone = [&](int g) { return a.group_rows[g + 1] - a.group_rows[g] == 1; };  // one row shares with no other
-    auto of = [&](int which, int s) {
+    // A group's lines and slots.  Its prefix is read through the table of its first row that is as long as the prefix, else of
+    // the longest one and as far as that has it.  (What a shorter row's table says there may be another row's.)  A thread looks at
+    // its group's first rows, as a rule at one; longer runs are looked at by the wave, which takes all of its lanes' groups.
+    auto group = [&](int s) {
+        Segment x = {0, 0, 0, 0, 0, 0, 0, 1};
+        int r = 0, r1 = 0, prefix = 0, len = 0, best = -1;
+        if (s < pl.side[0].segments && !alone(s)) {
+            x.row = r = bounded(a.group_rows[s], 0, c.rows);
+            r1 = bounded(a.group_rows[s + 1], 0, c.rows);
+            prefix = bounded(a.prefix[s], 0, a.max_len);
+            len = kv_len(a.lens, min(r, c.rows - 1), a.max_len);
+            x.token = first_token(a, r);
+            x.tokens = max(first_token(a, max(r, r1)) - x.token, 0);
+        }
+        auto look = [&](int at, int n) {
+            if (n > best) {
+                best = n;
+                x.row = at;
+            }
+        };
+        for (const int few = min(r + 4, r1); r < few && best < prefix;) {
+            look(r, len);
+            if (++r < few) len = kv_len(a.lens, r, a.max_len);
+        }
+        for (unsigned long long left = __ballot(r < r1 && best < prefix); left; left &= left - 1) {
+            const int src = __builtin_ctzll(left), end = __builtin_amdgcn_readlane(r1, src), enough = __builtin_amdgcn_readlane(prefix, src);
+            int at = __builtin_amdgcn_readlane(r, src), top = __builtin_amdgcn_readlane(best, src), top_row = -1;
+            for (; at < end && top < enough; at += 64) {
+                const int mine = at + (tid & 63), n = mine < end ? min(kv_len(a.lens, mine, a.max_len), enough) : -1, most = wave_max(n);
+                if (most > top) {
+                    top = most;
+                    top_row = at + __builtin_ctzll(__ballot(n == most));
+                }
+            }
+            if ((tid & 63) == src && top_row >= 0) look(top_row, top);
+        }
+        x.end = bounded(best, 0, prefix);
+        return x;
+    };
+    auto of = [&](int which, int s, Segment group) {
         Segment x = {s, 0, 0, 0, 0, 0, 0, 1};
-        if (which) {
+        if (!which) {
+            x = group;
+        } else {
             const int t0 = first_token(a, s), t1 = first_token(a, s + 1), g = groups.find(s);
             x.token = t0;
             x.tokens = max(t1 - t0, 0);
             x.start = g < 0 || alone(g) ? 0 : bounded(a.prefix[g], 0, a.max_len);
             x.end = kv_len(a.lens, s, a.max_len);
-        } else {
-            const int r0 = bounded(a.group_rows[s], 0, c.rows), r1 = bounded(a.group_rows[s + 1], 0, c.rows);
-            x.row = r0;
-            x.token = first_token(a, r0);
-            x.tokens = r0 < r1 && !alone(s) ? max(first_token(a, r1) - x.token, 0) : 0;
-            x.end = bounded(a.prefix[s], 0, a.max_len);
         }
         if (x.tokens == 0) x.end = x.start;
         x.end = max(x.end, x.start);
@@ -235,6 +270,17 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
     };
     int s0[2], s1[2];
     Segment mine[2];
+    {
+        const int n = pl.side[0].segments, strip = (n + PLAN_THREADS - 1) / PLAN_THREADS;
+        for (int i = 0; i < strip; ++i) {  // in all lanes
+            mine[0] = group(tid * strip + i);
+            if (strip > 1 && tid * strip + i < n) pl.side[0].segment[tid * strip + i] = mine[0];
+        }
+    }
+    auto kept = [&](int which, int s, bool one) {  // what group() gave
+        if (which || one) return mine[0];
+        return pl.side[0].segment[s];
+    };
     int own_units = 0;  // the most of a row's own slots
     uint32_t sums[5] = {0, 0, 0, 0, 0}, all[5];  // units and blocks of both sides, and tokens that see no prefix
 #pragma unroll
@@ -243,7 +289,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
         s0[which] = min(tid * strip, n);
         s1[which] = min(s0[which] + strip, n);
         for (int s = s0[which]; s < s1[which]; ++s) {
-            const Segment x = mine[which] = of(which, s);
+            const Segment x = mine[which] = of(which, s, kept(which, s, strip == 1));
             const uint32_t blocks = bounded((uint64_t)c.heads * x.blocks);
             sums[which] = plus(sums[which], bounded((uint64_t)blocks * units_of(x)));
             sums[2 + which] = plus(sums[2 + which], blocks);
@@ -293,7 +339,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
         }
         const bool one = s1[which] - s0[which] <= 1;
         for (int s = s0[which]; s < s1[which]; ++s) {
-            if (!one) mine[which] = of(which, s);
+            if (!one) mine[which] = of(which, s, kept(which, s, false));
             cut(which, mine[which]);
             next[which] = plus(next[which], places_of(mine[which]));
             next[2 + which] = plus(next[2 + which], cost_of(mine[which]));
@@ -308,7 +354,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void kv_shared_plan_kernel(KvCache c,
         const bool one = s1[which] - s0[which] <= 1;
         for (int s = s0[which]; s < s1[which]; ++s) {
             if (!one) {
-                mine[which] = of(which, s);
+                mine[which] = of(which, s, kept(which, s, false));
                 cut(which, mine[which]);
             }
             Segment x = mine[which];

@@ -440,8 +440,8 @@ def kv_attend_shared(cache: KVCache, q, lens, *, cu=None, groups=None, prefix=No
     cu[r]..cu[r+1]-1 for row r, of which each sees the ones up to itself.
 
     ``groups`` (int32 [n + 1], ascending from 0 to rows) and ``prefix`` (int32 [n]): the first
-    prefix[g] slots are the same for rows groups[g]..groups[g+1]-1, and are read once for all of
-    them, through the table of the first.  ``scale``, ``max_len`` and ``workspace`` as for
+    prefix[g] slots are the same for rows groups[g]..groups[g+1]-1 as far as each is long, and are read
+    once for all of them, through the table of the first that has them all.  ``scale``, ``max_len`` and ``workspace`` as for
     :func:`kv_attend` (``cache.attend_shared_workspace_bytes(...)``)."""
     index = cache._dev
     if _current_device() != index:
