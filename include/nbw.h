@@ -588,6 +588,9 @@ typedef struct nbw_kv_attend_shared_args {
     int64_t max_len;          /* as for nbw_kv_attend */
     void *workspace;          /* as for nbw_kv_attend; nbw_kv_attend_shared_workspace_bytes bytes */
     int64_t workspace_bytes;
+    int32_t all_bits;         /* 1: all weights keep their 24 bits; 0: they may be rounded to bf16 where
+                                 more than 32 lines share the slots */
+    int32_t reserved;         /* 0 */
 } nbw_kv_attend_shared_args;
 
 /* Attention of each row's new tokens over its cached slots.  Token j of the n of
@@ -599,9 +602,13 @@ typedef struct nbw_kv_attend_shared_args {
  * group's first row that is as long as the prefix, or of the longest (the first
  * such) if none is: the other rows must hold the same there.  A row shorter than
  * the prefix, one that has ended among them, has as much of it as it is long.
- * Scores, softmax and sums are in fp32; the weights are rounded to bf16 for the
- * product with the values, and so divided by the sum of what they were rounded
- * to: an average of equal values is exact.  out is rounded once.  A token that
+ * Scores, softmax and sums are in fp32, and so are the weights, as in
+ * nbw_kv_attend, with all_bits or where few lines (tokens times query heads of a
+ * head) share their slots: up to 32 on average of all groups, for prefixes, or of
+ * all rows, for their own slots.  Otherwise, unless all_bits is 1, they are rounded
+ * to bf16 for the product with the values, and divided by the sum of what they were
+ * rounded to: an average of equal values is exact.  (all_bits costs more where
+ * many lines share a long prefix: up to three times the time.)  out is rounded once.  A token that
  * sees no slot gives zeros, as does a head whose scores are all -infinity; else
  * a NaN among the scores or values that a token sees gives NaN, and so does an
  * infinite value whose weight is 0.  What a token does not see has no part in

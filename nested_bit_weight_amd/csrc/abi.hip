@@ -3,6 +3,7 @@
 // Host code only: argument validation, weight views, kernel choice by batch
 // size, and launches on the caller's stream.  Every check runs before any
 // HIP call, so a rejected call queues nothing.
+#include <algorithm>
 #include <climits>
 #include <mutex>
 #include <vector>
@@ -166,6 +167,12 @@ bool tokens_ok(int64_t tokens, int32_t q_heads) {
 }
 
 bool groups_ok(int64_t groups) { return groups >= 0 && groups <= (1 << 20); }
+
+// Scratch of nbw_kv_attend_shared, enough with all_bits and without; -1: more than a launch takes without.
+int64_t shared_bytes(const nbw::KvCache &c, int q_heads, int tokens, int groups, int max_len, int cus) {
+    const int64_t need = nbw::kv_attend_shared_workspace_bytes(c, q_heads, tokens, groups, max_len, false, cus);
+    return need < 0 ? -1 : std::max(need, nbw::kv_attend_shared_workspace_bytes(c, q_heads, tokens, groups, max_len, true, cus));
+}
 
 }  // namespace
 
@@ -618,7 +625,7 @@ int64_t nbw_kv_attend_shared_workspace_bytes(const nbw_kvcache *cache, int32_t q
         return -1;
     if (c.rows == 0 || tokens == 0) return 0;
     if (cu_count(&cus) != NBW_OK) return -1;
-    return nbw::kv_attend_shared_workspace_bytes(c, q_heads, (int)tokens, (int)groups, most, cus);
+    return shared_bytes(c, q_heads, (int)tokens, (int)groups, most, cus);
 }
 
 nbw_status nbw_kv_attend_shared(const nbw_kvcache *cache, const nbw_kv_attend_shared_args *args, void *stream) {
@@ -636,6 +643,7 @@ nbw_status nbw_kv_attend_shared(const nbw_kvcache *cache, const nbw_kv_attend_sh
     if (!(g.scale >= -3.4e38f && g.scale <= 3.4e38f)) return NBW_EINVAL;  // NaN too
     if (!tokens_ok(g.tokens, g.q_heads) || (!g.cu && g.tokens != c.rows)) return NBW_EINVAL;
     if (!groups_ok(g.groups) || (g.groups && (!g.group_rows || !g.prefix))) return NBW_EINVAL;
+    if (g.all_bits != 0 && g.all_bits != 1) return NBW_EINVAL;
     if (g.workspace_bytes < 0) return NBW_EINVAL;
     if (c.rows == 0 || g.tokens == 0) return NBW_OK;
     if (!g.q || !g.out || !g.lens) return NBW_EINVAL;
@@ -644,8 +652,10 @@ nbw_status nbw_kv_attend_shared(const nbw_kvcache *cache, const nbw_kv_attend_sh
         return NBW_EALIGN;
     int cus = 0;
     if ((st = cu_count(&cus)) != NBW_OK) return st;
-    const int64_t need = nbw::kv_attend_shared_workspace_bytes(c, g.q_heads, (int)g.tokens, (int)g.groups, a.max_len, cus);
-    if (need < 0) return NBW_EINVAL;  // more than a launch takes
+    a.all_bits = g.all_bits;
+    const int64_t need = shared_bytes(c, g.q_heads, (int)g.tokens, (int)g.groups, a.max_len, cus);
+    if (need < 0 || (a.all_bits && nbw::kv_attend_shared_workspace_bytes(c, g.q_heads, (int)g.tokens, (int)g.groups, a.max_len, true, cus) < 0))
+        return NBW_EINVAL;  // more than a launch takes
     if (need > 0 && (!g.workspace || g.workspace_bytes < need)) return NBW_ESCRATCH;
     a.q = (const uint16_t *)g.q;
     a.out = (uint16_t *)g.out;

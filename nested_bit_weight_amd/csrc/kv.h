@@ -81,6 +81,7 @@ struct KvAttendShared {
     const int32_t *cu, *lens, *group_rows, *prefix;
     int groups;
     int max_len;
+    int all_bits;  // of the weights
     uint8_t *ws;
 };
 
@@ -106,7 +107,8 @@ int64_t kv_evict_workspace_bytes(const KvCache &c, int budget, int max_len);
 hipError_t launch_kv_evict(const KvCache &c, const KvEvict &a, hipStream_t stream);
 
 hipError_t launch_kv_reserve(const KvCache &c, const KvReserve &a, int cu_count, hipStream_t stream);
-int64_t kv_attend_shared_workspace_bytes(const KvCache &c, int q_heads, int tokens, int groups, int max_len, int cu_count);
+int64_t kv_attend_shared_workspace_bytes(const KvCache &c, int q_heads, int tokens, int groups, int max_len, bool all_bits,
+                                         int cu_count);
 hipError_t launch_kv_attend_shared(const KvCache &c, const KvAttendShared &a, int cu_count, hipStream_t stream);
 int64_t verify_drafts_workspace_bytes(int rows, int vocab);
 hipError_t launch_verify_drafts(const VerifyDrafts &a, int cu_count, hipStream_t stream);

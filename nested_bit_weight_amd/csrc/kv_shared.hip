@@ -28,10 +28,12 @@
 //    transposing loads of four slots each, and o has its line in the lane too: rescaling it
 //    is a product with the lane's own number.
 //
-// The weights are rounded to bf16, half a step of 2^-8, for the second product; 24 bits, as
-// in the attention of one token, would take three times its matrix instructions, and the prefix
-// is bound by them.  The sum is taken over the rounded ones, so that an average of equal
-// values is exact and the error is that of the weights' differences.
+// The weights enter the second product with all their 24 bits, as three bf16 parts, where lines are few; as they are then bound
+// by bytes that costs little (16 rows of 4096 slots with 5 tokens 42.5 -> 43.5 us a call, 64 rows behind a prefix 49.3 -> 50.6).
+// Many lines are bound by that product, and there the weights are rounded to bf16, half a step of 2^-8, unless the caller asks
+// for all bits; the sum is then taken over the rounded ones, so that an average of equal values is exact and the error is that of
+// the weights' differences, about as much again as the result's own rounding.  (Two parts, 16 bits, in blocks of 128 lines: 96 rows with 5 tokens
+// behind a prefix of 32767 188 -> 253 us, 64 rows 49 -> 59; three: 320 and 66.)  With all bits asked for every block has 32 lines: 467 and 63.
 //
 // The running maximum m of a line is only raised, and o and the sum rescaled, when a score
 // passes it by more than 8 (a factor of 2^8).
@@ -613,7 +615,8 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
             for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
         float m = NEG_INF, sum = 0.f;
         f32x16_sh s[SUBS];
-        u32x4_kv p[SUBS][2];
+        constexpr int PARTS = FEW ? 3 : 1;  // of a weight
+        u32x4_kv p[SUBS][2][PARTS];
 
         // S^T of the tile whose keys are at kb; the keys AHEAD products on are under way.
         constexpr int AHEAD = 3;
@@ -675,13 +678,38 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
             }
             return m == NEG_INF ? 0.f : m;
         };
-        // Weights 8 b + i and the one after it, in s and rounded in p, and the sum of what they are rounded to in `part`.
+        // Weights 2 i and 2 i + 1 of run b, in s, their bf16 parts in p, and in `part` the sum of what these stand for.
         auto weigh = [&](int b, int i, float ref, float &part) {
             s[b][2 * i] = __builtin_amdgcn_exp2f(fmaf(s[b][2 * i], by, -ref));
             s[b][2 * i + 1] = __builtin_amdgcn_exp2f(fmaf(s[b][2 * i + 1], by, -ref));
-            const bf16x2_sh two = {(__bf16)s[b][2 * i], (__bf16)s[b][2 * i + 1]};
-            part = __builtin_amdgcn_fdot2_f32_bf16(two, bf16x2_sh{(__bf16)1.f, (__bf16)1.f}, part, false);
-            p[b][i / 4][i % 4] = __builtin_bit_cast(uint32_t, two);
+            auto &mine = p[b][i / 4];
+            if constexpr (PARTS == 1) {
+                const bf16x2_sh two = {(__bf16)s[b][2 * i], (__bf16)s[b][2 * i + 1]};
+                part = __builtin_amdgcn_fdot2_f32_bf16(two, bf16x2_sh{(__bf16)1.f, (__bf16)1.f}, part, false);
+                mine[0][i % 4] = __builtin_bit_cast(uint32_t, two);
+            } else {
+                // Each part but the last is cut off, not rounded, so that none is negative; and what is left is no less than
+                // the smallest normal number, or than the weight itself: the middle one of the three.  So no part is
+                // 0 unless the weight is, and an infinite value stays one.
+                constexpr float TINY = 0x1p-126f;
+                float w0 = s[b][2 * i], w1 = s[b][2 * i + 1];
+                part += w0 + w1;
+#pragma unroll
+                for (int x = 0; x + 1 < PARTS; ++x) {
+                    const uint32_t cut = __builtin_amdgcn_perm(__float_as_uint(w1), __float_as_uint(w0), 0x07060302u);
+                    mine[x][i % 4] = cut;
+                    w0 = __builtin_amdgcn_fmed3f(w0 - bf16_lo(cut), TINY, w0);
+                    w1 = __builtin_amdgcn_fmed3f(w1 - bf16_hi(cut), TINY, w1);
+                }
+                mine[PARTS - 1][i % 4] = bf16_pair(w0, w1);
+            }
+        };
+        // Adds 16 values, of some dims, times the weights of step k.
+        auto add_step = [&](f32x16_sh &to, const u32x4_kv &values, int k) {
+#pragma unroll
+            for (int x = 0; x < PARTS; ++x)
+                to = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_sh, values),
+                                                             __builtin_bit_cast(bf16x8_sh, p[k / 2][k % 2][x]), to, 0, 0, 0);
         };
         // O^T with the values at vb.  Step k is 16 slots: while its products run, the values three products on are under
         // way and the next step's weights are worked out.
@@ -706,8 +734,7 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
                 const int k = j / DB, d = j % DB;
                 if (j + AHEAD < PRODUCTS) ask(j + AHEAD);
                 in_order();
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_sh, vf[j % (AHEAD + 1)]),
-                                                               __builtin_bit_cast(bf16x8_sh, p[k / 2][k % 2]), o[d], 0, 0, 0);
+                add_step(o[d], vf[j % (AHEAD + 1)], k);
                 if (j + DB < PRODUCTS)
 #pragma unroll
                     for (int i = d * 4 / DB; i < (d + 1) * 4 / DB; ++i) weigh((k + 1) / 2, (k + 1) % 2 * 4 + i, ref, part);
@@ -759,8 +786,7 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
                         if ((vf[e] & 0x7F80u) == 0x7F80u) vf[e] &= 0xFFFF0000u;
                         if ((vf[e] & 0x7F800000u) == 0x7F800000u) vf[e] &= 0x0000FFFFu;
                     }
-                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_sh, vf),
-                                                                   __builtin_bit_cast(bf16x8_sh, p[k / 2][k % 2]), o[d], 0, 0, 0);
+                    add_step(o[d], vf, k);
                 }
             }
             sum += part;
@@ -1108,8 +1134,8 @@ __global__ __launch_bounds__(JOIN_THREADS, JOIN_WAVES / 4) void kv_shared_join_k
 }
 
 // The plan, its scratch laid out from `base`; returns the bytes (-1: more than a launch takes).
-static int64_t shared_plan(const KvCache &c, int q_heads, int tokens, int groups, int max_len, int cu_count, uint8_t *base,
-                           SharedPlan *pl) {
+static int64_t shared_plan(const KvCache &c, int q_heads, int tokens, int groups, int max_len, bool all_bits, int cu_count,
+                           uint8_t *base, SharedPlan *pl) {
     if ((((int64_t)c.pages * c.heads) << c.page_log2) * (c.dim / 8) >> 32) return -1;  // a pool's pieces are counted in 32 bits
     pl->group = q_heads / c.heads;
     const int64_t lines = (int64_t)tokens * pl->group, chunks = (max_len + UNIT - 1) / UNIT;
@@ -1118,7 +1144,7 @@ static int64_t shared_plan(const KvCache &c, int q_heads, int tokens, int groups
         auto &side = pl->side[which];
         side.segments = which ? c.rows : groups;
         const int64_t mean = side.segments ? (lines + side.segments - 1) / side.segments : 0;  // lines of a segment
-        side.lines = mean <= 32 ? 32 : 128;
+        side.lines = mean <= 32 || all_bits ? 32 : 128;
         if (side.segments) units += (lines / side.lines + side.segments) * c.heads * chunks;
         if (units > INT32_MAX / (1 + START)) return -1;
     }
@@ -1148,9 +1174,10 @@ static int64_t shared_plan(const KvCache &c, int q_heads, int tokens, int groups
     return at;
 }
 
-int64_t kv_attend_shared_workspace_bytes(const KvCache &c, int q_heads, int tokens, int groups, int max_len, int cu_count) {
+int64_t kv_attend_shared_workspace_bytes(const KvCache &c, int q_heads, int tokens, int groups, int max_len, bool all_bits,
+                                         int cu_count) {
     SharedPlan pl;
-    return shared_plan(c, q_heads, tokens, groups, max_len, cu_count, nullptr, &pl);
+    return shared_plan(c, q_heads, tokens, groups, max_len, all_bits, cu_count, nullptr, &pl);
 }
 
 template <int DIM>
@@ -1167,7 +1194,7 @@ static void launch_shared(const KvCache &c, const KvAttendShared &a, const Share
 
 hipError_t launch_kv_attend_shared(const KvCache &c, const KvAttendShared &a, int cu_count, hipStream_t stream) {
     SharedPlan pl;
-    shared_plan(c, a.q_heads, a.tokens, a.groups, a.max_len, cu_count, a.ws, &pl);
+    shared_plan(c, a.q_heads, a.tokens, a.groups, a.max_len, a.all_bits, cu_count, a.ws, &pl);
     const unsigned finders = (unsigned)((a.tokens + PLAN_THREADS - 1) / PLAN_THREADS);
     hipLaunchKernelGGL(kv_shared_plan_kernel, dim3(finders + 1), dim3(PLAN_THREADS), 0, stream, c, a, pl);
     switch (c.dim) {

@@ -64,7 +64,7 @@ class ReserveArgs(ctypes.Structure):
 class AttendSharedArgs(ctypes.Structure):
     _fields_ = [("q", _vp), ("out", _vp), ("q_ld", _i64), ("out_ld", _i64), ("tokens", _i64), ("q_heads", _i32),
                 ("scale", _f32), ("cu", _vp), ("lens", _vp), ("group_rows", _vp), ("prefix", _vp), ("groups", _i64),
-                ("max_len", _i64), ("workspace", _vp), ("workspace_bytes", _i64)]
+                ("max_len", _i64), ("workspace", _vp), ("workspace_bytes", _i64), ("all_bits", _i32), ("reserved", _i32)]
 
 
 SIZES_KEPT = 64
@@ -433,7 +433,7 @@ def kv_reserve(cache: KVCache, lens, want, held, free, count, max_tokens: int, *
 
 
 def kv_attend_shared(cache: KVCache, q, lens, *, cu=None, groups=None, prefix=None, scale: float | None = None, out=None,
-                     max_len: int | None = None, workspace="auto") -> torch.Tensor:
+                     max_len: int | None = None, workspace="auto", all_bits: bool = False) -> torch.Tensor:
     """Attention of each row's new tokens, ``q`` bf16 [tokens][q_heads][dim], over the row's first
     ``lens`` slots (int32 [rows], the new tokens' the last among them): bf16
     [tokens][q_heads][dim].  One token for each row, or with ``cu`` (int32 [rows + 1]) tokens
@@ -442,12 +442,16 @@ def kv_attend_shared(cache: KVCache, q, lens, *, cu=None, groups=None, prefix=No
     ``groups`` (int32 [n + 1], ascending from 0 to rows) and ``prefix`` (int32 [n]): the first
     prefix[g] slots are the same for rows groups[g]..groups[g+1]-1 as far as each is long, and are read
     once for all of them, through the table of the first that has them all.  ``scale``, ``max_len`` and ``workspace`` as for
-    :func:`kv_attend` (``cache.attend_shared_workspace_bytes(...)``)."""
+    :func:`kv_attend` (``cache.attend_shared_workspace_bytes(...)``).
+
+    Where more than 32 lines (tokens times query heads of a head) share slots, on average, the weights are
+    rounded to bf16 for the product with the values; with ``all_bits`` they keep their 24 bits
+    everywhere, as in :func:`kv_attend`, which takes longer where many tokens share a long prefix."""
     index = cache._dev
     if _current_device() != index:
         with torch.cuda.device(index):
             return kv_attend_shared(cache, q, lens, cu=cu, groups=groups, prefix=prefix, scale=scale, out=out, max_len=max_len,
-                                    workspace=workspace)
+                                    workspace=workspace, all_bits=all_bits)
     tokens = q.size(0) if isinstance(q, torch.Tensor) and q.dim() else 0
     if cu is None and tokens != cache.rows:
         raise ValueError(f"without cu there is one token for each of the {cache.rows} rows, got {tokens}")
@@ -477,7 +481,7 @@ def kv_attend_shared(cache: KVCache, q, lens, *, cu=None, groups=None, prefix=No
     ws, ws_bytes = cache._scratch(workspace, lib.nbw_kv_attend_shared_workspace_bytes, (q_heads, tokens, n, max_len), stream)
     args = AttendSharedArgs(qp, op, q_ld, out_ld, tokens, q_heads, scale,
                             None if cu is None else _is(cu, "cu", _INT32, (cache.rows + 1,), index),
-                            _is(lens, "lens", _INT32, cache._row, index), gp, pp, n, max_len, ws, ws_bytes)
+                            _is(lens, "lens", _INT32, cache._row, index), gp, pp, n, max_len, ws, ws_bytes, bool(all_bits), 0)
     st = lib.nbw_kv_attend_shared(cache._ref, ctypes.byref(args), stream)
     if st:
         _check(st, "nbw_kv_attend_shared")
