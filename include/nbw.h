@@ -611,7 +611,8 @@ typedef struct nbw_kv_attend_shared_args {
  * many lines share a long prefix: up to three times the time.)  out is rounded once.  A token that
  * sees no slot gives zeros, as does a head whose scores are all -infinity; else
  * a NaN among the scores or values that a token sees gives NaN, and so does an
- * infinite value whose weight is 0.  What a token does not see has no part in
+ * infinite value whose weight is 0.  (Of scores past 2^27, whose sums of n weights are
+ * not kept below 1, values past 2^127 / n may run over.)  What a token does not see has no part in
  * its result.  Tokens from cu[rows] on are left as they are.  Deterministic.
  * Workspaces are as for nbw_kv_attend: two calls that may run at the same time
  * have one each.  out does not overlap an input.

@@ -390,6 +390,10 @@ template <class... T>
 __device__ __forceinline__ void again(T &...x) {
     (..., ([](auto &y) { asm volatile("" : "+v"(y)); })(x));
 }
+__device__ __forceinline__ float rounded_product(float a, float b) {  // by itself, not as part of a sum
+#pragma clang fp contract(off)
+    return a * b;
+}
 template <int LOADS_LEFT>
 __device__ __forceinline__ void wait_loads() {  // all but the last so many have arrived; nothing is moved across
     __builtin_amdgcn_sched_barrier(0);
@@ -565,7 +569,8 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
         // (Not 0, which an infinite score would make a NaN of: what is smaller tells no two finite scores apart.)
         const float by = fmaxf(fabsf(a.scale) * 1.44269504088896340736f * (FP8 ? c.k_scale[head] : 1.f), 0x1p-126f);
         // Weights are up to 2^RAISE, and as many meet the values as the segment has slots: times a
-        // power of two, in their exponent, they sum to 1 at the most, and finite values cannot run over.
+        // power of two, in their exponent, they sum to 1 at the most, and finite values cannot run over (but for scores so large,
+        // past 2^27, that nothing can be taken off them).
         const int n = sg.end - sg.start;
         const float room = RAISE + (n > 1 ? 32 - __builtin_clz(n - 1) : 0);
 
@@ -644,8 +649,10 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
                                                                     __builtin_bit_cast(bf16x8_sh, qj), s[j / QF], 0, 0, 0);
             }
         };
-        // The running maximum, for the scores in s; gives what the weights are taken from.  `first` is the
-        // tile's first slot, `all` says that every line sees the whole tile.
+        // The running maximum, for the scores in s, which get their factor; gives what the weights are taken from.  `first` is the
+        // tile's first slot, `all` says that every line sees the whole tile.  (The factor's product is rounded before anything is taken
+        // from it, as the maximum is: of scores past 2^31 the two would differ by more than an exponential bears.  In one step, product
+        // and difference take 200 us in place of 205 of the document, 152 of 156 at 256 dims, and as long within 1% elsewhere.)
         auto raise = [&](int first, auto all, const uint32_t *there) {
             if constexpr (!decltype(all)::value) {
 #pragma unroll
@@ -663,8 +670,10 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
 #pragma unroll
             for (int b = 0; b < SUBS; ++b)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-            top *= by;  // by is positive: the largest stays the largest
+                for (int i = 0; i < 16; ++i) {
+                    s[b][i] = rounded_product(s[b][i], by);
+                    top = fmaxf(top, s[b][i]);
+                }
             if (__any(top + room > m + RAISE)) {
                 top = fmaxf(top, __shfl_xor(top, 32)) + room;
                 top = fmaxf(m, top);
@@ -678,10 +687,10 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
             }
             return m == NEG_INF ? 0.f : m;
         };
-        // Weights 2 i and 2 i + 1 of run b, in s, their bf16 parts in p, and in `part` the sum of what these stand for.
+        // Weights 2 i and 2 i + 1 of run b, in s in the scores' place, their bf16 parts in p, and in `part` the sum of what these stand for.
         auto weigh = [&](int b, int i, float ref, float &part) {
-            s[b][2 * i] = __builtin_amdgcn_exp2f(fmaf(s[b][2 * i], by, -ref));
-            s[b][2 * i + 1] = __builtin_amdgcn_exp2f(fmaf(s[b][2 * i + 1], by, -ref));
+            s[b][2 * i] = __builtin_amdgcn_exp2f(s[b][2 * i] - ref);
+            s[b][2 * i + 1] = __builtin_amdgcn_exp2f(s[b][2 * i + 1] - ref);
             auto &mine = p[b][i / 4];
             if constexpr (PARTS == 1) {
                 const bf16x2_sh two = {(__bf16)s[b][2 * i], (__bf16)s[b][2 * i + 1]};
