@@ -64,10 +64,10 @@ class Speculation:
         ints = lambda x: torch.full((rows,), x, dtype=I32, device="cuda")  # noqa: E731
         self.lens, self.held, self.shared, self.want = ints(prompt), ints(prompt // page), ints(prompt // page), ints(drafts + 1)
         self.last = torch.zeros(rows, dtype=I32, device="cuda")
+        self.runs = torch.arange(rows, dtype=I32, device="cuda") * (drafts + 1)
         self.groups = torch.tensor([0, rows], dtype=I32, device="cuda")
         self.prefix = torch.tensor([prompt], dtype=I32, device="cuda")
         self.accepted = torch.zeros((), dtype=torch.int64, device="cuda")
-        self.tokens = 0
 
     def layer(self, ids, r, lens, positions, cu, groups, prefix, cache=None):
         """Hidden states [tokens][hidden] after the layer's attention, by the r-bit child."""
@@ -95,27 +95,34 @@ class Speculation:
         self.last = nbw.verify_drafts(p, None, torch.rand(self.rows, generator=self.gen, device="cuda"))[1]
 
     def step(self):
-        """One step: drafts, their check, and what stands: (accepted, next), int32 [rows]."""
+        """One step: drafts, their check, and what stands: (accepted, next), int32 [rows].
+
+        A row that is granted no place, as the pages are used up or it has reached its capacity, stays as it is, with
+        nothing accepted and the next token it had."""
         rows, n = self.rows, self.drafts + 1
         got = nbw.kv_reserve(self.cache, self.lens, self.want, self.held, self.free, self.count, rows * n, shared=self.shared)
         u = torch.rand(rows, 2 * n, generator=self.gen, device="cuda")
         ids = torch.empty(rows, n, dtype=I32, device="cuda")
         draft = torch.empty(rows, n, self.vocab, device="cuda")  # the last line of a row is not read
+        # a row without places drafts past its capacity: nothing is stored, and what it drafts is not looked at
+        served = got.granted > 0
+        first = torch.where(served, self.lens, self.cache.capacity)
         ids[:, 0] = self.last
         for i in range(self.drafts):
-            lens = self.lens + i
+            lens = first + i
             h = self.layer(ids[:, i], self.r_draft, lens, lens, None, self.groups, self.prefix)
             draft[:, i] = self.probabilities(h, self.r_draft)
-            ids[:, i + 1] = nbw.verify_drafts(draft[:, i], None, u[:, n + i].contiguous())[1]
-        # the wide child's keys and values take the places of the drafts'
-        ids = ids.flatten()
+            ids[:, i + 1] = nbw.verify_drafts(draft[:, i], None, u[:, n + i].contiguous())[1].clamp_(min=0)
+        # Rows with places have n each, side by side in their order: the row of each run of places (any, behind the last).
+        # The wide child's keys and values take the places of the drafts'.
+        row = torch.searchsorted(got.cu[1:], self.runs, right=True).clamp_(max=rows - 1)
+        ids, draft = ids[row].flatten(), draft[row].flatten(0, 1)
         h = self.layer(ids, self.r, self.lens, got.positions, got.cu, self.groups, self.prefix)
-        accepted, self.last = nbw.verify_drafts(self.probabilities(h, self.r), ids, u[:, :n].contiguous().flatten(),
-                                                draft=draft.view(rows * n, -1), cu=got.cu)
-        self.lens = self.lens + accepted + 1
+        accepted, after = nbw.verify_drafts(self.probabilities(h, self.r), ids, u[row, :n].flatten(), draft=draft, cu=got.cu)
+        self.lens = torch.where(served, self.lens + accepted + 1, self.lens)
+        self.last = torch.where(served, after, self.last)
         self.held, self.count = got.held, got.count
         self.accepted += accepted.sum()
-        self.tokens += rows * n
         return accepted, self.last
 
 

@@ -563,7 +563,9 @@ typedef struct nbw_kv_reserve_args {
  * -1.  Table entries are written only where a page is taken, free only above
  * count and below count_out: the call can be repeated on the same inputs, and
  * a reservation that is given back leaves stack and pages as they were.
- * cu, positions and the cache are what nbw_kv_append takes.
+ * cu, positions and the cache are what nbw_kv_append takes.  Tokens of granted rows
+ * lie side by side, with no room for those of others: token t is of the row r with
+ * cu[r] <= t < cu[r + 1].
  * held is bounded by 0 and the width, count by 0 and free_size.  Exact: whole
  * numbers only.  Other overlaps of inputs and outputs are not allowed.
  * Errors: NBW_EINVAL, NBW_EALIGN, NBW_EUNSUPPORTED, NBW_EHIP. */

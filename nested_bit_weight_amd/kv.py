@@ -400,7 +400,9 @@ def kv_reserve(cache: KVCache, lens, want, held, free, count, max_tokens: int, *
     (int32 [rows]); one that holds fewer takes them.  Rows are served in order while pages, and
     ``max_tokens`` places for tokens, last; the others are granted 0.  A token's position counts
     from ``seen`` (int32 [rows], ``lens`` if None); its slot is page * page size + place, or -1.
-    ``positions`` (int32) and ``slots`` (int64) have 0 and -1 from token cu[rows] on.  The call
+    ``positions`` (int32) and ``slots`` (int64) have 0 and -1 from token cu[rows] on.  Tokens are packed: the row of
+    token t is ``torch.searchsorted(cu[1:], t, right=True)``, and what the caller has by row goes to the calls that take
+    ``cu`` in that order (``examples/speculative_decode.py`` does so).  The call
     can be repeated on the same inputs; ``held_out`` and ``count_out`` are tensors of their own."""
     index = cache._dev
     if _current_device() != index:
