@@ -441,9 +441,9 @@ struct Shape {
 
 // 16 bytes of each lane to LDS, side by side from `lds` on, which is the same for all of them.  Written out, as the
 // compiler puts a wait for all such loads before each transposing read, whatever that reads; what
-// has to have arrived is said by wait_loads.  No register is written but m0, which nothing else here uses.
+// has to have arrived is said by wait_loads.
 __device__ __forceinline__ void load_to_lds(const uint8_t *p, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory", "m0");
 }
 
 struct SharedLds {
