@@ -931,10 +931,11 @@ __device__ __forceinline__ void attend_share(const KvCache &c, const KvAttendSha
             const int sl = block * X::LINES + ln;
             const int64_t t = sg.token + sl / pl.group, qh = head * pl.group + sl % pl.group;
             if (sole) {
-                const float inv = total == 0.f ? 0.f : v_by / total;
+                x *= total == 0.f ? 0.f : 1.f / total;
                 if (total == 0.f) x = f32x4_sh{0.f, 0.f, 0.f, 0.f};  // nothing to attend to, whatever the values are
+                if (FP8) x *= v_by;  // by itself: a large factor over the small sum could run over
                 *reinterpret_cast<u32x2_kv *>(a.out + t * a.out_ld + qh * DIM + d) =
-                    u32x2_kv{bf16_pair(x[0] * inv, x[1] * inv), bf16_pair(x[2] * inv, x[3] * inv)};
+                    u32x2_kv{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
             } else {
                 const int64_t at = part0 + ln;
                 *reinterpret_cast<f32x4_sh *>(side.o + at * DIM + d) = x;

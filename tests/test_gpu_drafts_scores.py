@@ -110,3 +110,17 @@ def test_scores_that_rise_from_slot_to_slot(nbw, step):  # noqa: F811
             sees = s.lens[row] - s.cu[row + 1] + 1 + t
             want = value(s, row, sees - 1)
             assert torch.allclose(out[t], want, rtol=2.0 ** -8, atol=2.0 ** -30), (row, t)
+
+
+@pytest.mark.parametrize("by", [1e-36, 1e-20, 1e20, 1e31, 1e34, 7e35])
+@pytest.mark.parametrize("groups", [[(0, [(5, 1), (40, 2)])], [(0, [(900, 40)])], [(300, [(60, 2), (50, 30)])], [(0, [(9000, 1)])]])
+def test_factors_of_values_of_any_size(nbw, by, groups):  # noqa: F811
+    """Equal values of 256: their average is 256 times the factor, whatever the weights add up to."""
+    s = Shared(nbw, groups, 8, 2, 128, 16, FP8, seed=1)
+    s.scales[1].fill_(by)
+    s.v.copy_(torch.where(s.v.float().isnan(), math.nan, 256.0).to(FP8))
+    want = torch.tensor(by, dtype=torch.float32) * 256
+    for bits in (False, True):
+        out = s.call(all_bits=bits).float().cpu()
+        # the division, the factor's product and the sums (2^-24 each for up to 9000 slots), and the result's own rounding
+        assert bool(((out - want).abs() <= want * (2.0**-8 + 2.0**-10)).all()), (bits, out.flatten()[:3], want)
