@@ -617,7 +617,9 @@ typedef struct nbw_kv_attend_shared_args {
  * not kept below 1, values past 2^127 / n may run over.)  What a token does not see has no part in
  * its result.  Tokens from cu[rows] on are left as they are.  Deterministic.
  * Workspaces are as for nbw_kv_attend: two calls that may run at the same time
- * have one each.  out does not overlap an input.
+ * have one each.  out does not overlap an input.  There are no running totals of the
+ * weights (nbw_kv_attend's acc): rows that nbw_kv_evict shortens by them take
+ * their tokens through nbw_kv_attend.
  * Refused (NBW_EINVAL) is what its 32-bit numbers do not reach: a pool of
  * 2^35 elements or more (64 GiB of bf16), and batches of more than some 7e8
  * runs of 128 slots with 32 lines each, rows and groups counted at max_len.
@@ -625,7 +627,10 @@ typedef struct nbw_kv_attend_shared_args {
 nbw_status nbw_kv_attend_shared(const nbw_kvcache *cache, const nbw_kv_attend_shared_args *args, void *stream);
 
 /* Bytes of workspace nbw_kv_attend_shared needs, or -1 on bad arguments.  Host
- * only; queries the device's compute-unit count. */
+ * only; queries the device's compute-unit count.  For prefixes (with groups) and
+ * for own slots each: 4 * (dim + 2) bytes for each token and query head, whether its
+ * parts are joined or written at once, and for up to 2 * 128 lines of each workgroup (68 MB with
+ * 128 dims and 256 CUs): 409 MB for 8192 tokens of 32 heads of 128 with groups. */
 int64_t nbw_kv_attend_shared_workspace_bytes(const nbw_kvcache *cache, int32_t q_heads, int64_t tokens,
                                              int64_t groups, int64_t max_len);
 

@@ -38,10 +38,10 @@
 // The running maximum m of a line is only raised, and o and the sum rescaled, when a score
 // passes it by more than 8 (a factor of 2^8).
 //
-// Measured (32 query heads over 8 of 128 dims, bf16; the second launch, then all three): 64 rows behind a prefix of
-// 8192, 600 slots of their own each, 122 MB: 37 and 53 us; 16 rows of 4096 slots with 5 tokens, 148 MB: 32 us (4.6 TB/s)
-// and 44; 96 rows with 5 tokens behind a prefix of 32767, 140 GFLOP with what the mask covers: 189 us (740 TFLOP/s; matrix
-// units busy 37% of the time, VALU at least 30) and 204.  Loads through registers and barriers, prefixes and
+// Measured (32 query heads over 8 of 128 dims, bf16; the second launch as a trace's median, then a call's three): 64 rows behind a
+// prefix of 8192, 600 slots of their own each, 122 MB: 39 (3.1 TB/s) and 50 us; 16 rows of 4096 slots with 5 tokens, 148 MB: 34
+// us (4.3 TB/s) and 44; 96 rows with up to 5 tokens, 232 in all, behind a prefix of 32767, 125.5 GFLOP: 220 us (least 194; matrix units
+// busy 38% of the time, VALU 35) and 205 without the trace, 610 TFLOP/s.  Loads through registers and barriers, prefixes and
 // own slots in launches of their own: 148 us, 87 and 295 in all.
 #include <algorithm>
 #include <type_traits>
@@ -99,9 +99,10 @@ struct SharedPlan {
 // start and the result at its end (few lines: 7 us beside 3 for a unit; many: 8 beside 5).
 constexpr int START = 2;
 // Units that a share which ends within a piece costs beyond that, for what it writes and the join reads; and units that the
-// join takes for each line that whole pieces would spare it (0.23 ns each, beside units of 5 and 3 us).  13 rows of 500 new tokens
-// of 50 query heads, in all: divided 179 us, whole 110.  Where pieces are long, whole ones lose, as in the prefixes too: the
-// second launch of 64 rows behind one of 8192 slots 37 us divided, 52 with whole pieces of both sides.
+// join takes for each line that whole pieces would spare it (0.23 ns each, beside units of 5 and 3 us).  Calls divided and with
+// whole pieces of own slots: 13 rows of up to 496 new tokens, 50 query heads over 10, 149 and 94 us (whole is taken); 61 rows of up to 27 49 and 40
+// (whole); 64 rows behind a prefix of 8192 50 and 56, 16 rows of 4096 slots with 5 tokens 44 and 64 (divided).  34 rows of up to 395 new tokens behind
+// 2000 slots of their own are divided, as their pieces would be longer than a share: 355 us, where whole ones take 288.
 constexpr float CUT = 2.f;
 constexpr float JOINED_MANY = 1.f / 22000, JOINED_FEW = 1.f / 13000;
 __device__ __forceinline__ uint32_t head_cost(const Segment &s) {
@@ -1153,6 +1154,12 @@ static int64_t shared_plan(const KvCache &c, int q_heads, int tokens, int groups
     for (int which = 0; which < 2; ++which) {
         auto &side = pl->side[which];
         side.segments = which ? c.rows : groups;
+        // Few lines cost least where a block has them all, and half again as much with one line more; many, in blocks of 128, cost about
+        // the same up to 128.  Calls with blocks of 32 and 128 lines: 16 rows of 8192 slots, 32 lines each 116 and 123 us (8 bits 70 and
+        // 103), 36 lines 171 and 124 (106 and 103), 128 lines 339 and 143; 16 rows of 4096 of 256 dims, 32 lines 121 and 136, 36 lines 173 and 136; a
+        // prefix of 16384, 32 lines 43 and 42, 64 lines 44 and 46, 256 lines 76 and 69.  The mean decides, as the lines of each segment are on the
+        // device: 63 single tokens over 4096 slots beside a prompt's 512 over 2048 (mean 36) 240 and 246, 15 over 8192 beside
+        // 2048 over 4096 (516) 510 and 267, 500 over 2048 beside 300 (6) 737 and 865.
         const int64_t mean = side.segments ? (lines + side.segments - 1) / side.segments : 0;  // lines of a segment
         side.lines = mean <= 32 || all_bits ? 32 : 128;
         if (side.segments) units += (lines / side.lines + side.segments) * c.heads * chunks;

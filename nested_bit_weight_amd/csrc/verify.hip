@@ -332,8 +332,10 @@ int64_t verify_drafts_workspace_bytes(int rows, int vocab) {
 
 hipError_t launch_verify_drafts(const VerifyDrafts &a, int cu_count, hipStream_t stream) {
     const int spans = spans_of(a.vocab);
-    // A workgroup a row spares a launch where a row is short and there is a CU for each: 1 row of 32000 12.2 -> 8.2 us a call,
-    // 256 of 32000 14.4 -> 12.4, 256 of 65536 23 -> 19; one row of more weights is too much for one CU.
+    // A workgroup a row spares a launch where a row is short and there is a CU for each.  Calls in one launch and in two (fp32, drafts
+    // sampled): 1 row of 32000 8.8 and 11.6 us, of 65536 8.8 and 11.6, of 100000 9.5 and 11.6, of 128256 11.5 and 11.5, of 151936
+    // 14.3 and 11.6, 64 of 100000 14.5 and 11.7, of 128256 18.0 and 14.8; 256 of 32000 11.5 and 14.2, of 65536 17.4 and 20.8; in bf16 256 of 65536 9.6 and
+    // 12.5, 257 15.7 and 13.3.
     if (spans <= ROW_SPANS && a.rows <= cu_count) {
         const dim3 grid((unsigned)a.rows), threads(64 * ROW_WAVES);
         if (a.bf16) hipLaunchKernelGGL(verify_row_kernel<true>, grid, threads, 0, stream, a, spans);
