@@ -9,14 +9,14 @@ import numpy as np
 
 def wanted(dims, dim, sees):
     """dims [slots]: each slot's dim, or -1 -> what a token that sees the first `sees` slots gets."""
-    d = np.asarray(dims)[:sees]
+    d = np.asarray(dims)[:max(sees, 0)]
     return np.bincount(d[d >= 0], minlength=dim) / max(sees, 1)
 
 
 def wrong(got, want, sees):
     """Dims that are off by more than the result's rounding to bf16 (2^-8) and the sums of up to `sees` equal numbers in
     fp32, for numerator and denominator (2^-24 each time)."""
-    return np.flatnonzero(~(np.abs(np.asarray(got) - want) <= (2.0**-8 + 2 * sees * 2.0**-24) * want))
+    return np.flatnonzero(~(np.abs(np.asarray(got) - want) <= (2.0**-8 + 2 * max(sees, 0) * 2.0**-24) * want))
 
 
 def runs(slots, length, dim, first=0):
